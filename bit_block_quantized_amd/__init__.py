@@ -69,8 +69,32 @@ class MoeLayerC(ctypes.Structure):
                 ("expert_data", ctypes.c_void_p)]
 
 
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class KVBatchC(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("q_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
+class QkRopeC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("inv_freq", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("n_heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+# Element types of queries, cache and attention output.
+F32, F16, BF16 = 0, 1, 2
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
@@ -105,6 +129,9 @@ _SIGS = {
     "rfx_moe_forward_status": ([_P, _I, _I, _P, _SZ, _P], _I),
     "rfx_moe_debug_hidden": ([_P, _I, _I, _P, _SZ, _P, _P, _P, _P], _I),
     "rfx_moe_debug_prefill": ([_P, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _P, _P, _P, _P, _P], _I),
+    "rfx_qk_norm_rope": ([_P, _P, _P, _P, _P], _I),
+    "rfx_attn_workspace_bytes": ([_P, _P, _I], _SZ),
+    "rfx_attn": ([_P, _P, _P, _I, _F, _I, _I, _P, _I, _P, _SZ, _P], _I),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -375,6 +402,156 @@ def moe_debug_prefill(layer, q, k, xq, xs, topk_w, pairs_sorted, expert_off, ws,
                                        _dptr(expert_off), _dptr(ws), ws.numel() * ws.element_size(), probe_expert,
                                        probe_first, _dptr(h), _dptr(dots_gate), _dptr(dots_up), _dptr(dots_down),
                                        _stream(stream)))
+
+
+# ------------------------------------------------------------ attention
+
+def _elem(dtype):
+    """RFX_F32 / RFX_F16 / RFX_BF16 of a torch dtype."""
+    name = str(dtype)
+    if name not in _ELEM:
+        raise ValueError(f"element type {dtype}: float32, float16 or bfloat16")
+    return _ELEM[name]
+
+
+_ELEM = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
+
+
+def _want(t, name, dtype, shape, device=None):
+    """A contiguous device tensor of this dtype and shape (None entries of
+    the shape: any size)."""
+    if str(t.dtype) != dtype:
+        raise ValueError(f"{name}: {t.dtype}, {dtype} wanted")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} wanted")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
+    return t.data_ptr()
+
+
+def _call_on(device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current; the stream
+    defaults to that device's current one."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors on {device}: the kernels need GPU memory")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _check(fn(*args, _stream(stream)))
+    return _check(fn(*args, _stream(stream)))
+
+
+class DeviceKVCache:
+    """The paged cache of one layer: k and v [n_pages][n_kv_heads][page_size]
+    [head_dim], float16 or bfloat16 (kept alive here)."""
+
+    def __init__(self, k, v):
+        n_pages, n_kv_heads, page_size, head_dim = k.shape
+        if str(k.dtype) == "torch.float32":
+            raise ValueError("the cache is float16 or bfloat16")
+        self.k, self.v = k, v
+        self.dtype, self.device = k.dtype, k.device
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, n_kv_heads, page_size, head_dim
+        self._dtype = str(k.dtype)
+        self.c = KVCacheC(_elem(k.dtype), n_kv_heads, head_dim, page_size, n_pages, 0,
+                          _want(k, "k", self._dtype, tuple(k.shape)),
+                          _want(v, "v", self._dtype, tuple(k.shape), k.device))
+
+    @classmethod
+    def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
+        import torch
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        dtype = torch.bfloat16 if dtype is None else dtype
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+class KVBatch:
+    """A batch of sequences with new tokens (rfx_kv_batch): int32 device
+    tensors q_off [n_seq + 1], kv_len [n_seq] (new tokens included) and
+    page_table [n_seq][pages]; n_tokens rows in the token arrays, at most
+    max_q new tokens per sequence."""
+
+    def __init__(self, q_off, kv_len, page_table, n_tokens, max_q):
+        n_seq, stride = page_table.shape
+        self.q_off, self.kv_len, self.page_table = q_off, kv_len, page_table
+        self.n_seq, self.n_tokens, self.max_q = n_seq, n_tokens, max_q
+        dev = page_table.device
+        self.device = dev
+        self.c = KVBatchC(n_seq, n_tokens, max_q, stride, _want(q_off, "q_off", "torch.int32", (n_seq + 1,), dev),
+                          _want(kv_len, "kv_len", "torch.int32", (n_seq,), dev),
+                          _want(page_table, "page_table", "torch.int32", (n_seq, stride)))
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def rope_inv_freq(rot_dim, base=10000.0):
+    """Angles per position of the rot_dim / 2 rotated pairs, float64:
+    base^(-2 i / rot_dim)."""
+    return np.float64(base) ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
+
+
+def _head_rows(t, name, n_tokens, heads, dim, device):
+    """Pointer and row stride of fp32 [n_tokens][heads][dim]; rows may be
+    part of longer ones (a fused projection's output)."""
+    if str(t.dtype) != "torch.float32" or tuple(t.shape) != (n_tokens, heads, dim):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, float32 {(n_tokens, heads, dim)} wanted")
+    st = t.stride()
+    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
+        raise ValueError(f"{name}: heads of a row are not contiguous (strides {st})")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
+    return t.data_ptr(), st[0] if n_tokens > 1 else heads * dim
+
+
+def qk_norm_rope(q, k, v, cache: DeviceKVCache, batch: KVBatch, q_out, inv_freq, q_weight=None, k_weight=None,
+                 eps=1e-6, interleaved=False, stream=None):
+    """Norm and rotation of the new tokens' queries (into q_out) and keys,
+    keys and values appended to the cache. q, k, v: float32 [n_tokens][heads]
+    [head_dim], rows may be strided; inv_freq: float64 device tensor
+    [rot_dim / 2] (see rope_inv_freq); weights float32 [head_dim] or None."""
+    T, D, dev = batch.n_tokens, cache.head_dim, cache.device
+    Hq = q.shape[1]
+    qp, qs = _head_rows(q, "q", T, Hq, D, dev)
+    kp, ks = _head_rows(k, "k", T, cache.n_kv_heads, D, dev)
+    vp, vs = _head_rows(v, "v", T, cache.n_kv_heads, D, dev)
+    if batch.device != dev:
+        raise ValueError(f"batch on {batch.device}, the cache is on {dev}")
+    args = QkRopeC(qp, kp, vp, qs, ks, vs, _want(inv_freq, "inv_freq", "torch.float64", (None,), dev),
+                   None if q_weight is None else _want(q_weight, "q_weight", "torch.float32", (D,), dev),
+                   None if k_weight is None else _want(k_weight, "k_weight", "torch.float32", (D,), dev),
+                   eps, Hq, 2 * inv_freq.shape[0], int(interleaved))
+    _call_on(dev, stream, lib().rfx_qk_norm_rope, ctypes.byref(args), cache.ref(), batch.ref(),
+             _want(q_out, "q_out", cache._dtype, (T, Hq, D), dev))
+
+
+def attn_workspace_bytes(cache: DeviceKVCache, batch: KVBatch, n_heads: int) -> int:
+    return int(lib().rfx_attn_workspace_bytes(cache.ref(), batch.ref(), n_heads))
+
+
+def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0, ws=None, stream=None):
+    """Attention of the batch's new tokens over the paged cache: q
+    [n_tokens][n_heads][head_dim] in the cache's type, out the same shape in
+    that type or float32; window > 0: only the last `window` keys and the
+    first `sinks`."""
+    T, D, dev = batch.n_tokens, cache.head_dim, cache.device
+    Hq = q.shape[1]
+    qp = _want(q, "q", cache._dtype, (T, Hq, D), dev)
+    op = _want(out, "out", str(out.dtype), (T, Hq, D), dev)
+    if batch.device != dev:
+        raise ValueError(f"batch on {batch.device}, the cache is on {dev}")
+    wp, wn = None, 0
+    if ws is not None:
+        if ws.device != dev:
+            raise ValueError(f"ws: on {ws.device}, the cache is on {dev}")
+        wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call_on(dev, stream, lib().rfx_attn, qp, cache.ref(), batch.ref(), Hq, scale, window, sinks, op, _elem(out.dtype),
+             wp, wn)
 
 
 from .layer import DeviceMoeLayer, MoeBuffers, PlacedMoeLayer, hot_experts_by_frequency  # noqa: E402,F401

@@ -1,0 +1,467 @@
+// Attention of few new tokens per sequence over the paged cache (decode and
+// speculative verification): o = softmax(scale q k^T + mask) v for the up to
+// 32 query rows (tokens x query heads of a group) that share a kv head.
+//
+// Bound by the cache's bytes: every visible key and value is read once, for
+// all rows of its kv head. A wave takes tiles of 32 keys; its keys and
+// values of the next tile are in flight while it computes the current one.
+//   S^T = K Q^T on v_mfma_f32_16x16x32: A = 16 keys straight from memory, B =
+//   the rows' queries (registers, loaded once). A lane ends with scores of one
+//   row. The keys' order inside a tile is chosen so that they are 8 (l / 16)
+//   .. + 7, which is the B operand's order of
+//   O^T = V^T P^T: the weights go from S to the next product without leaving
+//   their lane. V^T comes from LDS (each wave its own 32 x D piece, no
+//   barrier) by transposed reads.
+// Each wave keeps a running maximum and sum per row (fp32); waves are joined
+// through LDS, and where few rows have long sequences the keys are split
+// over S workgroups whose partials the last to arrive joins in split order
+// (results do not depend on the arrival order).
+#include "rfx_kv.h"
+
+using namespace rfx;
+using namespace rfx::dev;
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int BN = 32;                  // keys per wave and tile
+constexpr int kWaitVmcnt0 = 0x0F70;     // s_waitcnt vmcnt(0)
+
+// LDS bytes: each wave's V piece, reused for the waves' join
+// ([wave][16 rows][DP + 4] floats).
+template <int DP>
+constexpr int lds_bytes()
+{
+    constexpr int v = kWaves * BN * (DP * 2 + 32), o = kWaves * 16 * (DP + 4) * 4;
+    return v > o ? v : o;
+}
+
+// Key (of a tile's 32) that sits in row r of the wave's V piece: the four
+// rows that a group of 16 lanes reads at once are neighbours, so that with a
+// pitch of 2 D + 32 bytes the groups' rows fall on different banks.
+__device__ __forceinline__ int row_key(int r) { return (r & 3) + 8 * ((r >> 2) & 3) + 4 * (r >> 4); }
+
+template <class T, int DP, int NR, bool BIG>
+__global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
+{
+    constexpr int NC = DP / 32;         // K steps of the score product
+    constexpr int NV = DP / 16;         // 16-byte loads per lane and V tile; also 16-row tiles of O^T
+    constexpr int CH = DP / 8;          // 16-byte chunks per key
+    constexpr int RPI = 64 / CH;        // keys per V load instruction
+    constexpr int VP = DP * 2 + 32;     // pitch of the V piece
+    constexpr int TERMS = T::TERMS;
+    __shared__ __align__(16) char smem[lds_bytes<DP>()];
+    __shared__ float s_m[kWaves][NR * 16], s_l[kWaves][NR * 16];
+    __shared__ int s_last;
+
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const KvArgs &kv = a.kv;
+    int b = blockIdx.x;
+    const int split = b % a.S;
+    b /= a.S;
+    const int rb = b % a.row_blocks;
+    b /= a.row_blocks;
+    const int hk = b % kv.Hk, seq = b / kv.Hk;
+    const int unit = blockIdx.x / a.S;
+    const int D = kv.D;
+
+    const Seq sq = load_seq(kv, seq);
+    const int nrows = sq.nq * kv.G;
+    const int row0 = rb * (NR * 16);
+    if (row0 >= nrows)
+        return;
+    const int row_end = min(nrows, row0 + NR * 16);
+    const int p_lo = sq.p0 + row0 / kv.G, p_hi = sq.p0 + (row_end - 1) / kv.G;
+    const KeyTiles kt = key_tiles<BN>(p_lo, p_hi, sq.kv, a.window, a.sinks);
+    const int per = max(a.min_tiles, (kt.n + a.S - 1) / a.S);
+    const int active = max(1, (kt.n + per - 1) / per);
+    if (split >= active)
+        return;
+    const int t_begin = split * per + wave, t_end = min(kt.n, (split + 1) * per);
+
+    // this lane's row of each row tile: its query as the B operand (lane l:
+    // row l % 16, elements 32 c + 8 (l / 16) .. + 7) and its position
+    u4 qf[NR][NC];
+    int pos[NR];
+    bool row_ok[NR];
+#pragma unroll
+    for (int n = 0; n < NR; n++) {
+        const int row = row0 + 16 * n + r16;
+        row_ok[n] = row < nrows;
+        const int rr = min(row, nrows - 1), tok = rr / kv.G, head = hk * kv.G + rr % kv.G;
+        pos[n] = sq.p0 + tok;
+        const uint16_t *qp = a.q + ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            const int d = 32 * c + 8 * g4;
+            const u4 x = *reinterpret_cast<const u4 *>(qp + (d < D ? d : 0));
+            qf[n][c] = d < D ? x : (u4){0, 0, 0, 0};
+        }
+    }
+
+    f32x4 acc[NR][NV];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int n = 0; n < NR; n++) {
+        m[n] = -INFINITY;
+        l[n] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            acc[n][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int32_t *table = kv.table + (size_t)seq * kv.stride;
+    const int last_key = max(0, kt.hi - 1);
+    const int ps = kv.page_shift, pm = (1 << ps) - 1;
+    const size_t head_stride = (size_t)D << ps;             // elements of one head of a page
+    const int ka = 8 * (r16 >> 2) + (r16 & 3);              // the lane's keys of a tile: ka and ka + 4
+    const int vrow = lane / CH, vch = 8 * (lane % CH) < D ? 8 * (lane % CH) : 0;
+    char *vbuf = smem + wave * (BN * VP);
+
+    // Page ids. Pages of 32 keys or more: one id per tile; lane i holds the
+    // id of the wave's i-th next tile, refilled every 64 tiles. Smaller
+    // pages: lane i holds the id of key i % 32 of one tile.
+    const auto ids_big = [&](int t) {
+        const int key = min(tile_key<BN>(kt, min(t + kWaves * lane, max(kt.n - 1, 0))), last_key);
+        return table[key >> ps];
+    };
+    const auto ids_small = [&](int t) {
+        const int key = min(tile_key<BN>(kt, t) + (lane & 31), last_key);
+        return table[key >> ps];
+    };
+    const auto usable = [&](int id) { return (unsigned)id < (unsigned)kv.n_pages; };
+
+    u4 kf[2][NC], vf[NV];
+    // The loads of tile t; addresses are always inside the cache.
+    const auto load_k = [&](int key0, int ids) {
+        if constexpr (BIG) {
+            const uint16_t *p = kv.k + ((size_t)(usable(ids) ? ids : 0) * kv.Hk + hk) * head_stride;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const uint16_t *kp = p + (size_t)((key0 + ka + 4 * j) & pm) * D;
+#pragma unroll
+                for (int c = 0; c < NC; c++) {
+                    const int d = 32 * c + 8 * g4;
+                    kf[j][c] = *reinterpret_cast<const u4 *>(kp + (d < D ? d : 0));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int id = __shfl(ids, ka + 4 * j, 64);
+                const uint16_t *kp = kv.k + ((size_t)(usable(id) ? id : 0) * kv.Hk + hk) * head_stride +
+                                     (size_t)((key0 + ka + 4 * j) & pm) * D;
+#pragma unroll
+                for (int c = 0; c < NC; c++) {
+                    const int d = 32 * c + 8 * g4;
+                    kf[j][c] = *reinterpret_cast<const u4 *>(kp + (d < D ? d : 0));
+                }
+            }
+        }
+    };
+    const auto load_v = [&](int key0, int ids) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int key = row_key(i * RPI + vrow);
+            const int id = BIG ? ids : __shfl(ids, key, 64);
+            const uint16_t *p = kv.v + ((size_t)(usable(id) ? id : 0) * kv.Hk + hk) * head_stride +
+                                (size_t)((key0 + key) & pm) * D;
+            vf[i] = *reinterpret_cast<const u4 *>(p + vch);
+        }
+    };
+
+    int ids = 0, ids_at = 0;   // BIG: ids of tiles ids_at, ids_at + 4, ...
+    int cur = 0, nxt = 0;      // ids of the tile in the registers, and of the next
+    if (t_begin < t_end) {
+        if constexpr (BIG) {
+            ids = ids_big(t_begin);
+            ids_at = t_begin;
+            cur = __builtin_amdgcn_readlane(ids, 0);
+        } else {
+            cur = ids_small(t_begin);
+            nxt = ids_small(min(t_begin + kWaves, t_end - 1));
+        }
+        load_k(tile_key<BN>(kt, t_begin), cur);
+        load_v(tile_key<BN>(kt, t_begin), cur);
+    }
+    for (int t = t_begin; t < t_end; t += kWaves) {
+        const int key0 = tile_key<BN>(kt, t);
+        const int tn = t + kWaves < t_end ? t + kWaves : t; // the next tile, or this one again
+        const int key_n = tile_key<BN>(kt, tn);
+        const int cur_ids = cur;
+        if constexpr (BIG) {
+            if ((tn - ids_at) / kWaves >= 64) {
+                ids = ids_big(tn);
+                ids_at = tn;
+            }
+            nxt = __builtin_amdgcn_readlane(ids, (tn - ids_at) / kWaves);
+        }
+
+        // scores: register v of s[n][j] is key key0 + 8 (l / 16) + 4 j + v
+        f32x4 s[NR][2];
+        if (D != DP) { // elements past D in the last K step
+#pragma unroll
+            for (int c = 0; c < NC; c++)
+                if (32 * c + 8 * g4 >= D)
+                    kf[0][c] = kf[1][c] = (u4){0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int n = 0; n < NR; n++)
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                s[n][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+#pragma unroll
+            for (int n = 0; n < NR; n++)
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    s[n][j] = T::mma16(kf[j][c], qf[n][c], s[n][j]);
+        load_k(key_n, nxt);
+
+        // a tile that some row sees only in part, or whose page ids are not
+        // all good (in the small-page case every tile is checked for that)
+        const bool page_bad = BIG ? !usable(cur_ids) : __ballot(!usable(cur_ids)) != 0;
+        const bool edge = key0 + BN - 1 > p_lo || key0 + BN > kt.hi ||
+                          (a.window && key0 <= p_hi - a.window && key0 + BN > a.sinks) || page_bad;
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int v = 0; v < 4; v++) {
+                    const int key = key0 + 8 * g4 + 4 * j + v;
+                    const bool good = usable(BIG ? cur_ids : __shfl(cur_ids, 8 * g4 + 4 * j + v, 64)) && key < kt.hi;
+#pragma unroll
+                    for (int n = 0; n < NR; n++) {
+                        const bool seen = good && key <= pos[n] && (!a.window || key > pos[n] - a.window || key < a.sinks);
+                        s[n][j][v] = seen ? s[n][j][v] : -INFINITY;
+                    }
+                }
+            // values of keys that no row sees may be anything: zero
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const int kk = row_key(i * RPI + vrow), key = key0 + kk;
+                const bool any = usable(BIG ? cur_ids : __shfl(cur_ids, kk, 64)) && key < kt.hi &&
+                                 (key >= kt.lo || key < kt.sk);
+                if (!any)
+                    vf[i] = (u4){0, 0, 0, 0};
+            }
+        }
+
+        u4 pt[NR][TERMS];
+#pragma unroll
+        for (int n = 0; n < NR; n++) {
+            float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
+                              fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float mn = fmaxf(m[n], top);
+            if (__any(mn > m[n])) {
+                // nothing seen yet: the sums are zero, and so is the factor
+                const float f = m[n] == -INFINITY ? 0.f : fast_exp2(a.c * (m[n] - mn));
+                l[n] *= f;
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+                    acc[n][i] *= f;
+                m[n] = mn;
+            }
+            const float off = mn == -INFINITY ? 0.f : T::BIAS - a.c * mn;
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                p[i] = fast_exp2(fmaf(a.c, s[n][i >> 2][i & 3], off));
+                l[n] += p[i];
+            }
+            split_terms<T, TERMS>(p, pt[n]);
+        }
+
+        // V through the wave's LDS piece: its previous reads are done (in
+        // order within a wave), then this tile's rows, then the transposed
+        // reads
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            *reinterpret_cast<u4 *>(vbuf + (i * RPI + vrow) * VP + 16 * (lane % CH)) = vf[i];
+        load_v(key_n, nxt);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const char *vr = vbuf + (4 * g4 + (r16 >> 2)) * VP + 8 * (r16 & 3);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const u2 lo = lds_read_tr(vr + 32 * i), hi = lds_read_tr(vr + 16 * VP + 32 * i);
+            const u4 vt = {lo.x, lo.y, hi.x, hi.y}; // element 16 i + l % 16 of keys 8 (l / 16) .. + 7
+#pragma unroll
+            for (int n = 0; n < NR; n++)
+#pragma unroll
+                for (int k = 0; k < TERMS; k++)
+                    acc[n][i] = T::mma16(vt, pt[n][k], acc[n][i]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        cur = nxt;
+        if constexpr (!BIG)
+            nxt = ids_small(min(t + 2 * kWaves, t_end - 1));
+    }
+
+    // the waves' sums joined in wave order
+#pragma unroll
+    for (int n = 0; n < NR; n++) {
+        l[n] += __shfl_xor(l[n], 16, 64);
+        l[n] += __shfl_xor(l[n], 32, 64);
+        if (g4 == 0) {
+            s_m[wave][16 * n + r16] = m[n];
+            s_l[wave][16 * n + r16] = l[n];
+        }
+    }
+    float *part = a.part + ((size_t)unit * a.S + split) * (NR * 16) * (DP + 2);
+    const bool joined = active == 1;
+    float *o_lds = reinterpret_cast<float *>(smem);
+    constexpr int OP = DP + 4;
+#pragma unroll
+    for (int n = 0; n < NR; n++) {
+        __syncthreads();
+        float top = s_m[0][16 * n + r16];
+#pragma unroll
+        for (int w = 1; w < kWaves; w++)
+            top = fmaxf(top, s_m[w][16 * n + r16]);
+        const float f = m[n] == -INFINITY ? 0.f : fast_exp2(a.c * (m[n] - top));
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            *reinterpret_cast<f32x4 *>(o_lds + (wave * 16 + r16) * OP + 16 * i + 4 * g4) = acc[n][i] * f;
+        __syncthreads();
+        // 16 threads per row, four elements each at a time
+        const int r = threadIdx.x >> 4, row = row0 + 16 * n + r;
+        float rm = s_m[0][16 * n + r], rl = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWaves; w++)
+            rm = fmaxf(rm, s_m[w][16 * n + r]);
+#pragma unroll
+        for (int w = 0; w < kWaves; w++)
+            rl += s_m[w][16 * n + r] == -INFINITY ? 0.f : s_l[w][16 * n + r] * fast_exp2(a.c * (s_m[w][16 * n + r] - rm));
+        if (row >= nrows)
+            continue;
+        const float inv = rl > 0.f ? 1.0f / rl : 0.f; // a row that sees nothing is zero
+        const size_t at = ((size_t)(sq.t0 + row / kv.G) * kv.Hq + hk * kv.G + row % kv.G) * D;
+        for (int d = 4 * (threadIdx.x & 15); d < D; d += 64) {
+            f32x4 o = *reinterpret_cast<const f32x4 *>(o_lds + r * OP + d);
+#pragma unroll
+            for (int w = 1; w < kWaves; w++)
+                o += *reinterpret_cast<const f32x4 *>(o_lds + (w * 16 + r) * OP + d);
+            if (joined) {
+                o *= inv;
+                if (a.out_f32)
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at + d) = o;
+                else
+                    *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at + d) = (u2){T::pack(o[0], o[1]), T::pack(o[2], o[3])};
+            } else {
+                // agent-scope stores: the joining workgroup may run on another XCD
+                unsigned long long *pp = reinterpret_cast<unsigned long long *>(part + (size_t)(16 * n + r) * DP + d);
+                __hip_atomic_store(pp, __builtin_bit_cast(unsigned long long, (f2){o[0], o[1]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(pp + 1, __builtin_bit_cast(unsigned long long, (f2){o[2], o[3]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        if (!joined && (threadIdx.x & 15) == 0)
+            __hip_atomic_store(reinterpret_cast<unsigned long long *>(part + (size_t)NR * 16 * DP) + 16 * n + r,
+                               __builtin_bit_cast(unsigned long long, (f2){rm, rl}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (joined)
+        return;
+
+    // the last of the unit's splits to arrive joins them
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned n = __hip_atomic_fetch_add(a.cnt + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = n == (unsigned)active - 1;
+        if (s_last)
+            __hip_atomic_store(a.cnt + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!s_last)
+        return;
+    const size_t pstride = (size_t)NR * 16 * (DP + 2);
+    const float *parts = a.part + (size_t)unit * a.S * pstride;
+    for (int r = threadIdx.x >> 4; row0 + r < row_end; r += 16) {
+        const int row = row0 + r;
+        const size_t at = ((size_t)(sq.t0 + row / kv.G) * kv.Hq + hk * kv.G + row % kv.G) * D;
+        const auto stat = [&](int s) {
+            return __builtin_bit_cast(f2, __hip_atomic_load(reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)NR * 16 * DP) + r,
+                                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        };
+        // 16 lanes share a row: lane j reads the statistics of splits j, j + 16, ...
+        const int j = threadIdx.x & 15;
+        float rm = -INFINITY;
+        for (int s = j; s < active; s += 16)
+            rm = fmaxf(rm, stat(s).x);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            rm = fmaxf(rm, __shfl_xor(rm, o, 16));
+        float rl = 0.f;
+        f32x4 o[DP / 64];
+#pragma unroll
+        for (int i = 0; i < DP / 64; i++)
+            o[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < active; s++) { // split order
+            const f2 st = stat(s);
+            const float f = st.x == -INFINITY ? 0.f : fast_exp2(a.c * (st.x - rm));
+            rl += st.y * f;
+#pragma unroll
+            for (int i = 0; i < DP / 64; i++) {
+                const int d = 4 * j + 64 * i;
+                if (d < D) {
+                    const unsigned long long *pp = reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)r * DP + d);
+                    const f2 x = __builtin_bit_cast(f2, __hip_atomic_load(pp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+                    const f2 y = __builtin_bit_cast(f2, __hip_atomic_load(pp + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+                    o[i][0] += x.x * f;
+                    o[i][1] += x.y * f;
+                    o[i][2] += y.x * f;
+                    o[i][3] += y.y * f;
+                }
+            }
+        }
+        const float inv = rl > 0.f ? 1.0f / rl : 0.f;
+#pragma unroll
+        for (int i = 0; i < DP / 64; i++) {
+            const int d = 4 * j + 64 * i;
+            if (d < D) {
+                const f32x4 y = o[i] * inv;
+                if (a.out_f32)
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at + d) = y;
+                else
+                    *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at + d) = (u2){T::pack(y[0], y[1]), T::pack(y[2], y[3])};
+            }
+        }
+    }
+}
+
+template <class T, int DP, int NR>
+int launch(const AttnArgs &a, hipStream_t st)
+{
+    const unsigned grid = (unsigned)a.kv.n_seq * a.kv.Hk * a.row_blocks * a.S;
+    if (a.kv.page_shift >= 5)
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, true>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, false>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    return hip_status("attn decode launch");
+}
+
+template <class T>
+int launch_dim(const AttnArgs &a, int row_tiles, hipStream_t st)
+{
+    const int D = a.kv.D;
+    if (row_tiles == 1)
+        return D <= 64 ? launch<T, 64, 1>(a, st) : D <= 128 ? launch<T, 128, 1>(a, st) : launch<T, 256, 1>(a, st);
+    return D <= 64 ? launch<T, 64, 2>(a, st) : launch<T, 128, 2>(a, st);
+}
+
+} // namespace
+
+namespace rfx {
+
+int attn_decode_launch(const AttnArgs &a, int type, int row_tiles, hipStream_t st)
+{
+    return type == RFX_BF16 ? launch_dim<BF16>(a, row_tiles, st) : launch_dim<F16>(a, row_tiles, st);
+}
+
+} // namespace rfx

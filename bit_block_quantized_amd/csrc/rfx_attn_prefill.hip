@@ -1,0 +1,378 @@
+// Attention of prompts and chunks over the paged cache: o = softmax(scale q
+// k^T + mask) v with a causal mask, an optional sliding window and a few
+// first tokens that stay visible (sinks).
+//
+// Bound by the matrix core and by the exponentials beside it. The query
+// heads that share a kv head are packed into the rows (row = token * G +
+// head of the group), so that a key tile serves all of them and short chunks
+// still fill the row tiles. A workgroup of four waves takes 128 rows; key
+// tiles of BN keys go through two LDS buffers, the next one's loads in
+// flight in registers during the current one's products.
+//   S^T = K Q^T on v_mfma_f32_32x32x16: A = 32 keys (LDS), B = the wave's 32
+//   rows (registers). A lane holds half of one row's scores, so a row's
+//   maximum takes one exchange between lane halves and its sum none.
+//   O^T = V^T P^T: S^T's register order is P^T's operand order once the keys
+//   of V^T are read in that order (transposed LDS reads), so the weights stay
+//   in their lane.
+// Tiles outside a wave's rows' window or after their positions are skipped.
+// Few row blocks over long sequences: the keys are split over S workgroups,
+// and the last to arrive joins the partials in split order.
+//
+// Rounding: weights are rounded once to the cache's type for a result of
+// that type (its own rounding is as large); for an fp32 result they are
+// carried as the sum of TERMS values. The row sums are of the fp32 weights.
+#include "rfx_kv.h"
+
+using namespace rfx;
+using namespace rfx::dev;
+
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kWaitVmcnt0 = 0x0F70; // s_waitcnt vmcnt(0)
+
+// Pitches (bytes) of the LDS rows: K rows are read 16 bytes per lane down a
+// column, so neighbours are 16 bytes apart modulo the 256 bytes of the
+// banks; four V rows are read 64 bytes at a time, so theirs are 64 apart.
+template <int DP>
+struct Tile {
+    static constexpr int BN = DP <= 128 ? 64 : 32;
+    static constexpr int KP = DP * 2 + 16, VP = DP * 2 + 64;
+    static constexpr int buf = BN * (KP + VP);
+    static constexpr int CH = DP / 8;           // 16-byte chunks per key
+    static constexpr int KPI = kThreads / CH;   // keys per load of the workgroup
+    static constexpr int NL = BN / KPI;         // loads per thread, K and V each
+};
+
+template <class T, int DP, int TERMS>
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kernel(AttnArgs a)
+{
+    using L = Tile<DP>;
+    constexpr int BN = L::BN, NC = DP / 16, ND = DP / 32, NK = BN / 32;
+    __shared__ __align__(16) char smem[2 * L::buf];
+    __shared__ unsigned s_bad[3][2]; // keys of a tile with an unusable page id
+    __shared__ int s_last;
+
+    const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, hl = lane >> 5, i16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const KvArgs &kv = a.kv;
+    // kv heads vary fastest: workgroups go round the XCDs in order, so with
+    // eight kv heads each XCD's L2 holds one head's keys and values
+    int b = blockIdx.x;
+    const int hk = b % kv.Hk;
+    b /= kv.Hk;
+    const int split = b % a.S;
+    b /= a.S;
+    const int rb = a.row_blocks - 1 - b % a.row_blocks; // the longest first
+    const int seq = b / a.row_blocks;
+    const int unit = (seq * a.row_blocks + rb) * kv.Hk + hk;
+    const int D = kv.D;
+
+    const Seq sq = load_seq(kv, seq);
+    const int nrows = sq.nq * kv.G, row0 = rb * kRows;
+    if (row0 >= nrows)
+        return;
+    const int row_end = min(nrows, row0 + kRows);
+    const KeyTiles kt = key_tiles<BN>(sq.p0 + row0 / kv.G, sq.p0 + (row_end - 1) / kv.G, sq.kv, a.window, a.sinks);
+    const int per = max(a.min_tiles, (kt.n + a.S - 1) / a.S);
+    const int active = max(1, (kt.n + per - 1) / per);
+    if (split >= active)
+        return;
+    const int t_begin = split * per, t_end = min(kt.n, t_begin + per);
+
+    // the wave's rows
+    const int wrow = row0 + 32 * wave;
+    const bool wave_on = wrow < nrows;
+    const int row = min(wrow + r32, nrows - 1), tok = row / kv.G, head = hk * kv.G + row % kv.G;
+    const bool row_ok = wrow + r32 < nrows;
+    const int pos = sq.p0 + tok;
+    const int w_lo = sq.p0 + min(wrow, nrows - 1) / kv.G, w_hi = sq.p0 + min(wrow + 31, nrows - 1) / kv.G;
+    const size_t at = ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
+    u4 qf[NC];
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+        const int d = 16 * c + 8 * hl;
+        const u4 x = *reinterpret_cast<const u4 *>(a.q + at + (d < D ? d : 0));
+        qf[c] = d < D ? x : (u4){0, 0, 0, 0};
+    }
+
+    f32x16 acc[ND];
+#pragma unroll
+    for (int i = 0; i < ND; i++)
+#pragma unroll
+        for (int v = 0; v < 16; v++)
+            acc[i][v] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    // staging: this thread's chunk of NL keys of a tile
+    const int32_t *table = kv.table + (size_t)seq * kv.stride;
+    const int last_key = max(0, kt.hi - 1), ps = kv.page_shift, pm = (1 << ps) - 1;
+    const int skey = tid / L::CH, sch = tid % L::CH;
+    const bool ch_ok = 8 * sch < D;
+    const size_t head_stride = (size_t)D << ps;
+    u4 kx[L::NL], vx[L::NL];
+    int ids[L::NL], ids_n[L::NL];
+    const auto load_ids = [&](int t, int (&id)[L::NL]) {
+        const int key0 = tile_key<BN>(kt, min(t, t_end - 1));
+#pragma unroll
+        for (int i = 0; i < L::NL; i++)
+            id[i] = table[min(key0 + i * L::KPI + skey, last_key) >> ps];
+    };
+    const auto load_tile = [&](int t, const int (&id)[L::NL]) {
+        const int key0 = tile_key<BN>(kt, t);
+#pragma unroll
+        for (int i = 0; i < L::NL; i++) {
+            const int key = key0 + i * L::KPI + skey;
+            const int pid = (unsigned)id[i] < (unsigned)kv.n_pages ? id[i] : 0;
+            const size_t off = ((size_t)pid * kv.Hk + hk) * head_stride + (size_t)(key & pm) * D + (ch_ok ? 8 * sch : 0);
+            kx[i] = *reinterpret_cast<const u4 *>(kv.k + off);
+            vx[i] = *reinterpret_cast<const u4 *>(kv.v + off);
+        }
+    };
+    // tile t (its loads and ids in the registers) into buffer bf; keys that
+    // no row of the workgroup sees, and elements past D, become zero: their
+    // memory may hold anything
+    const auto store_tile = [&](int t, const int (&id)[L::NL], int bf) {
+        const int key0 = tile_key<BN>(kt, t);
+        char *kb = smem + bf * L::buf, *vb = kb + BN * L::KP;
+#pragma unroll
+        for (int i = 0; i < L::NL; i++) {
+            const int kk = i * L::KPI + skey, key = key0 + kk;
+            const bool good = (unsigned)id[i] < (unsigned)kv.n_pages;
+            const bool any = good && ch_ok && key < kt.hi && (key >= kt.lo || key < kt.sk);
+            if (!good && sch == 0)
+                atomicOr(&s_bad[t % 3][kk >> 5], 1u << (kk & 31));
+            const u4 z = {0, 0, 0, 0};
+            *reinterpret_cast<u4 *>(kb + kk * L::KP + 16 * sch) = any ? kx[i] : z;
+            *reinterpret_cast<u4 *>(vb + kk * L::VP + 16 * sch) = any ? vx[i] : z;
+        }
+    };
+
+    if (tid < 6)
+        s_bad[tid >> 1][tid & 1] = 0;
+    __syncthreads();
+    if (t_begin < t_end) {
+        load_ids(t_begin, ids);
+        load_tile(t_begin, ids);
+        load_ids(t_begin + 1, ids_n);
+        store_tile(t_begin, ids, t_begin & 1);
+    }
+    __syncthreads();
+
+    for (int t = t_begin; t < t_end; t++) {
+        const bool more = t + 1 < t_end;
+        if (more) {
+#pragma unroll
+            for (int i = 0; i < L::NL; i++)
+                ids[i] = ids_n[i];
+            load_tile(t + 1, ids);
+            load_ids(t + 2, ids_n);
+        }
+        if (tid < 2)
+            s_bad[(t + 2) % 3][tid] = 0; // last read for tile t - 1
+        const int key0 = tile_key<BN>(kt, t);
+        const char *kb = smem + (t & 1) * L::buf, *vb = kb + BN * L::KP;
+        const bool seen = wave_on && key0 <= w_hi && (!a.window || key0 + BN - 1 > w_lo - a.window || key0 < a.sinks);
+        if (seen) {
+            f32x16 s[NK];
+#pragma unroll
+            for (int k = 0; k < NK; k++)
+#pragma unroll
+                for (int v = 0; v < 16; v++)
+                    s[k][v] = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC; c++)
+#pragma unroll
+                for (int k = 0; k < NK; k++) {
+                    const u4 kf = *reinterpret_cast<const u4 *>(kb + (32 * k + r32) * L::KP + 32 * c + 16 * hl);
+                    s[k] = T::mma32(kf, qf[c], s[k]);
+                }
+            const unsigned bad0 = s_bad[t % 3][0], bad1 = s_bad[t % 3][1];
+            const bool edge = key0 + BN - 1 > w_lo || (a.window && key0 <= w_hi - a.window && key0 + BN > a.sinks) || (bad0 | bad1);
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < NK; k++)
+#pragma unroll
+                    for (int v = 0; v < 16; v++) {
+                        const int kk = 8 * (v >> 2) + 4 * hl + (v & 3), key = key0 + 32 * k + kk;
+                        const bool ok = key <= pos && (!a.window || key > pos - a.window || key < a.sinks) &&
+                                        !(((k ? bad1 : bad0) >> kk) & 1);
+                        s[k][v] = ok ? s[k][v] : -INFINITY;
+                    }
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int k = 0; k < NK; k++)
+#pragma unroll
+                for (int v = 0; v < 16; v++)
+                    top = fmaxf(top, s[k][v]);
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float mn = fmaxf(m, top);
+            if (__any(mn > m)) {
+                const float f = m == -INFINITY ? 0.f : fast_exp2(a.c * (m - mn));
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < ND; i++)
+                    acc[i] *= f;
+                m = mn;
+            }
+            const float off = mn == -INFINITY ? 0.f : T::BIAS - a.c * mn;
+#pragma unroll
+            for (int k = 0; k < NK; k++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    float p[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        p[i] = fast_exp2(fmaf(a.c, s[k][8 * h + i], off));
+                        l += p[i];
+                    }
+                    u4 pt[TERMS];
+                    split_terms<T, TERMS>(p, pt);
+                    // values of keys 32 k + 16 h + 4 hl + 0..3 and + 8..11
+                    const char *vr = vb + (32 * k + 16 * h + 4 * hl + (i16 >> 2)) * L::VP + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
+#pragma unroll
+                    for (int i = 0; i < ND; i++) {
+                        const u2 x = lds_read_tr(vr + 64 * i), y = lds_read_tr(vr + 8 * L::VP + 64 * i);
+                        const u4 vt = {x.x, x.y, y.x, y.y};
+#pragma unroll
+                        for (int n = 0; n < TERMS; n++)
+                            acc[i] = T::mma32(vt, pt[n], acc[i]);
+                    }
+                }
+        }
+        if (more)
+            store_tile(t + 1, ids, (t + 1) & 1);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    // lane (row r32), register 4 j + v of acc[i]: element 32 i + 8 j + 4 hl + v
+    if (active == 1) {
+        if (!row_ok)
+            return;
+        const float inv = l > 0.f ? 1.0f / l : 0.f; // a row that sees nothing is zero
+#pragma unroll
+        for (int i = 0; i < ND; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int d = 32 * i + 8 * j + 4 * hl;
+                if (d >= D)
+                    continue;
+                const f32x4 o = {acc[i][4 * j] * inv, acc[i][4 * j + 1] * inv, acc[i][4 * j + 2] * inv, acc[i][4 * j + 3] * inv};
+                if (a.out_f32)
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at + d) = o;
+                else
+                    *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at + d) = (u2){T::pack(o[0], o[1]), T::pack(o[2], o[3])};
+            }
+        return;
+    }
+
+    // partials by agent-scope stores (the joining workgroup may run on
+    // another XCD), then the arrival count
+    constexpr size_t pstride = (size_t)kRows * (DP + 2);
+    float *part = a.part + ((size_t)unit * a.S + split) * pstride;
+    const int lr = 32 * wave + r32;
+    if (row_ok) {
+#pragma unroll
+        for (int i = 0; i < ND; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                unsigned long long *pp = reinterpret_cast<unsigned long long *>(part + (size_t)lr * DP + 32 * i + 8 * j + 4 * hl);
+                __hip_atomic_store(pp, __builtin_bit_cast(unsigned long long, (f2){acc[i][4 * j], acc[i][4 * j + 1]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(pp + 1, __builtin_bit_cast(unsigned long long, (f2){acc[i][4 * j + 2], acc[i][4 * j + 3]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        if (hl == 0)
+            __hip_atomic_store(reinterpret_cast<unsigned long long *>(part + (size_t)kRows * DP) + lr,
+                               __builtin_bit_cast(unsigned long long, (f2){m, l}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    if (tid == 0) {
+        const unsigned n = __hip_atomic_fetch_add(a.cnt + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = n == (unsigned)active - 1;
+        if (s_last)
+            __hip_atomic_store(a.cnt + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!s_last)
+        return;
+    const float *parts = a.part + (size_t)unit * a.S * pstride;
+    const int j16 = tid & 15;
+    for (int r = tid >> 4; row0 + r < row_end; r += kThreads / 16) {
+        const auto stat = [&](int s) {
+            return __builtin_bit_cast(f2, __hip_atomic_load(reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)kRows * DP) + r,
+                                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        };
+        float rm = -INFINITY, rl = 0.f;
+        for (int s = j16; s < active; s += 16)
+            rm = fmaxf(rm, stat(s).x);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            rm = fmaxf(rm, __shfl_xor(rm, o, 16));
+        f32x4 o[DP / 64];
+#pragma unroll
+        for (int i = 0; i < DP / 64; i++)
+            o[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int s = 0; s < active; s++) { // split order
+            const f2 st = stat(s);
+            const float f = st.x == -INFINITY ? 0.f : fast_exp2(a.c * (st.x - rm));
+            rl += st.y * f;
+#pragma unroll
+            for (int i = 0; i < DP / 64; i++) {
+                const unsigned long long *pp = reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)r * DP + 4 * j16 + 64 * i);
+                const f2 x = __builtin_bit_cast(f2, __hip_atomic_load(pp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+                const f2 y = __builtin_bit_cast(f2, __hip_atomic_load(pp + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+                o[i][0] += x.x * f;
+                o[i][1] += x.y * f;
+                o[i][2] += y.x * f;
+                o[i][3] += y.y * f;
+            }
+        }
+        const float inv = rl > 0.f ? 1.0f / rl : 0.f;
+        const int jr = row0 + r;
+        const size_t to = ((size_t)(sq.t0 + jr / kv.G) * kv.Hq + hk * kv.G + jr % kv.G) * D;
+#pragma unroll
+        for (int i = 0; i < DP / 64; i++) {
+            const int d = 4 * j16 + 64 * i;
+            if (d >= D)
+                continue;
+            const f32x4 y = o[i] * inv;
+            if (a.out_f32)
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to + d) = y;
+            else
+                *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + to + d) = (u2){T::pack(y[0], y[1]), T::pack(y[2], y[3])};
+        }
+    }
+}
+
+template <class T, int DP>
+int launch(const AttnArgs &a, hipStream_t st)
+{
+    const unsigned grid = (unsigned)a.kv.n_seq * a.kv.Hk * a.row_blocks * a.S;
+    if (a.out_f32)
+        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, T::TERMS>), dim3(grid), dim3(kThreads), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, 1>), dim3(grid), dim3(kThreads), 0, st, a);
+    return hip_status("attn prefill launch");
+}
+
+template <class T>
+int launch_dim(const AttnArgs &a, hipStream_t st)
+{
+    return a.kv.D <= 64 ? launch<T, 64>(a, st) : a.kv.D <= 128 ? launch<T, 128>(a, st) : launch<T, 256>(a, st);
+}
+
+} // namespace
+
+namespace rfx {
+
+int attn_prefill_launch(const AttnArgs &a, int type, hipStream_t st)
+{
+    return type == RFX_BF16 ? launch_dim<BF16>(a, st) : launch_dim<F16>(a, st);
+}
+
+} // namespace rfx

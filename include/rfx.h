@@ -411,6 +411,97 @@ int rfx_moe_debug_prefill(const rfx_moe_layer *L, int q, int k, const int8_t *xq
                           size_t ws_bytes, int probe_expert, int probe_first, float *h, int32_t *dots_gate,
                           int32_t *dots_up, int32_t *dots_down, void *stream);
 
+/* ------------------------------------------------------------------ */
+/* Attention over a paged key-value cache.                             */
+/* ------------------------------------------------------------------ */
+/* The half of a decoder layer between its projections (rfx_gemv_grouped,
+ * rfx_gemm) and its MoE layer: rfx_qk_norm_rope turns the projections'
+ * outputs into queries and cache entries, rfx_attn reads the cache.
+ *
+ * Element types of queries, cache and attention output. */
+enum { RFX_F32 = 0, RFX_F16 = 1, RFX_BF16 = 2 };
+
+/* The cache of one layer: keys and values [n_pages][n_kv_heads][page_size]
+ * [head_dim], so that one head's keys of a page are contiguous. Slots that
+ * hold no token may contain anything (NaN included). */
+typedef struct rfx_kv_cache {
+    int32_t type;       /* RFX_F16 or RFX_BF16 */
+    int32_t n_kv_heads; /* >= 1 */
+    int32_t head_dim;   /* multiple of 8, 8..256 */
+    int32_t page_size;  /* tokens per page: a power of two, 1..4096 */
+    int32_t n_pages;    /* >= 1 */
+    int32_t reserved;
+    void *k, *v;        /* device, 16-B aligned */
+} rfx_kv_cache;
+
+/* A batch of sequences with new tokens. Sequence s has the token rows
+ * q_off[s] .. q_off[s+1] - 1 (none is allowed) and kv_len[s] cached tokens,
+ * the new ones included: its last new token is at position kv_len[s] - 1.
+ * Token p of sequence s is slot p % page_size of page page_table[s *
+ * table_stride + p / page_size]. The arrays are on the device and may change
+ * between replays of a captured graph; the kernels stay inside the buffers
+ * whatever they hold: rows outside 0..n_tokens - 1, tokens past the table
+ * and pages outside 0..n_pages - 1 are neither read nor written (such a key
+ * is not visible; a sequence whose rows leave 0..n_tokens - 1 is skipped),
+ * and kv_len counts as at most table_stride * page_size. Rows of no
+ * sequence, before q_off[0] or from q_off[n_seq] on, keep what their outputs
+ * hold. table_stride * page_size <= 2^30; n_tokens and max_q <= 2^23. */
+typedef struct rfx_kv_batch {
+    int32_t n_seq;             /* >= 1 */
+    int32_t n_tokens;          /* rows of the token arrays, >= 0 */
+    int32_t max_q;             /* most new tokens of any sequence; rfx_attn leaves a sequence's rows past it */
+    int32_t table_stride;      /* entries per row of page_table */
+    const int32_t *q_off;      /* [n_seq + 1], ascending */
+    const int32_t *kv_len;     /* [n_seq] */
+    const int32_t *page_table; /* [n_seq][table_stride] */
+} rfx_kv_batch;
+
+/* Per head of the new tokens' queries and keys: an RMS norm (where its
+ * weight is given), x w / sqrt(mean(x^2) + eps), then the rotation of the
+ * first rot_dim elements by the token's position p: each pair (a, b) becomes
+ * (a cos t - b sin t, b cos t + a sin t), t = p inv_freq[i]. Pair i is
+ * elements i and rot_dim / 2 + i, or 2 i and 2 i + 1 with interleaved != 0.
+ * Queries go to q_out [n_tokens][n_heads][head_dim] in the cache's type;
+ * keys, and the values unchanged, to the tokens' cache slots (two rows with
+ * one slot race). fp32 arithmetic (angles fp64), one rounding to nearest
+ * even at the end. q_out must not overlap the inputs. One launch.
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_HIP. */
+typedef struct rfx_qk_rope {
+    const float *q, *k, *v;              /* fp32 rows [heads][head_dim], 16-B aligned */
+    int64_t q_stride, k_stride, v_stride; /* elements between rows: multiples of 4, at least heads * head_dim */
+    const double *inv_freq;              /* fp64 [rot_dim / 2] radians per position (NULL allowed at rot_dim 0) */
+    const float *q_weight, *k_weight;    /* fp32 [head_dim], 16-B aligned, or NULL: no norm */
+    float eps;                           /* >= 0 */
+    int32_t n_heads;                     /* query heads: a multiple of n_kv_heads, at most 1024 */
+    int32_t rot_dim;                     /* multiple of 8, 0..head_dim */
+    int32_t interleaved;
+} rfx_qk_rope;
+int rfx_qk_norm_rope(const rfx_qk_rope *args, const rfx_kv_cache *cache, const rfx_kv_batch *batch, void *q_out,
+                     void *stream);
+
+/* out = softmax(scale q k^T) v over the keys each token sees, per query head
+ * h against kv head h / (n_heads / n_kv_heads). The token at position p sees
+ * the cached tokens j <= p, and with window > 0 only those with j > p -
+ * window or j < sinks (the first tokens, which stay visible). A row that
+ * sees nothing is zero. q [n_tokens][n_heads][head_dim] in the cache's type;
+ * out the same shape in out_type: RFX_F32 (what rfx_quantize_act takes) or
+ * the cache's type. Scores, softmax and sums are fp32; for an fp32 result
+ * the softmax weights enter the matrix core as two (fp16) or three (bf16)
+ * terms, for a 16-bit result of more than a few rows per kv head as one.
+ * Cached keys and values that a sequence's tokens see are assumed finite; a
+ * key outside every row's window, and every slot past kv_len, may hold
+ * anything. Results do not depend on timing: splits of the keys are joined
+ * in a fixed order.
+ * ws: zero-filled workspace of rfx_attn_workspace_bytes (which depends on
+ * n_seq, max_q, table_stride, the page size and the heads), 256-B aligned,
+ * NULL allowed when that is 0; every completed call leaves its counters
+ * zero. A workspace must not be shared by calls that can run concurrently,
+ * graphs captured with it included. scale > 0.
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
+size_t rfx_attn_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads);
+int rfx_attn(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads, float scale,
+             int window, int sinks, void *out, int out_type, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
