@@ -1,5 +1,5 @@
-// Host side of the paged-cache entry points: argument checks, the choice of
-// kernel and split, workspace sizes.
+// Host side of the paged-cache entry points (argument checks, the choice of
+// kernel and split, workspace sizes), and the launch that joins split keys.
 #include <cmath>
 
 #include "rfx_kv.h"
@@ -43,6 +43,96 @@ int check_kv(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads, const ch
 
 namespace {
 
+using namespace dev;
+
+constexpr int kMaxSplits = 64; // one lane of the join each
+
+// Joins the splits of one row per wave: lane s holds the factor of split s,
+// exp2(c (m_s - max m)), and the partials are added in split order, so
+// the result does not depend on timing. Reads S partials per row once;
+// blocks that one split covered are done already.
+template <class T, int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
+{
+    constexpr int PER = DP / 64; // elements per lane
+    typedef float fp __attribute__((ext_vector_type(PER)));
+    const KvArgs &kv = a.kv;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int unit = blockIdx.x / (a.rows / 4), r = blockIdx.x % (a.rows / 4) * 4 + wave;
+    const int hk = unit % kv.Hk, rb = unit / kv.Hk % a.row_blocks, seq = unit / kv.Hk / a.row_blocks;
+    const Seq sq = load_seq(kv, seq);
+    const int nrows = sq.nq * kv.G, row0 = rb * a.rows, row = row0 + r;
+    if (row >= nrows)
+        return;
+    const int row_end = min(nrows, row0 + a.rows);
+    const KeyTiles kt = key_tiles(a.bn, sq.p0 + row0 / kv.G, sq.p0 + (row_end - 1) / kv.G, sq.kv, a.window, a.sinks);
+    int per, active;
+    split_tiles(a, kt.n, per, active);
+    if (active == 1)
+        return;
+    const size_t slot = (size_t)unit * a.S * a.rows + r;
+    f2 st = {-INFINITY, 0.f};
+    if (lane < active)
+        st = *reinterpret_cast<const f2 *>(a.stat + (slot + (size_t)lane * a.rows) * 2);
+    float m = st.x;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor(m, o, 64));
+    const float f = st.x == -INFINITY ? 0.f : fast_exp2(a.c * (st.x - m));
+    float l = st.y * f;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        l += __shfl_xor(l, o, 64);
+    fp sum;
+#pragma unroll
+    for (int i = 0; i < PER; i++)
+        sum[i] = 0.f;
+    const float *p = a.part + slot * DP + PER * lane;
+    const size_t stride = (size_t)a.rows * DP;
+    // eight partials' loads at a time; past the last, the last again with
+    // factor zero
+    for (int s = 0; s < active; s += 8) {
+        fp x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            x[i] = *reinterpret_cast<const fp *>(p + min(s + i, active - 1) * stride);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float w = s + i < active ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(s + i, 63))) : 0.f;
+            sum += x[i] * w;
+        }
+    }
+    const int d = PER * lane;
+    if (d >= kv.D)
+        return;
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const size_t at = ((size_t)(sq.t0 + row / kv.G) * kv.Hq + hk * kv.G + row % kv.G) * kv.D + d;
+    if (a.out_f32) {
+        *reinterpret_cast<fp *>(static_cast<float *>(a.out) + at) = sum * inv;
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+        if constexpr (PER == 1)
+            *o = (uint16_t)T::pack(sum[0] * inv, 0.f);
+        else
+#pragma unroll
+            for (int i = 0; i < PER; i += 2)
+                *reinterpret_cast<uint32_t *>(o + i) = T::pack(sum[i] * inv, sum[i + 1] * inv);
+    }
+}
+
+template <class T>
+int join(const AttnArgs &a, int64_t units, hipStream_t st)
+{
+    const dim3 grid((unsigned)(units * (a.rows / 4)));
+    if (a.kv.D <= 64)
+        hipLaunchKernelGGL((attn_join_kernel<T, 64>), grid, dim3(256), 0, st, a);
+    else if (a.kv.D <= 128)
+        hipLaunchKernelGGL((attn_join_kernel<T, 128>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<T, 256>), grid, dim3(256), 0, st, a);
+    return hip_status("attn join launch");
+}
+
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Plan {
@@ -50,8 +140,9 @@ struct Plan {
     int row_tiles;   // decode: 16-row tiles per workgroup
     int row_blocks;
     int S, min_tiles;
-    int64_t units;   // (sequence, kv head, row block)
-    size_t part, cnt;
+    int rows, bn;    // rows of a block, keys of a tile
+    int64_t units;   // (sequence, row block, kv head)
+    size_t part, stat;
 };
 
 // The decode kernel serves up to 32 rows (new tokens x query heads of a kv
@@ -65,28 +156,32 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
     const int64_t rows = (int64_t)B->max_q * (n_heads / C->n_kv_heads);
     const int dp = C->head_dim <= 64 ? 64 : C->head_dim <= 128 ? 128 : 256;
     p.decode = rows <= (dp == 256 ? 16 : 32);
-    const int per_block = p.decode ? (rows <= 16 ? 16 : 32) : 128;
-    p.row_tiles = per_block / 16;
-    p.row_blocks = (int)((rows + per_block - 1) / per_block);
-    const int bn = p.decode ? 32 : dp == 256 ? 32 : 64;
+    p.rows = p.decode ? (rows <= 16 ? 16 : 32) : 128;
+    p.row_tiles = p.rows / 16;
+    p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
+    p.bn = p.decode || dp == 256 ? 32 : 64;
     p.min_tiles = p.decode ? 8 : 4;
-    const int64_t tiles = ceil_div((int64_t)B->table_stride * C->page_size, bn);
+    const int64_t tiles = ceil_div((int64_t)B->table_stride * C->page_size, p.bn);
     p.units = (int64_t)B->n_seq * C->n_kv_heads * p.row_blocks;
     const int64_t want = 2 * 256 / (p.units < 512 ? p.units : 512);
     const int64_t most = ceil_div(tiles, p.min_tiles);
     p.S = (int)(want < most ? want : most);
-    if (p.S < 1)
-        p.S = 1;
-    if (p.S > 64)
-        p.S = 64;
+    p.S = p.S < 1 ? 1 : p.S > kMaxSplits ? kMaxSplits : p.S;
     if (p.S > 1) {
-        p.part = align256((size_t)p.units * p.S * per_block * (dp + 2) * sizeof(float));
-        p.cnt = align256((size_t)p.units * sizeof(unsigned));
+        const size_t n = (size_t)p.units * p.S * p.rows;
+        p.part = align256(n * dp * sizeof(float));
+        p.stat = align256(n * 2 * sizeof(float));
     }
     return p;
 }
 
 } // namespace
+
+int attn_join_launch(const AttnArgs &a, int type, int64_t units, hipStream_t st)
+{
+    return type == RFX_BF16 ? join<BF16>(a, units, st) : join<F16>(a, units, st);
+}
+
 } // namespace rfx
 
 using namespace rfx;
@@ -99,7 +194,7 @@ size_t rfx_attn_workspace_bytes(const rfx_kv_cache *C, const rfx_kv_batch *B, in
         C->head_dim > kMaxHeadDim || C->page_size < 1 || B->n_seq < 1 || B->max_q < 1 || B->max_q > kMaxTokens || B->table_stride < 1)
         return 0;
     const Plan p = plan(C, B, n_heads);
-    return p.part + p.cnt;
+    return p.part + p.stat;
 }
 
 int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads, float scale, int window,
@@ -120,9 +215,9 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     if (p.units * p.S >= (int64_t)kMaxTokens)
         return fail(RFX_E_INVAL, "rfx_attn: %d sequences of up to %d new tokens need more than %d workgroups",
                     B->n_seq, B->max_q, kMaxTokens);
-    if (p.part + p.cnt) {
-        if (!ws || ws_bytes < p.part + p.cnt)
-            return fail(RFX_E_WORKSPACE, "rfx_attn: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.part + p.cnt);
+    if (p.part + p.stat) {
+        if (!ws || ws_bytes < p.part + p.stat)
+            return fail(RFX_E_WORKSPACE, "rfx_attn: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.part + p.stat);
         if ((st = check_ptr(ws, 256, "ws")))
             return st;
     }
@@ -138,11 +233,16 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     a.sinks = sinks;
     a.S = p.S;
     a.row_blocks = p.row_blocks;
+    a.rows = p.rows;
+    a.bn = p.bn;
     a.min_tiles = p.min_tiles;
-    a.cnt = static_cast<unsigned *>(ws);
-    a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.cnt);
-    return p.decode ? attn_decode_launch(a, C->type, p.row_tiles, (hipStream_t)stream)
-                    : attn_prefill_launch(a, C->type, (hipStream_t)stream);
+    if (p.S > 1) {
+        a.part = static_cast<float *>(ws);
+        a.stat = reinterpret_cast<float *>(static_cast<char *>(ws) + p.part);
+    }
+    st = p.decode ? attn_decode_launch(a, C->type, p.row_tiles, (hipStream_t)stream)
+                  : attn_prefill_launch(a, C->type, (hipStream_t)stream);
+    return st || p.S == 1 ? st : attn_join_launch(a, C->type, p.units, (hipStream_t)stream);
 }
 
 } // extern "C"

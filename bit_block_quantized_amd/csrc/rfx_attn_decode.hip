@@ -14,8 +14,7 @@
 //   barrier) by transposed reads.
 // Each wave keeps a running maximum and sum per row (fp32); waves are joined
 // through LDS, and where few rows have long sequences the keys are split
-// over S workgroups whose partials the last to arrive joins in split order
-// (results do not depend on the arrival order).
+// over S workgroups whose partials a second launch joins in split order.
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -25,7 +24,6 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int BN = 32;                  // keys per wave and tile
-constexpr int kWaitVmcnt0 = 0x0F70;     // s_waitcnt vmcnt(0)
 
 // LDS bytes: each wave's V piece, reused for the waves' join
 // ([wave][16 rows][DP + 4] floats).
@@ -52,30 +50,21 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     constexpr int TERMS = T::TERMS;
     __shared__ __align__(16) char smem[lds_bytes<DP>()];
     __shared__ float s_m[kWaves][NR * 16], s_l[kWaves][NR * 16];
-    __shared__ int s_last;
 
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const KvArgs &kv = a.kv;
-    int b = blockIdx.x;
-    const int split = b % a.S;
-    b /= a.S;
-    const int rb = b % a.row_blocks;
-    b /= a.row_blocks;
-    const int hk = b % kv.Hk, seq = b / kv.Hk;
-    const int unit = blockIdx.x / a.S;
+    const int split = blockIdx.x % a.S, unit = blockIdx.x / a.S, hk = unit % kv.Hk, seq = unit / kv.Hk;
     const int D = kv.D;
 
     const Seq sq = load_seq(kv, seq);
-    const int nrows = sq.nq * kv.G;
-    const int row0 = rb * (NR * 16);
-    if (row0 >= nrows)
+    const int nrows = min(sq.nq * kv.G, NR * 16);
+    if (nrows <= 0)
         return;
-    const int row_end = min(nrows, row0 + NR * 16);
-    const int p_lo = sq.p0 + row0 / kv.G, p_hi = sq.p0 + (row_end - 1) / kv.G;
-    const KeyTiles kt = key_tiles<BN>(p_lo, p_hi, sq.kv, a.window, a.sinks);
-    const int per = max(a.min_tiles, (kt.n + a.S - 1) / a.S);
-    const int active = max(1, (kt.n + per - 1) / per);
+    const int p_lo = sq.p0, p_hi = sq.p0 + (nrows - 1) / kv.G;
+    const KeyTiles kt = key_tiles(BN, p_lo, p_hi, sq.kv, a.window, a.sinks);
+    int per, active;
+    split_tiles(a, kt.n, per, active);
     if (split >= active)
         return;
     const int t_begin = split * per + wave, t_end = min(kt.n, (split + 1) * per);
@@ -84,12 +73,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     // row l % 16, elements 32 c + 8 (l / 16) .. + 7) and its position
     u4 qf[NR][NC];
     int pos[NR];
-    bool row_ok[NR];
 #pragma unroll
     for (int n = 0; n < NR; n++) {
-        const int row = row0 + 16 * n + r16;
-        row_ok[n] = row < nrows;
-        const int rr = min(row, nrows - 1), tok = rr / kv.G, head = hk * kv.G + rr % kv.G;
+        const int row = 16 * n + r16, rr = min(row, nrows - 1), tok = rr / kv.G, head = hk * kv.G + rr % kv.G;
         pos[n] = sq.p0 + tok;
         const uint16_t *qp = a.q + ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
 #pragma unroll
@@ -313,7 +299,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
             s_l[wave][16 * n + r16] = l[n];
         }
     }
-    float *part = a.part + ((size_t)unit * a.S + split) * (NR * 16) * (DP + 2);
+    const size_t slot = ((size_t)unit * a.S + split) * (NR * 16);
     const bool joined = active == 1;
     float *o_lds = reinterpret_cast<float *>(smem);
     constexpr int OP = DP + 4;
@@ -330,7 +316,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
             *reinterpret_cast<f32x4 *>(o_lds + (wave * 16 + r16) * OP + 16 * i + 4 * g4) = acc[n][i] * f;
         __syncthreads();
         // 16 threads per row, four elements each at a time
-        const int r = threadIdx.x >> 4, row = row0 + 16 * n + r;
+        const int r = threadIdx.x >> 4, row = 16 * n + r;
         float rm = s_m[0][16 * n + r], rl = 0.f;
 #pragma unroll
         for (int w = 1; w < kWaves; w++)
@@ -354,91 +340,18 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
                 else
                     *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at + d) = (u2){T::pack(o[0], o[1]), T::pack(o[2], o[3])};
             } else {
-                // agent-scope stores: the joining workgroup may run on another XCD
-                unsigned long long *pp = reinterpret_cast<unsigned long long *>(part + (size_t)(16 * n + r) * DP + d);
-                __hip_atomic_store(pp, __builtin_bit_cast(unsigned long long, (f2){o[0], o[1]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                __hip_atomic_store(pp + 1, __builtin_bit_cast(unsigned long long, (f2){o[2], o[3]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                *reinterpret_cast<f32x4 *>(a.part + (slot + row) * DP + d) = o;
             }
         }
         if (!joined && (threadIdx.x & 15) == 0)
-            __hip_atomic_store(reinterpret_cast<unsigned long long *>(part + (size_t)NR * 16 * DP) + 16 * n + r,
-                               __builtin_bit_cast(unsigned long long, (f2){rm, rl}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (joined)
-        return;
-
-    // the last of the unit's splits to arrive joins them
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const unsigned n = __hip_atomic_fetch_add(a.cnt + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = n == (unsigned)active - 1;
-        if (s_last)
-            __hip_atomic_store(a.cnt + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s_last)
-        return;
-    const size_t pstride = (size_t)NR * 16 * (DP + 2);
-    const float *parts = a.part + (size_t)unit * a.S * pstride;
-    for (int r = threadIdx.x >> 4; row0 + r < row_end; r += 16) {
-        const int row = row0 + r;
-        const size_t at = ((size_t)(sq.t0 + row / kv.G) * kv.Hq + hk * kv.G + row % kv.G) * D;
-        const auto stat = [&](int s) {
-            return __builtin_bit_cast(f2, __hip_atomic_load(reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)NR * 16 * DP) + r,
-                                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        };
-        // 16 lanes share a row: lane j reads the statistics of splits j, j + 16, ...
-        const int j = threadIdx.x & 15;
-        float rm = -INFINITY;
-        for (int s = j; s < active; s += 16)
-            rm = fmaxf(rm, stat(s).x);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            rm = fmaxf(rm, __shfl_xor(rm, o, 16));
-        float rl = 0.f;
-        f32x4 o[DP / 64];
-#pragma unroll
-        for (int i = 0; i < DP / 64; i++)
-            o[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int s = 0; s < active; s++) { // split order
-            const f2 st = stat(s);
-            const float f = st.x == -INFINITY ? 0.f : fast_exp2(a.c * (st.x - rm));
-            rl += st.y * f;
-#pragma unroll
-            for (int i = 0; i < DP / 64; i++) {
-                const int d = 4 * j + 64 * i;
-                if (d < D) {
-                    const unsigned long long *pp = reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)r * DP + d);
-                    const f2 x = __builtin_bit_cast(f2, __hip_atomic_load(pp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-                    const f2 y = __builtin_bit_cast(f2, __hip_atomic_load(pp + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-                    o[i][0] += x.x * f;
-                    o[i][1] += x.y * f;
-                    o[i][2] += y.x * f;
-                    o[i][3] += y.y * f;
-                }
-            }
-        }
-        const float inv = rl > 0.f ? 1.0f / rl : 0.f;
-#pragma unroll
-        for (int i = 0; i < DP / 64; i++) {
-            const int d = 4 * j + 64 * i;
-            if (d < D) {
-                const f32x4 y = o[i] * inv;
-                if (a.out_f32)
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at + d) = y;
-                else
-                    *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + at + d) = (u2){T::pack(y[0], y[1]), T::pack(y[2], y[3])};
-            }
-        }
+            *reinterpret_cast<f2 *>(a.stat + (slot + row) * 2) = (f2){rm, rl};
     }
 }
 
 template <class T, int DP, int NR>
 int launch(const AttnArgs &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)a.kv.n_seq * a.kv.Hk * a.row_blocks * a.S;
+    const unsigned grid = (unsigned)a.kv.n_seq * a.kv.Hk * a.S;
     if (a.kv.page_shift >= 5)
         hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, true>), dim3(grid), dim3(64 * kWaves), 0, st, a);
     else

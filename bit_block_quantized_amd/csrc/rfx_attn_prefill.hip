@@ -15,8 +15,8 @@
 //   of V^T are read in that order (transposed LDS reads), so the weights stay
 //   in their lane.
 // Tiles outside a wave's rows' window or after their positions are skipped.
-// Few row blocks over long sequences: the keys are split over S workgroups,
-// and the last to arrive joins the partials in split order.
+// Few row blocks over long sequences: the keys are split over S workgroups
+// and a second launch joins the partials in split order.
 //
 // Rounding: weights are rounded once to the cache's type for a result of
 // that type (its own rounding is as large); for an fp32 result they are
@@ -31,7 +31,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kWaitVmcnt0 = 0x0F70; // s_waitcnt vmcnt(0)
 
 // Pitches (bytes) of the LDS rows: K rows are read 16 bytes per lane down a
 // column, so neighbours are 16 bytes apart modulo the 256 bytes of the
@@ -53,7 +52,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     constexpr int BN = L::BN, NC = DP / 16, ND = DP / 32, NK = BN / 32;
     __shared__ __align__(16) char smem[2 * L::buf];
     __shared__ unsigned s_bad[3][2]; // keys of a tile with an unusable page id
-    __shared__ int s_last;
 
     const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, hl = lane >> 5, i16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -75,9 +73,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     if (row0 >= nrows)
         return;
     const int row_end = min(nrows, row0 + kRows);
-    const KeyTiles kt = key_tiles<BN>(sq.p0 + row0 / kv.G, sq.p0 + (row_end - 1) / kv.G, sq.kv, a.window, a.sinks);
-    const int per = max(a.min_tiles, (kt.n + a.S - 1) / a.S);
-    const int active = max(1, (kt.n + per - 1) / per);
+    const KeyTiles kt = key_tiles(BN, sq.p0 + row0 / kv.G, sq.p0 + (row_end - 1) / kv.G, sq.kv, a.window, a.sinks);
+    int per, active;
+    split_tiles(a, kt.n, per, active);
     if (split >= active)
         return;
     const int t_begin = split * per, t_end = min(kt.n, t_begin + per);
@@ -270,83 +268,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
         return;
     }
 
-    // partials by agent-scope stores (the joining workgroup may run on
-    // another XCD), then the arrival count
-    constexpr size_t pstride = (size_t)kRows * (DP + 2);
-    float *part = a.part + ((size_t)unit * a.S + split) * pstride;
-    const int lr = 32 * wave + r32;
-    if (row_ok) {
-#pragma unroll
-        for (int i = 0; i < ND; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                unsigned long long *pp = reinterpret_cast<unsigned long long *>(part + (size_t)lr * DP + 32 * i + 8 * j + 4 * hl);
-                __hip_atomic_store(pp, __builtin_bit_cast(unsigned long long, (f2){acc[i][4 * j], acc[i][4 * j + 1]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                __hip_atomic_store(pp + 1, __builtin_bit_cast(unsigned long long, (f2){acc[i][4 * j + 2], acc[i][4 * j + 3]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-        if (hl == 0)
-            __hip_atomic_store(reinterpret_cast<unsigned long long *>(part + (size_t)kRows * DP) + lr,
-                               __builtin_bit_cast(unsigned long long, (f2){m, l}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-    __syncthreads();
-    if (tid == 0) {
-        const unsigned n = __hip_atomic_fetch_add(a.cnt + unit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = n == (unsigned)active - 1;
-        if (s_last)
-            __hip_atomic_store(a.cnt + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s_last)
+    if (!row_ok)
         return;
-    const float *parts = a.part + (size_t)unit * a.S * pstride;
-    const int j16 = tid & 15;
-    for (int r = tid >> 4; row0 + r < row_end; r += kThreads / 16) {
-        const auto stat = [&](int s) {
-            return __builtin_bit_cast(f2, __hip_atomic_load(reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)kRows * DP) + r,
-                                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        };
-        float rm = -INFINITY, rl = 0.f;
-        for (int s = j16; s < active; s += 16)
-            rm = fmaxf(rm, stat(s).x);
+    const size_t slot = ((size_t)unit * a.S + split) * kRows + 32 * wave + r32;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            rm = fmaxf(rm, __shfl_xor(rm, o, 16));
-        f32x4 o[DP / 64];
+    for (int i = 0; i < ND; i++)
 #pragma unroll
-        for (int i = 0; i < DP / 64; i++)
-            o[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int s = 0; s < active; s++) { // split order
-            const f2 st = stat(s);
-            const float f = st.x == -INFINITY ? 0.f : fast_exp2(a.c * (st.x - rm));
-            rl += st.y * f;
-#pragma unroll
-            for (int i = 0; i < DP / 64; i++) {
-                const unsigned long long *pp = reinterpret_cast<const unsigned long long *>(parts + s * pstride + (size_t)r * DP + 4 * j16 + 64 * i);
-                const f2 x = __builtin_bit_cast(f2, __hip_atomic_load(pp, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-                const f2 y = __builtin_bit_cast(f2, __hip_atomic_load(pp + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-                o[i][0] += x.x * f;
-                o[i][1] += x.y * f;
-                o[i][2] += y.x * f;
-                o[i][3] += y.y * f;
-            }
-        }
-        const float inv = rl > 0.f ? 1.0f / rl : 0.f;
-        const int jr = row0 + r;
-        const size_t to = ((size_t)(sq.t0 + jr / kv.G) * kv.Hq + hk * kv.G + jr % kv.G) * D;
-#pragma unroll
-        for (int i = 0; i < DP / 64; i++) {
-            const int d = 4 * j16 + 64 * i;
-            if (d >= D)
-                continue;
-            const f32x4 y = o[i] * inv;
-            if (a.out_f32)
-                *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + to + d) = y;
-            else
-                *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.out) + to + d) = (u2){T::pack(y[0], y[1]), T::pack(y[2], y[3])};
-        }
-    }
+        for (int j = 0; j < 4; j++)
+            *reinterpret_cast<f32x4 *>(a.part + slot * DP + 32 * i + 8 * j + 4 * hl) =
+                (f32x4){acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+    if (hl == 0)
+        *reinterpret_cast<f2 *>(a.stat + slot * 2) = (f2){m, l};
 }
 
 template <class T, int DP>

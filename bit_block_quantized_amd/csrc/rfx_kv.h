@@ -63,13 +63,17 @@ struct AttnArgs {
     int window, sinks; // window 0: none
     int S;             // splits of a sequence's keys (grid)
     int row_blocks;    // row blocks of a (sequence, kv head) (grid)
+    int rows;          // rows of a block
+    int bn;            // keys of a tile
     int min_tiles;     // key tiles a split takes at least
-    float *part;       // workspace: partials of the splits
-    unsigned *cnt;     // workspace: arrival counter per (sequence, kv head, row block)
+    // workspace, where S > 1, by unit = (seq * row_blocks + block) * Hk + hk:
+    float *part;       // [unit][split][rows][DP] unnormalized results
+    float *stat;       // [unit][split][rows][2] their maxima and sums
 };
 
 int attn_decode_launch(const AttnArgs &a, int type, int row_tiles, hipStream_t st);
 int attn_prefill_launch(const AttnArgs &a, int type, hipStream_t st);
+int attn_join_launch(const AttnArgs &a, int type, int64_t units, hipStream_t st);
 
 namespace dev {
 
@@ -185,7 +189,7 @@ __device__ __forceinline__ Seq load_seq(const KvArgs &a, int s)
     return q;
 }
 
-// The key tiles of BN keys that rows with first position p_lo and last
+// The key tiles of bn keys that rows with first position p_lo and last
 // position p_hi can see: the sinks' tiles, then those of the window.
 struct KeyTiles {
     int hi;    // keys from hi on are after every row
@@ -196,17 +200,24 @@ struct KeyTiles {
     int n;     // tiles in all
 };
 
-template <int BN>
-__device__ __forceinline__ KeyTiles key_tiles(int p_lo, int p_hi, int kv, int window, int sinks)
+__device__ __forceinline__ KeyTiles key_tiles(int bn, int p_lo, int p_hi, int kv, int window, int sinks)
 {
     KeyTiles t;
     t.hi = max(0, min(kv, p_hi + 1));
     t.lo = window ? max(0, min(p_lo - window + 1, t.hi)) : 0;
     t.sk = min(sinks, t.lo);
-    t.nst = (t.sk + BN - 1) / BN;
-    t.wt = max(t.lo / BN, t.nst);
-    t.n = t.nst + max(0, (t.hi + BN - 1) / BN - t.wt);
+    t.nst = (t.sk + bn - 1) / bn;
+    t.wt = max(t.lo / bn, t.nst);
+    t.n = t.nst + max(0, (t.hi + bn - 1) / bn - t.wt);
     return t;
+}
+
+// How a block's n key tiles are split: `per` tiles each over `active` of the
+// grid's S splits (one, with no tiles, for a block that sees no key).
+__device__ __forceinline__ void split_tiles(const AttnArgs &a, int n, int &per, int &active)
+{
+    per = max(a.min_tiles, (n + a.S - 1) / a.S);
+    active = max(1, (n + per - 1) / per);
 }
 
 // First key of the i-th tile.

@@ -492,11 +492,11 @@ int rfx_qk_norm_rope(const rfx_qk_rope *args, const rfx_kv_cache *cache, const r
  * key outside every row's window, and every slot past kv_len, may hold
  * anything. Results do not depend on timing: splits of the keys are joined
  * in a fixed order.
- * ws: zero-filled workspace of rfx_attn_workspace_bytes (which depends on
- * n_seq, max_q, table_stride, the page size and the heads), 256-B aligned,
- * NULL allowed when that is 0; every completed call leaves its counters
- * zero. A workspace must not be shared by calls that can run concurrently,
- * graphs captured with it included. scale > 0.
+ * ws: workspace of rfx_attn_workspace_bytes (which depends on n_seq, max_q,
+ * table_stride, the page size and the heads), 256-B aligned, NULL allowed
+ * when that is 0; it needs no initialisation. A workspace must not be shared
+ * by calls that can run concurrently, graphs captured with it included.
+ * scale > 0. One launch, and a second one where keys are split.
  * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
 size_t rfx_attn_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads);
 int rfx_attn(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads, float scale,

@@ -19,12 +19,9 @@ def run(b, q, scale, window=0, sinks=0, out="f32", ws=None):
     o = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
     n = R.attn_workspace_bytes(cache, batch, heads)
     if ws is None and n:
-        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN: it needs no initialisation
     R.attn(q.cuda(), cache, batch, o, scale, window, sinks, ws)
     torch.cuda.synchronize()
-    if ws is not None and n:
-        units = -(-batch.n_seq * cache.n_kv_heads * 4 // 256) * 256
-        assert not ws[:units].any(), "the workspace's counters are not zero after the call"
     return o.cpu()
 
 
