@@ -129,6 +129,8 @@ _SIGS = {
     "rfx_moe_forward_status": ([_P, _I, _I, _P, _SZ, _P], _I),
     "rfx_moe_debug_hidden": ([_P, _I, _I, _P, _SZ, _P, _P, _P, _P], _I),
     "rfx_moe_debug_prefill": ([_P, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _P, _P, _P, _P, _P], _I),
+    "rfx_gemm_workspace_bytes": ([_P, _I], _SZ),
+    "rfx_gemm": ([_P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _SZ, _P], _I),
     "rfx_qk_norm_rope": ([_P, _P, _P, _P, _P], _I),
     "rfx_attn_workspace_bytes": ([_P, _P, _I], _SZ),
     "rfx_attn": ([_P, _P, _P, _I, _F, _I, _I, _P, _I, _P, _SZ, _P], _I),
@@ -309,6 +311,21 @@ def gemv_q4(W: DeviceQMat, xq, xs, xsum, y, ws=None, stream=None):
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().rfx_gemv_q4(W.ref(), _dptr(xq), _dptr(xs), _dptr(xsum), _dptr(y), _dptr(ws),
                              ws_bytes, _stream(stream)))
+
+
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+
+
+def gemm_workspace_bytes(W: DeviceQMat, q: int) -> int:
+    return int(lib().rfx_gemm_workspace_bytes(W.ref(), q))
+
+
+def gemm(W: DeviceQMat, xq, xs, xsum, q, y, bias=None, act=ACT_NONE, resid=None, ws=None, stream=None):
+    """y = resid + act(W x + bias) for q columns (rfx_gemm)."""
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().rfx_gemm(W.ref(), _dptr(xq), _dptr(xs), _dptr(xsum), q, _dptr(bias), act, _dptr(resid), _dptr(y),
+                          _dptr(ws), ws_bytes, _stream(stream)))
 
 
 def gemv_jobs(jobs):

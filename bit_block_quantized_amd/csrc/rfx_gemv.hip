@@ -55,6 +55,7 @@
 #include "rfx_decode.h"
 #include "rfx_mx4.h"
 #include "rfx_xtile.h"
+#include "rfx_epi.h"
 #include "rfx_internal.h"
 
 namespace rfx {
@@ -217,10 +218,20 @@ __device__ __forceinline__ void compute_tile(const WTile<FMT, Q> &t, int s, int 
     }
 }
 
+// What happens to a finished sum on its way to y: nothing (rfx_gemv), or
+// the epilogue of rfx_gemm.
+struct Plain {
+    __device__ __forceinline__ float operator()(float v, int, int, int) const { return v; }
+};
+struct Epi {
+    EpiArgs e;
+    __device__ __forceinline__ float operator()(float v, int j, int n, int N) const { return finish(e, v, j, n, N); }
+};
+
 // Wave 0 of a workgroup: sum the W waves' partials (fixed order) and
 // either store y or climb the split-K exchange tree.
-template <int Q>
-__device__ __forceinline__ void gemv_finish(const GemvArgs &a, int p, int g, int W, const float *red)
+template <int Q, class E>
+__device__ __forceinline__ void gemv_finish(const GemvArgs &a, int p, int g, int W, const float *red, const E &epi)
 {
     const int lane = threadIdx.x & 63;
     const int row = g * 64 + lane;
@@ -236,7 +247,7 @@ __device__ __forceinline__ void gemv_finish(const GemvArgs &a, int p, int g, int
         if (row < a.N) {
 #pragma unroll
             for (int j = 0; j < Q; j++)
-                a.y[(size_t)j * a.N + row] = val[j];
+                a.y[(size_t)j * a.N + row] = epi(val[j], j, row, a.N);
         }
         return;
     }
@@ -278,7 +289,7 @@ __device__ __forceinline__ void gemv_finish(const GemvArgs &a, int p, int g, int
 #pragma unroll
         for (int j = 0; j < Q; j++)
             if (active[j])
-                a.y[(size_t)j * a.N + row] = val[j];
+                a.y[(size_t)j * a.N + row] = epi(val[j], j, row, a.N);
     }
 }
 
@@ -289,8 +300,8 @@ __device__ __forceinline__ void gemv_finish(const GemvArgs &a, int p, int g, int
 // Workgroup p (of P) of row group g; red holds W x Q x 64 floats of LDS.
 // LBC: the multi-tile loop takes the broadcast path too (two activation
 // slices in registers; affordable below 1024 threads per workgroup).
-template <int FMT, int Q, bool DOTS, bool FULL, bool LBC = false>
-__device__ __forceinline__ void gemv_body(const GemvArgs &a, int p, int g, float *red)
+template <int FMT, int Q, bool DOTS, bool FULL, bool LBC = false, class E = Plain>
+__device__ __forceinline__ void gemv_body(const GemvArgs &a, int p, int g, float *red, const E &epi = E())
 {
     // wave index is uniform per wave; say so, so the tile index, the
     // activation addresses and the loop bounds live in SGPRs.
@@ -361,7 +372,7 @@ __device__ __forceinline__ void gemv_body(const GemvArgs &a, int p, int g, float
         red[(wave * Q + j) * 64 + lane] = acc[j];
     __syncthreads();
     if (wave == 0)
-        gemv_finish<Q>(a, p, g, W, red);
+        gemv_finish<Q>(a, p, g, W, red, epi);
 }
 
 // FP4 blocks go to the block-scaled matrix core (rfx_mx4.h) for one or two
@@ -382,8 +393,8 @@ constexpr bool use_mx()
 // keeps the next tile in flight (two tile buffers; within the register
 // budget of a workgroup of at most 256 threads), else it loads and
 // computes one tile at a time.
-template <int Q, bool FULL, bool LBC>
-__device__ __forceinline__ void gemv_body_mx(const GemvArgs &a, int p, int g, float *red)
+template <int Q, bool FULL, bool LBC, class E = Plain>
+__device__ __forceinline__ void gemv_body_mx(const GemvArgs &a, int p, int g, float *red, const E &epi = E())
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int W = blockDim.x >> 6;
@@ -433,7 +444,7 @@ __device__ __forceinline__ void gemv_body_mx(const GemvArgs &a, int p, int g, fl
     mx_to_red<Q>(acc, red, wave, lane);
     __syncthreads();
     if (wave == 0)
-        gemv_finish<Q>(a, p, g, W, red);
+        gemv_finish<Q>(a, p, g, W, red, epi);
 }
 
 // Test hook on the block-scaled matrix core: the products gemv_body_mx
@@ -492,6 +503,19 @@ __global__ __launch_bounds__(1024) void gemv_kernel(GemvArgs a)
     } else {
         gemv_body<FMT, Q, DOTS, FULL>(a, blockIdx.x, blockIdx.y, red);
     }
+}
+
+// The same with rfx_gemm's epilogue: applied by the lane that ends up with
+// the whole sum, so the result costs no further launch or pass.
+template <int FMT, int Q, bool FULL>
+__global__ __launch_bounds__(1024) void gemv_epi_kernel(GemvArgs a, EpiArgs e)
+{
+    __shared__ float red[16 * Q * 64];
+    const Epi epi{e};
+    if constexpr (use_mx<FMT, Q>())
+        gemv_body_mx<Q, FULL, false>(a, blockIdx.x, blockIdx.y, red, epi);
+    else
+        gemv_body<FMT, Q, false, FULL>(a, blockIdx.x, blockIdx.y, red, epi);
 }
 
 // Several independent GEMVs in one launch. The workgroups are the jobs'
@@ -624,6 +648,25 @@ int launch(int fmt, const GemvArgs &a, int q, int G, int W, hipStream_t st)
     case RFX_FP3E: return full ? launch_q<RFX_FP3E, DOTS, true>(a, q, G, W, st) : launch_q<RFX_FP3E, DOTS, false>(a, q, G, W, st);
     }
     return fail(RFX_E_INVAL, "unknown format");
+}
+
+template <int FMT, bool FULL>
+int launch_epi_q(const GemvArgs &a, const EpiArgs &e, int q, int G, int W, hipStream_t st)
+{
+    dim3 grid(a.P, G), block(64 * W);
+    switch (q) {
+    case 1: hipLaunchKernelGGL((gemv_epi_kernel<FMT, 1, FULL>), grid, block, 0, st, a, e); break;
+    case 2: hipLaunchKernelGGL((gemv_epi_kernel<FMT, 2, FULL>), grid, block, 0, st, a, e); break;
+    case 3: hipLaunchKernelGGL((gemv_epi_kernel<FMT, 3, FULL>), grid, block, 0, st, a, e); break;
+    default: hipLaunchKernelGGL((gemv_epi_kernel<FMT, 4, FULL>), grid, block, 0, st, a, e); break;
+    }
+    return hip_status("gemv epilogue launch");
+}
+
+template <int FMT>
+int launch_epi(const GemvArgs &a, const EpiArgs &e, int q, int G, int W, hipStream_t st)
+{
+    return a.K % kTileCols == 0 ? launch_epi_q<FMT, true>(a, e, q, G, W, st) : launch_epi_q<FMT, false>(a, e, q, G, W, st);
 }
 
 // P per job (a power of two, at most 8, and no more than its tiles need).
@@ -843,7 +886,45 @@ int scratch_address(void **out, hipStream_t st)
     return RFX_OK;
 }
 
+GemvArgs lone_args(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t *xsum, float *y, void *ws, int P)
+{
+    GemvArgs a{};
+    a.W = static_cast<const uint8_t *>(W->data);
+    a.N = W->rows;
+    a.K = W->cols;
+    a.S = (int)ceil_div(W->cols, kTileCols);
+    a.nb = W->cols / 32;
+    a.P = P;
+    a.xq = xq;
+    a.xs = xs;
+    a.xsum = xsum;
+    a.y = y;
+    a.slots = static_cast<unsigned *>(ws);
+    return a;
+}
+
 } // namespace
+
+namespace rfx {
+
+int gemv_epi(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t *xsum, int q, const EpiArgs &e,
+             float *y, void *ws, hipStream_t st)
+{
+    const int G = (int)ceil_div(W->rows, kTileRows), S = (int)ceil_div(W->cols, kTileCols);
+    const LaunchShape sh = choose_shape(G, S);
+    const GemvArgs a = lone_args(W, xq, xs, xsum, y, ws, sh.P);
+    switch (W->fmt) {
+    case RFX_FP2: return launch_epi<RFX_FP2>(a, e, q, G, sh.W, st);
+    case RFX_FP3: return launch_epi<RFX_FP3>(a, e, q, G, sh.W, st);
+    case RFX_FP4: return launch_epi<RFX_FP4>(a, e, q, G, sh.W, st);
+    case RFX_FP2M: return launch_epi<RFX_FP2M>(a, e, q, G, sh.W, st);
+    case RFX_Q8: return launch_epi<RFX_Q8>(a, e, q, G, sh.W, st);
+    case RFX_FP2S: return launch_epi<RFX_FP2S>(a, e, q, G, sh.W, st);
+    default: return launch_epi<RFX_FP3E>(a, e, q, G, sh.W, st);
+    }
+}
+
+} // namespace rfx
 
 extern "C" {
 
@@ -899,19 +980,7 @@ int rfx_gemv(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t
         if ((st = check_ptr(ws, 256, "ws")))
             return st;
     }
-    GemvArgs a{};
-    a.W = static_cast<const uint8_t *>(W->data);
-    a.N = W->rows;
-    a.K = W->cols;
-    a.S = S;
-    a.nb = W->cols / 32;
-    a.P = sh.P;
-    a.xq = xq;
-    a.xs = xs;
-    a.xsum = xsum;
-    a.y = y;
-    a.slots = static_cast<unsigned *>(ws);
-    return launch<false>(W->fmt, a, q, G, sh.W, (hipStream_t)stream);
+    return launch<false>(W->fmt, lone_args(W, xq, xs, xsum, y, ws, sh.P), q, G, sh.W, (hipStream_t)stream);
 }
 
 int rfx_gemv_noalloc(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t *xsum, int q, float *y,

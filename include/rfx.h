@@ -249,6 +249,31 @@ typedef struct rfx_gemv_job {
 size_t rfx_gemv_grouped_workspace_bytes(const rfx_gemv_job *jobs, int n_jobs);
 int rfx_gemv_grouped(const rfx_gemv_job *jobs, int n_jobs, void *ws, size_t ws_bytes, void *stream);
 
+/* The product with its epilogue, for any number of columns:
+ * y[j][n] = resid[j][n] + act(sum as in rfx_gemv + bias[n]).
+ * Decode's projections (q <= 4) run on the GEMV kernels, the epilogue in
+ * the lane that ends with the whole sum; prompts' (q > 4) on the matrix core,
+ * one exact integer block dot per 32-weight block and column, scaled and
+ * accumulated in fp32.
+ * W: count must be 1; any format at q <= 4, RFX_FP2, RFX_FP3 or RFX_FP4 at
+ * q > 4 (RFX_E_UNSUPPORTED otherwise). q 1..RFX_GEMM_MAX_Q. xq, xs and xsum
+ * as for rfx_gemv. bias fp32 [N] or NULL; act: RFX_ACT_SILU is z / (1 +
+ * e^-z), RFX_ACT_GELU z Phi(z), RFX_ACT_GELU_TANH its tanh approximation 0.5
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))); resid fp32 [q][N] or NULL,
+ * and may be y itself. y fp32 [q][N] overlaps no other argument.
+ * ws: zero-filled workspace of rfx_gemm_workspace_bytes(W, q) bytes, 256-B
+ * aligned (NULL allowed when that is 0). Calls of any W and q may use the
+ * same one in turn: its first 256 KiB are left zero, the rest needs no
+ * initialisation and holds anything afterwards. Launches that share it must
+ * not overlap. Results are deterministic (fixed-order sums).
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_UNSUPPORTED, RFX_E_WORKSPACE,
+ * RFX_E_HIP. */
+#define RFX_GEMM_MAX_Q 65536
+enum { RFX_ACT_NONE = 0, RFX_ACT_RELU = 1, RFX_ACT_SILU = 2, RFX_ACT_GELU = 3, RFX_ACT_GELU_TANH = 4 };
+size_t rfx_gemm_workspace_bytes(const rfx_qmat *W, int q);
+int rfx_gemm(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t *xsum, int q, const float *bias,
+             int act, const float *resid, float *y, void *ws, size_t ws_bytes, void *stream);
+
 /* Test hook: the decode path rfx_gemv takes for the same format and q,
  * storing every per-block integer dot D[j][n][b] (int32 [q][N][K/32])
  * instead of the scaled sum: the dot of the block's codebook values with the
@@ -494,8 +519,10 @@ int rfx_qk_norm_rope(const rfx_qk_rope *args, const rfx_kv_cache *cache, const r
  * in a fixed order.
  * ws: workspace of rfx_attn_workspace_bytes (which depends on n_seq, max_q,
  * table_stride, the page size and the heads), 256-B aligned, NULL allowed
- * when that is 0; it needs no initialisation. A workspace must not be shared
- * by calls that can run concurrently, graphs captured with it included.
+ * when that is 0; it needs no initialisation and holds anything after the
+ * call (so it is not one to share with an entry point that needs its
+ * workspace zero). A workspace must not be shared by calls that can run
+ * concurrently, graphs captured with it included.
  * scale > 0. One launch, and a second one where keys are split.
  * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
 size_t rfx_attn_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads);

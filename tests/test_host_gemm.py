@@ -1,0 +1,44 @@
+"""CPU tests of rfx_gemm's refusals and workspace sizes: every bad argument
+fails before any HIP call."""
+
+import ctypes
+
+import bit_block_quantized_amd as R
+
+INVAL, ALIGN, UNSUPPORTED, WORKSPACE = -1, -2, -4, -5
+P = 1 << 20  # an aligned address that is never followed
+
+
+def status(q=4, act=0, xq=P, xs=P, xsum=P, bias=None, resid=None, y=P, ws=None, ws_bytes=0, **kw):
+    W = R.QMat(*{**dict(fmt=4, rows=1024, cols=4096, count=1, data=P), **kw}.values())
+    return R.lib().rfx_gemm(ctypes.byref(W), xq, xs, xsum, q, bias, act, resid, y, ws, ws_bytes, None)
+
+
+def need(q, **kw):
+    W = R.QMat(*{**dict(fmt=4, rows=1024, cols=4096, count=1, data=P), **kw}.values())
+    return R.lib().rfx_gemm_workspace_bytes(ctypes.byref(W), q)
+
+
+def test_refusals():
+    for kw, st in ((dict(fmt=5), INVAL), (dict(rows=0), INVAL), (dict(cols=48), INVAL), (dict(count=2), INVAL),
+                   (dict(data=None), INVAL), (dict(data=P + 128), ALIGN), (dict(q=0), INVAL), (dict(q=65537), INVAL),
+                   (dict(act=-1), INVAL), (dict(act=5), INVAL), (dict(xq=None), INVAL), (dict(xq=P + 8), ALIGN),
+                   (dict(xs=P + 2), ALIGN), (dict(xsum=None), INVAL), (dict(y=None), INVAL), (dict(y=P + 1), ALIGN),
+                   (dict(bias=P + 2), ALIGN), (dict(resid=P + 3), ALIGN), (dict(ws=None), WORKSPACE),
+                   (dict(q=9, fmt=8), UNSUPPORTED), (dict(q=9, fmt=12), UNSUPPORTED), (dict(q=9, fmt=16), UNSUPPORTED),
+                   (dict(q=9, fmt=13), UNSUPPORTED), (dict(q=9), WORKSPACE),
+                   (dict(q=9, ws=P, ws_bytes=need(9) - 1), WORKSPACE), (dict(q=9, ws=P + 64, ws_bytes=1 << 40), ALIGN)):
+        assert status(**kw) == st, kw
+    assert R.lib().rfx_gemm(None, P, P, P, 1, None, 0, None, P, None, 0, None) == INVAL
+
+
+def test_workspace_sizes():
+    W = R.QMat(4, 1024, 4096, 1, P)
+    for q in (1, 4):
+        assert need(q) == R.lib().rfx_gemv_workspace_bytes(ctypes.byref(W), q) > 0
+    # the first 256 KiB stay the GEMV form's, whose slots fit in them
+    for q in (5, 64, 2048, 65536):
+        assert need(q) > (256 << 10) + 2 * q * 4096
+    assert all(R.lib().rfx_gemv_workspace_bytes(ctypes.byref(R.QMat(4, r, c, 1, P)), 4) <= 256 << 10
+               for r in (1, 64, 777, 4096, 20000) for c in (32, 512, 4096, 65536))
+    assert need(0) == need(65537) == need(9, fmt=8) == need(9, cols=33) == 0
