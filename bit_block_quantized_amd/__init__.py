@@ -571,5 +571,6 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
              wp, wn)
 
 
-from .layer import DeviceMoeLayer, MoeBuffers, PlacedMoeLayer, hot_experts_by_frequency  # noqa: E402,F401
+from .layer import (AttentionBuffers, DeviceAttention, DeviceMoeLayer, MoeBuffers, PlacedMoeLayer,  # noqa: E402,F401
+                    hot_experts_by_frequency)
 from . import layer  # noqa: E402,F401

@@ -180,3 +180,101 @@ class MoeBuffers:
         moe_ffn(layer, self.q, self.k, self.xq, self.xs, self.xsum, self.topk_idx, self.topk_w,
                 self.pairs_sorted, self.expert_off, y, self.ws, resid, stream)
         return y
+
+
+Q_PROJ, K_PROJ, V_PROJ, O_PROJ = 0, 1, 2, 3
+
+
+class DeviceAttention:
+    """The attention half of a decoder layer on the GPU: packed query, key,
+    value and output projections, optional per-head norm weights of queries
+    and keys, rotary frequencies, and the mask's window and sinks."""
+
+    def __init__(self, wq, wk, wv, wo, n_heads, n_kv_heads, head_dim, inv_freq, q_norm=None, k_norm=None, eps=1e-6,
+                 interleaved=False, window=0, sinks=0, scale=None):
+        self.wq, self.wk, self.wv, self.wo = wq, wk, wv, wo
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
+        for W, rows, name in ((wq, n_heads, "wq"), (wk, n_kv_heads, "wk"), (wv, n_kv_heads, "wv")):
+            if W.rows != rows * head_dim or W.cols != wq.cols:
+                raise ValueError(f"{name}: {W.rows} x {W.cols}, {rows * head_dim} x {wq.cols} wanted")
+        if wo.rows != wq.cols or wo.cols != n_heads * head_dim:
+            raise ValueError(f"wo: {wo.rows} x {wo.cols}, {wq.cols} x {n_heads * head_dim} wanted")
+        self.hidden = wq.cols
+        self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
+        self.eps, self.interleaved, self.window, self.sinks = eps, interleaved, window, sinks
+        self.scale = head_dim ** -0.5 if scale is None else scale
+
+    @classmethod
+    def build(cls, hidden, n_heads, n_kv_heads, head_dim, weight_fn, fmt=FP4, rot_dim=None, base=10000.0, q_norm=None,
+              k_norm=None, device="cuda", **kw):
+        """weight_fn(mat, rows, cols) -> fp32 [rows][cols]; mat is 0 query, 1
+        key, 2 value, 3 output. q_norm, k_norm: fp32 [head_dim] or None."""
+        import torch
+
+        from . import rope_inv_freq
+
+        def proj(mat, rows, cols):
+            return DeviceQMat.from_host(fmt, rows, cols, quantize_matrix(fmt, weight_fn(mat, rows, cols)), device=device)
+
+        def up(a):
+            return None if a is None else torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(device)
+
+        inv = torch.from_numpy(rope_inv_freq(head_dim if rot_dim is None else rot_dim, base)).to(device)
+        return cls(proj(Q_PROJ, n_heads * head_dim, hidden), proj(K_PROJ, n_kv_heads * head_dim, hidden),
+                   proj(V_PROJ, n_kv_heads * head_dim, hidden), proj(O_PROJ, hidden, n_heads * head_dim), n_heads,
+                   n_kv_heads, head_dim, inv, up(q_norm), up(k_norm), **kw)
+
+
+class AttentionBuffers:
+    """Device buffers for attention calls over batches of this shape
+    (n_tokens, max_q, sequences and page-table width as `batch` has them)."""
+
+    def __init__(self, attn: DeviceAttention, cache, batch, device="cuda"):
+        import torch
+
+        from . import attn_workspace_bytes, gemm_workspace_bytes, gemv_grouped_workspace_bytes
+        T, D, H = batch.n_tokens, attn.head_dim, attn.hidden
+        O = attn.n_heads * D
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        def act(k):
+            return empty(T, k, dtype=torch.int8), empty(T, k // 32), empty(T, k // 32, dtype=torch.int32)
+
+        def zeros(n):
+            return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+        self.x_act, self.o_act = act(H), act(O)
+        self.q, self.k, self.v = (empty(T, h, D) for h in (attn.n_heads, attn.n_kv_heads, attn.n_kv_heads))
+        self.q16 = empty(T, attn.n_heads, D, dtype=cache.dtype)
+        self.o, self.y = empty(T, attn.n_heads, D), empty(T, H)
+        mats = (attn.wq, attn.wk, attn.wv, attn.wo)
+        self.ws_gemm = zeros(max(gemm_workspace_bytes(W, T) for W in mats))
+        self.ws_attn = zeros(attn_workspace_bytes(cache, batch, attn.n_heads))
+        self.jobs = None
+        if T <= 4:  # decode: query, key and value projections in one launch
+            from . import gemv_jobs
+            self.jobs = gemv_jobs([(W, T, *self.x_act, y) for W, y in zip(mats, (self.q, self.k, self.v))])
+            self.ws_jobs = zeros(gemv_grouped_workspace_bytes(self.jobs))
+
+    def run(self, attn: DeviceAttention, x, cache, batch, resid=None, out=None, stream=None):
+        """Projections, norm, rotation and cache append, attention, output
+        projection for x (device fp32 [n_tokens][hidden]); y = resid +
+        Attention(x) lands in `out` (default self.y)."""
+        from . import attn as attention
+        from . import gemm, gemv_grouped, qk_norm_rope, quantize_act
+        T = batch.n_tokens
+        y = self.y if out is None else out
+        quantize_act(x, *self.x_act, stream)
+        if self.jobs is not None:
+            gemv_grouped(self.jobs, self.ws_jobs, stream)
+        else:
+            for W, o in ((attn.wq, self.q), (attn.wk, self.k), (attn.wv, self.v)):
+                gemm(W, *self.x_act, T, o, ws=self.ws_gemm, stream=stream)
+        qk_norm_rope(self.q, self.k, self.v, cache, batch, self.q16, attn.inv_freq, attn.q_norm, attn.k_norm, attn.eps,
+                     attn.interleaved, stream)
+        attention(self.q16, cache, batch, self.o, attn.scale, attn.window, attn.sinks, self.ws_attn, stream)
+        quantize_act(self.o.view(T, -1), *self.o_act, stream)
+        gemm(attn.wo, *self.o_act, T, y, resid=resid, ws=self.ws_gemm, stream=stream)
+        return y
