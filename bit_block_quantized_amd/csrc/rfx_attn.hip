@@ -229,7 +229,7 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     a.out = out;
     a.out_f32 = out_type == RFX_F32;
     a.c = scale * 1.4426950408889634f;
-    a.window = window;
+    a.window = window < 1 << 30 ? window : 1 << 30; // positions are below 2^30: differences stay in 32 bits
     a.sinks = sinks;
     a.S = p.S;
     a.row_blocks = p.row_blocks;

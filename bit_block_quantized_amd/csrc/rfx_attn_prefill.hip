@@ -32,6 +32,8 @@ constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;
 constexpr int kThreads = 64 * kWaves;
 
+constexpr int kIds = 1024;
+
 // Pitches (bytes) of the LDS rows: K rows are read 16 bytes per lane down a
 // column, so neighbours are 16 bytes apart modulo the 256 bytes of the
 // banks; four V rows are read 64 bytes at a time, so theirs are 64 apart.
@@ -52,6 +54,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     constexpr int BN = L::BN, NC = DP / 16, ND = DP / 32, NK = BN / 32;
     __shared__ __align__(16) char smem[2 * L::buf];
     __shared__ unsigned s_bad[3][2]; // keys of a tile with an unusable page id
+    __shared__ int s_ids[kIds];      // page ids of the next tiles, `ept` each
 
     const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, hl = lane >> 5, i16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -67,6 +70,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     const int seq = b / a.row_blocks;
     const int unit = (seq * a.row_blocks + rb) * kv.Hk + hk;
     const int D = kv.D;
+    const int window = a.window ? a.window : 1 << 30; // positions are below 2^30
 
     const Seq sq = load_seq(kv, seq);
     const int nrows = sq.nq * kv.G, row0 = rb * kRows;
@@ -104,47 +108,61 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
             acc[i][v] = 0.f;
     float m = -INFINITY, l = 0.f;
 
-    // staging: this thread's chunk of NL keys of a tile
+    // Page ids go through LDS, those of `ids_n` tiles from tile ids_at on, so
+    // that a tile's loads need no other global load first.
     const int32_t *table = kv.table + (size_t)seq * kv.stride;
     const int last_key = max(0, kt.hi - 1), ps = kv.page_shift, pm = (1 << ps) - 1;
-    const int skey = tid / L::CH, sch = tid % L::CH;
-    const bool ch_ok = 8 * sch < D;
-    const size_t head_stride = (size_t)D << ps;
-    u4 kx[L::NL], vx[L::NL];
-    int ids[L::NL], ids_n[L::NL];
-    const auto load_ids = [&](int t, int (&id)[L::NL]) {
-        const int key0 = tile_key<BN>(kt, min(t, t_end - 1));
-#pragma unroll
-        for (int i = 0; i < L::NL; i++)
-            id[i] = table[min(key0 + i * L::KPI + skey, last_key) >> ps];
+    const int ept = max(1, BN >> ps), ids_n = kIds / ept;
+    int ids_at = t_begin;
+    const auto fill_ids = [&](int t) {
+        for (int e = tid; e < ids_n * ept; e += kThreads) {
+            const int tt = t + e / ept;
+            if (tt < t_end)
+                s_ids[e] = table[min(tile_key<BN>(kt, tt) + ((e % ept) << ps), last_key) >> ps];
+        }
     };
-    const auto load_tile = [&](int t, const int (&id)[L::NL]) {
-        const int key0 = tile_key<BN>(kt, t);
+
+    // staging: this thread's chunk of NL keys of a tile
+    const int skey = tid / L::CH, sch = tid % L::CH;
+    const unsigned page_elems = (unsigned)kv.Hk * D << ps; // at most 2^30
+    const size_t lane_off = ((size_t)hk * D << ps) + (8 * sch < D ? 8 * sch : 0);
+    u4 kx[L::NL], vx[L::NL];
+    unsigned bad_pages; // loads whose page id is unusable
+    const auto load_tile = [&](int t) {
+        const int key0 = tile_key<BN>(kt, t), at0 = (t - ids_at) * ept;
+        bad_pages = 0;
 #pragma unroll
         for (int i = 0; i < L::NL; i++) {
-            const int key = key0 + i * L::KPI + skey;
-            const int pid = (unsigned)id[i] < (unsigned)kv.n_pages ? id[i] : 0;
-            const size_t off = ((size_t)pid * kv.Hk + hk) * head_stride + (size_t)(key & pm) * D + (ch_ok ? 8 * sch : 0);
+            const int kk = i * L::KPI + skey;
+            const int id = s_ids[at0 + (kk >> ps)];
+            const bool good = (unsigned)id < (unsigned)kv.n_pages;
+            bad_pages |= good ? 0u : 1u << i;
+            const size_t off = lane_off + (size_t)(good ? (unsigned)id : 0u) * page_elems + (unsigned)(((key0 + kk) & pm) * D);
             kx[i] = *reinterpret_cast<const u4 *>(kv.k + off);
             vx[i] = *reinterpret_cast<const u4 *>(kv.v + off);
         }
     };
-    // tile t (its loads and ids in the registers) into buffer bf; keys that
-    // no row of the workgroup sees, and elements past D, become zero: their
-    // memory may hold anything
-    const auto store_tile = [&](int t, const int (&id)[L::NL], int bf) {
+    // Tile t, in the registers, into buffer bf. Keys that no row of the
+    // workgroup sees, and elements past D, become zero: their memory may
+    // hold anything.
+    const auto store_tile = [&](int t, int bf) {
         const int key0 = tile_key<BN>(kt, t);
         char *kb = smem + bf * L::buf, *vb = kb + BN * L::KP;
+        if (key0 + BN > kt.hi || (key0 < kt.lo && key0 + BN > kt.sk) || D != DP || __any(bad_pages)) {
+#pragma unroll
+            for (int i = 0; i < L::NL; i++) {
+                const int kk = i * L::KPI + skey, key = key0 + kk;
+                const bool good = !(bad_pages >> i & 1);
+                if (!good && sch == 0)
+                    atomicOr(&s_bad[t % 3][kk >> 5], 1u << (kk & 31));
+                if (!(good & (8 * sch < D) & (key < kt.hi) & ((key >= kt.lo) | (key < kt.sk))))
+                    kx[i] = vx[i] = (u4){0, 0, 0, 0};
+            }
+        }
 #pragma unroll
         for (int i = 0; i < L::NL; i++) {
-            const int kk = i * L::KPI + skey, key = key0 + kk;
-            const bool good = (unsigned)id[i] < (unsigned)kv.n_pages;
-            const bool any = good && ch_ok && key < kt.hi && (key >= kt.lo || key < kt.sk);
-            if (!good && sch == 0)
-                atomicOr(&s_bad[t % 3][kk >> 5], 1u << (kk & 31));
-            const u4 z = {0, 0, 0, 0};
-            *reinterpret_cast<u4 *>(kb + kk * L::KP + 16 * sch) = any ? kx[i] : z;
-            *reinterpret_cast<u4 *>(vb + kk * L::VP + 16 * sch) = any ? vx[i] : z;
+            *reinterpret_cast<u4 *>(kb + (i * L::KPI + skey) * L::KP + 16 * sch) = kx[i];
+            *reinterpret_cast<u4 *>(vb + (i * L::KPI + skey) * L::VP + 16 * sch) = vx[i];
         }
     };
 
@@ -152,27 +170,28 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
         s_bad[tid >> 1][tid & 1] = 0;
     __syncthreads();
     if (t_begin < t_end) {
-        load_ids(t_begin, ids);
-        load_tile(t_begin, ids);
-        load_ids(t_begin + 1, ids_n);
-        store_tile(t_begin, ids, t_begin & 1);
+        fill_ids(t_begin);
+        __syncthreads();
+        load_tile(t_begin);
+        store_tile(t_begin, t_begin & 1);
     }
     __syncthreads();
 
     for (int t = t_begin; t < t_end; t++) {
-        const bool more = t + 1 < t_end;
-        if (more) {
-#pragma unroll
-            for (int i = 0; i < L::NL; i++)
-                ids[i] = ids_n[i];
-            load_tile(t + 1, ids);
-            load_ids(t + 2, ids_n);
+        // the next tile's loads (at the end, the last tile's again: on every
+        // path, so that nothing waits for them before they are stored)
+        const int tn = min(t + 1, t_end - 1);
+        if (tn - ids_at >= ids_n) {
+            fill_ids(tn); // every thread is past its reads of the old ids
+            ids_at = tn;
+            __syncthreads();
         }
+        load_tile(tn);
         if (tid < 2)
             s_bad[(t + 2) % 3][tid] = 0; // last read for tile t - 1
         const int key0 = tile_key<BN>(kt, t);
         const char *kb = smem + (t & 1) * L::buf, *vb = kb + BN * L::KP;
-        const bool seen = wave_on && key0 <= w_hi && (!a.window || key0 + BN - 1 > w_lo - a.window || key0 < a.sinks);
+        const bool seen = wave_on && key0 <= w_hi && (key0 + BN - 1 > w_lo - window || key0 < a.sinks);
         if (seen) {
             f32x16 s[NK];
 #pragma unroll
@@ -188,15 +207,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
                     s[k] = T::mma32(kf, qf[c], s[k]);
                 }
             const unsigned bad0 = s_bad[t % 3][0], bad1 = s_bad[t % 3][1];
-            const bool edge = key0 + BN - 1 > w_lo || (a.window && key0 <= w_hi - a.window && key0 + BN > a.sinks) || (bad0 | bad1);
+            const bool edge = key0 + BN - 1 > w_lo || (key0 <= w_hi - window && key0 + BN > a.sinks) || (bad0 | bad1);
             if (edge) {
 #pragma unroll
                 for (int k = 0; k < NK; k++)
 #pragma unroll
                     for (int v = 0; v < 16; v++) {
                         const int kk = 8 * (v >> 2) + 4 * hl + (v & 3), key = key0 + 32 * k + kk;
-                        const bool ok = key <= pos && (!a.window || key > pos - a.window || key < a.sinks) &&
-                                        !(((k ? bad1 : bad0) >> kk) & 1);
+                        const bool ok = (key <= pos) & ((key > pos - window) | (key < a.sinks)) & !(((k ? bad1 : bad0) >> kk) & 1);
                         s[k][v] = ok ? s[k][v] : -INFINITY;
                     }
             }
@@ -241,8 +259,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
                     }
                 }
         }
-        if (more)
-            store_tile(t + 1, ids, (t + 1) & 1);
+        store_tile(tn, (t + 1) & 1);
         __syncthreads();
     }
 
