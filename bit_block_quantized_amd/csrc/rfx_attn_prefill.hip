@@ -19,8 +19,9 @@
 // and a second launch joins the partials in split order.
 //
 // Rounding: weights are rounded once to the cache's type for a result of
-// that type (its own rounding is as large); for an fp32 result they are
-// carried as the sum of TERMS values. The row sums are of the fp32 weights.
+// that type (its own rounding is as large), and the row sums are of the
+// rounded ones; for an fp32 result they are carried as the sum of TERMS
+// values, and the sums are of the fp32 weights.
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -46,6 +47,12 @@ struct Tile {
     static constexpr int KPI = kThreads / CH;   // keys per load of the workgroup
     static constexpr int NL = BN / KPI;         // loads per thread, K and V each
 };
+
+__device__ __forceinline__ float max_halves(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 template <class T, int DP, int TERMS>
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kernel(AttnArgs a)
@@ -224,17 +231,18 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
                 for (int v = 0; v < 16; v++)
                     top = fmaxf(top, s[k][v]);
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float mn = fmaxf(m, top);
-            if (__any(mn > m)) {
-                const float f = m == -INFINITY ? 0.f : fast_exp2(a.c * (m - mn));
+            top = max_halves(top);
+            // Weights may grow to 2^LAG before the sums are rescaled: the
+            // largest score rises often by a little, seldom by much.
+            if (__any(a.c * (top - m) > T::LAG)) {
+                const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : fast_exp2(a.c * (m - mn));
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < ND; i++)
                     acc[i] *= f;
                 m = mn;
             }
-            const float off = mn == -INFINITY ? 0.f : T::BIAS - a.c * mn;
+            const float off = m == -INFINITY ? 0.f : T::BIAS - a.c * m;
 #pragma unroll
             for (int k = 0; k < NK; k++)
 #pragma unroll
@@ -243,10 +251,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         p[i] = fast_exp2(fmaf(a.c, s[k][8 * h + i], off));
-                        l += p[i];
+                        if (TERMS > 1)
+                            l += p[i];
                     }
                     u4 pt[TERMS];
                     split_terms<T, TERMS>(p, pt);
+                    if (TERMS == 1) // the sum of the weights as they are used
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            l = T::add_pair(pt[0][i], l);
                     // values of keys 32 k + 16 h + 4 hl + 0..3 and + 8..11
                     const char *vr = vb + (32 * k + 16 * h + 4 * hl + (i16 >> 2)) * L::VP + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
 #pragma unroll

@@ -90,11 +90,17 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 // The two 16-bit element types. TERMS: how many of them carry a softmax
 // weight where the result is fp32 (fp16 11 + 11 bits, bf16 8 + 8 + 8: about
 // fp32's 24). BIAS: power of two that weights are scaled by, so that the
-// small ones stay clear of fp16's subnormals (2^14 p <= 16384; it cancels in
-// the division by the sum); bf16 has fp32's exponents.
+// small ones stay clear of fp16's subnormals (it cancels in the division by
+// the sum); bf16 has fp32's exponents. LAG: power of two that weights may
+// grow beyond the running maximum's before sums are rescaled (2^(BIAS + LAG)
+// stays below fp16's largest value).
 struct F16 {
     static constexpr int TERMS = 2;
-    static constexpr float BIAS = 14.0f;
+    static constexpr float BIAS = 10.0f, LAG = 5.0f;
+    static __device__ __forceinline__ float add_pair(uint32_t u, float x)
+    {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(h2, u), (h2){(_Float16)1.0f, (_Float16)1.0f}, x, false);
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b)
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, h2));
@@ -115,7 +121,11 @@ struct F16 {
 
 struct BF16 {
     static constexpr int TERMS = 3;
-    static constexpr float BIAS = 0.0f;
+    static constexpr float BIAS = 0.0f, LAG = 8.0f;
+    static __device__ __forceinline__ float add_pair(uint32_t u, float x)
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, u), (b2){(__bf16)1.0f, (__bf16)1.0f}, x, false);
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b)
     {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
@@ -165,6 +175,14 @@ __device__ __forceinline__ u2 lds_read_tr(const char *p)
     typedef short s4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4 *lptr;
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uint32_t)(uintptr_t)p));
+}
+
+// A direct load into LDS: lane l's 16 bytes land at dst + 16 l.
+__device__ __forceinline__ void lds_load16(const void *src, void *dst)
+{
+    typedef const __attribute__((address_space(1))) void *gptr;
+    typedef __attribute__((address_space(3))) void *lptr;
+    __builtin_amdgcn_global_load_lds((gptr)(uintptr_t)src, (lptr)(uint32_t)(uintptr_t)dst, 16, 0, 0);
 }
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
