@@ -182,10 +182,33 @@ def _dptr(t):
     return t.data_ptr()
 
 
+class _Torch:
+    """torch's types and calls that the binding uses on every call, looked up
+    once (importing this package does not import torch)."""
+    f32 = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.f64, cls.i32 = torch.float64, torch.int32
+        cls.elem = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        cls.current_device, cls.device_guard = torch.cuda.current_device, torch.cuda.device
+        # the handle itself, without a Stream object around it, where torch has that
+        cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        cls.f32 = torch.float32
+
+
+def _torch():
+    if _Torch.f32 is None:
+        _Torch.load()
+    return _Torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        t = _torch()
+        return t.raw_stream(t.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -425,39 +448,32 @@ def moe_debug_prefill(layer, q, k, xq, xs, topk_w, pairs_sorted, expert_off, ws,
 
 def _elem(dtype):
     """RFX_F32 / RFX_F16 / RFX_BF16 of a torch dtype."""
-    name = str(dtype)
-    if name not in _ELEM:
+    e = _torch().elem.get(dtype)
+    if e is None:
         raise ValueError(f"element type {dtype}: float32, float16 or bfloat16")
-    return _ELEM[name]
+    return e
 
 
-_ELEM = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16}
-
-
-def _want(t, name, dtype, shape, device=None):
-    """A contiguous device tensor of this dtype and shape (None entries of
-    the shape: any size)."""
-    if str(t.dtype) != dtype:
-        raise ValueError(f"{name}: {t.dtype}, {dtype} wanted")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} wanted")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
-    return t.data_ptr()
+def _want(t, name, dtype, shape, device):
+    """Address of a contiguous tensor of this dtype and shape (a tuple) on
+    this device."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, {dtype} {tuple(shape)} wanted")
+    raise ValueError(f"{name}: not contiguous" if not t.is_contiguous() else f"{name}: on {t.device}, not {device}")
 
 
 def _call_on(device, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current; the stream
     defaults to that device's current one."""
-    import torch
     if device.type != "cuda":
         raise ValueError(f"tensors on {device}: the kernels need GPU memory")
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
+    t, index = _torch(), device.index
+    if t.current_device() != index:
+        with t.device_guard(device):
             return _check(fn(*args, _stream(stream)))
-    return _check(fn(*args, _stream(stream)))
+    return _check(fn(*args, t.raw_stream(index) if stream is None else _stream(stream)))
 
 
 class DeviceKVCache:
@@ -466,15 +482,13 @@ class DeviceKVCache:
 
     def __init__(self, k, v):
         n_pages, n_kv_heads, page_size, head_dim = k.shape
-        if str(k.dtype) == "torch.float32":
+        if _elem(k.dtype) == F32:
             raise ValueError("the cache is float16 or bfloat16")
         self.k, self.v = k, v
         self.dtype, self.device = k.dtype, k.device
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, n_kv_heads, page_size, head_dim
-        self._dtype = str(k.dtype)
         self.c = KVCacheC(_elem(k.dtype), n_kv_heads, head_dim, page_size, n_pages, 0,
-                          _want(k, "k", self._dtype, tuple(k.shape)),
-                          _want(v, "v", self._dtype, tuple(k.shape), k.device))
+                          _want(k, "k", k.dtype, k.shape, k.device), _want(v, "v", k.dtype, k.shape, k.device))
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -497,11 +511,11 @@ class KVBatch:
         n_seq, stride = page_table.shape
         self.q_off, self.kv_len, self.page_table = q_off, kv_len, page_table
         self.n_seq, self.n_tokens, self.max_q = n_seq, n_tokens, max_q
-        dev = page_table.device
-        self.device = dev
-        self.c = KVBatchC(n_seq, n_tokens, max_q, stride, _want(q_off, "q_off", "torch.int32", (n_seq + 1,), dev),
-                          _want(kv_len, "kv_len", "torch.int32", (n_seq,), dev),
-                          _want(page_table, "page_table", "torch.int32", (n_seq, stride)))
+        self.device = dev = page_table.device
+        i32 = _torch().i32
+        self.c = KVBatchC(n_seq, n_tokens, max_q, stride, _want(q_off, "q_off", i32, (n_seq + 1,), dev),
+                          _want(kv_len, "kv_len", i32, (n_seq,), dev),
+                          _want(page_table, "page_table", i32, (n_seq, stride), dev))
 
     def ref(self):
         return ctypes.byref(self.c)
@@ -513,17 +527,17 @@ def rope_inv_freq(rot_dim, base=10000.0):
     return np.float64(base) ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
 
 
-def _head_rows(t, name, n_tokens, heads, dim, device):
-    """Pointer and row stride of fp32 [n_tokens][heads][dim]; rows may be
+def _head_rows(t, name, shape, device):
+    """Address and row stride of float32 [n_tokens][heads][dim]; rows may be
     part of longer ones (a fused projection's output)."""
-    if str(t.dtype) != "torch.float32" or tuple(t.shape) != (n_tokens, heads, dim):
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, float32 {(n_tokens, heads, dim)} wanted")
-    st = t.stride()
-    if (dim > 1 and st[2] != 1) or (heads > 1 and st[1] != dim):
-        raise ValueError(f"{name}: heads of a row are not contiguous (strides {st})")
+    row, head, one = t.stride()
+    if t.dtype is not _Torch.f32 or t.shape != shape:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, float32 {shape} wanted")
+    if one != 1 or (head != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: heads of a row are not contiguous (strides {t.stride()})")
     if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
-    return t.data_ptr(), st[0] if n_tokens > 1 else heads * dim
+        raise ValueError(f"{name}: on {t.device}, not {device}")
+    return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
 
 
 def qk_norm_rope(q, k, v, cache: DeviceKVCache, batch: KVBatch, q_out, inv_freq, q_weight=None, k_weight=None,
@@ -532,19 +546,20 @@ def qk_norm_rope(q, k, v, cache: DeviceKVCache, batch: KVBatch, q_out, inv_freq,
     keys and values appended to the cache. q, k, v: float32 [n_tokens][heads]
     [head_dim], rows may be strided; inv_freq: float64 device tensor
     [rot_dim / 2] (see rope_inv_freq); weights float32 [head_dim] or None."""
-    T, D, dev = batch.n_tokens, cache.head_dim, cache.device
+    T, D, Hk, dev = batch.n_tokens, cache.head_dim, cache.n_kv_heads, cache.device
     Hq = q.shape[1]
-    qp, qs = _head_rows(q, "q", T, Hq, D, dev)
-    kp, ks = _head_rows(k, "k", T, cache.n_kv_heads, D, dev)
-    vp, vs = _head_rows(v, "v", T, cache.n_kv_heads, D, dev)
+    qp, qs = _head_rows(q, "q", (T, Hq, D), dev)
+    kp, ks = _head_rows(k, "k", (T, Hk, D), dev)
+    vp, vs = _head_rows(v, "v", (T, Hk, D), dev)
     if batch.device != dev:
         raise ValueError(f"batch on {batch.device}, the cache is on {dev}")
-    args = QkRopeC(qp, kp, vp, qs, ks, vs, _want(inv_freq, "inv_freq", "torch.float64", (None,), dev),
-                   None if q_weight is None else _want(q_weight, "q_weight", "torch.float32", (D,), dev),
-                   None if k_weight is None else _want(k_weight, "k_weight", "torch.float32", (D,), dev),
-                   eps, Hq, 2 * inv_freq.shape[0], int(interleaved))
+    half = inv_freq.shape[0]
+    args = QkRopeC(qp, kp, vp, qs, ks, vs, _want(inv_freq, "inv_freq", _Torch.f64, (half,), dev),
+                   None if q_weight is None else _want(q_weight, "q_weight", _Torch.f32, (D,), dev),
+                   None if k_weight is None else _want(k_weight, "k_weight", _Torch.f32, (D,), dev),
+                   eps, Hq, 2 * half, interleaved)
     _call_on(dev, stream, lib().rfx_qk_norm_rope, ctypes.byref(args), cache.ref(), batch.ref(),
-             _want(q_out, "q_out", cache._dtype, (T, Hq, D), dev))
+             _want(q_out, "q_out", cache.dtype, (T, Hq, D), dev))
 
 
 def attn_workspace_bytes(cache: DeviceKVCache, batch: KVBatch, n_heads: int) -> int:
@@ -556,17 +571,18 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
     [n_tokens][n_heads][head_dim] in the cache's type, out the same shape in
     that type or float32; window > 0: only the last `window` keys and the
     first `sinks`."""
-    T, D, dev = batch.n_tokens, cache.head_dim, cache.device
+    dev = cache.device
     Hq = q.shape[1]
-    qp = _want(q, "q", cache._dtype, (T, Hq, D), dev)
-    op = _want(out, "out", str(out.dtype), (T, Hq, D), dev)
+    shape = (batch.n_tokens, Hq, cache.head_dim)
+    qp = _want(q, "q", cache.dtype, shape, dev)
+    op = _want(out, "out", out.dtype, shape, dev)
     if batch.device != dev:
         raise ValueError(f"batch on {batch.device}, the cache is on {dev}")
     wp, wn = None, 0
     if ws is not None:
         if ws.device != dev:
-            raise ValueError(f"ws: on {ws.device}, the cache is on {dev}")
-        wp, wn = ws.data_ptr(), ws.numel() * ws.element_size()
+            raise ValueError(f"ws: on {ws.device}, not {dev}")
+        wp, wn = ws.data_ptr(), ws.nbytes
     _call_on(dev, stream, lib().rfx_attn, qp, cache.ref(), batch.ref(), Hq, scale, window, sinks, op, _elem(out.dtype),
              wp, wn)
 
