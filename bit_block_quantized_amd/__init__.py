@@ -454,24 +454,24 @@ def _elem(dtype):
     return e
 
 
-def _want(t, name, dtype, shape, device):
+def _want(t, name, dtype, shape, index):
     """Address of a contiguous tensor of this dtype and shape (a tuple) on
-    this device."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+    the device of this index (-1: host memory)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
         return t.data_ptr()
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, {dtype} {tuple(shape)} wanted")
-    raise ValueError(f"{name}: not contiguous" if not t.is_contiguous() else f"{name}: on {t.device}, not {device}")
+    raise ValueError(f"{name}: not contiguous" if not t.is_contiguous() else f"{name}: on {t.device}, not GPU {index}")
 
 
-def _call_on(device, stream, fn, *args):
+def _call_on(index, stream, fn, *args):
     """fn(*args, stream) with the tensors' device current; the stream
     defaults to that device's current one."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors on {device}: the kernels need GPU memory")
-    t, index = _torch(), device.index
+    if index < 0:
+        raise ValueError("tensors in host memory: the kernels need GPU memory")
+    t = _torch()
     if t.current_device() != index:
-        with t.device_guard(device):
+        with t.device_guard(index):
             return _check(fn(*args, _stream(stream)))
     return _check(fn(*args, t.raw_stream(index) if stream is None else _stream(stream)))
 
@@ -485,10 +485,10 @@ class DeviceKVCache:
         if _elem(k.dtype) == F32:
             raise ValueError("the cache is float16 or bfloat16")
         self.k, self.v = k, v
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, n_kv_heads, page_size, head_dim
         self.c = KVCacheC(_elem(k.dtype), n_kv_heads, head_dim, page_size, n_pages, 0,
-                          _want(k, "k", k.dtype, k.shape, k.device), _want(v, "v", k.dtype, k.shape, k.device))
+                          _want(k, "k", k.dtype, k.shape, self.index), _want(v, "v", k.dtype, k.shape, self.index))
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -511,7 +511,7 @@ class KVBatch:
         n_seq, stride = page_table.shape
         self.q_off, self.kv_len, self.page_table = q_off, kv_len, page_table
         self.n_seq, self.n_tokens, self.max_q = n_seq, n_tokens, max_q
-        self.device = dev = page_table.device
+        self.index = dev = page_table.get_device()
         i32 = _torch().i32
         self.c = KVBatchC(n_seq, n_tokens, max_q, stride, _want(q_off, "q_off", i32, (n_seq + 1,), dev),
                           _want(kv_len, "kv_len", i32, (n_seq,), dev),
@@ -527,7 +527,7 @@ def rope_inv_freq(rot_dim, base=10000.0):
     return np.float64(base) ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
 
 
-def _head_rows(t, name, shape, device):
+def _head_rows(t, name, shape, index):
     """Address and row stride of float32 [n_tokens][heads][dim]; rows may be
     part of longer ones (a fused projection's output)."""
     row, head, one = t.stride()
@@ -535,8 +535,8 @@ def _head_rows(t, name, shape, device):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, float32 {shape} wanted")
     if one != 1 or (head != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: heads of a row are not contiguous (strides {t.stride()})")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, not GPU {index}")
     return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
 
 
@@ -546,13 +546,13 @@ def qk_norm_rope(q, k, v, cache: DeviceKVCache, batch: KVBatch, q_out, inv_freq,
     keys and values appended to the cache. q, k, v: float32 [n_tokens][heads]
     [head_dim], rows may be strided; inv_freq: float64 device tensor
     [rot_dim / 2] (see rope_inv_freq); weights float32 [head_dim] or None."""
-    T, D, Hk, dev = batch.n_tokens, cache.head_dim, cache.n_kv_heads, cache.device
+    T, D, Hk, dev = batch.n_tokens, cache.head_dim, cache.n_kv_heads, cache.index
     Hq = q.shape[1]
     qp, qs = _head_rows(q, "q", (T, Hq, D), dev)
     kp, ks = _head_rows(k, "k", (T, Hk, D), dev)
     vp, vs = _head_rows(v, "v", (T, Hk, D), dev)
-    if batch.device != dev:
-        raise ValueError(f"batch on {batch.device}, the cache is on {dev}")
+    if batch.index != dev:
+        raise ValueError(f"batch on GPU {batch.index}, the cache is on GPU {dev}")
     half = inv_freq.shape[0]
     args = QkRopeC(qp, kp, vp, qs, ks, vs, _want(inv_freq, "inv_freq", _Torch.f64, (half,), dev),
                    None if q_weight is None else _want(q_weight, "q_weight", _Torch.f32, (D,), dev),
@@ -571,17 +571,17 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
     [n_tokens][n_heads][head_dim] in the cache's type, out the same shape in
     that type or float32; window > 0: only the last `window` keys and the
     first `sinks`."""
-    dev = cache.device
+    dev = cache.index
     Hq = q.shape[1]
     shape = (batch.n_tokens, Hq, cache.head_dim)
     qp = _want(q, "q", cache.dtype, shape, dev)
     op = _want(out, "out", out.dtype, shape, dev)
-    if batch.device != dev:
-        raise ValueError(f"batch on {batch.device}, the cache is on {dev}")
+    if batch.index != dev:
+        raise ValueError(f"batch on GPU {batch.index}, the cache is on GPU {dev}")
     wp, wn = None, 0
     if ws is not None:
-        if ws.device != dev:
-            raise ValueError(f"ws: on {ws.device}, not {dev}")
+        if ws.get_device() != dev:
+            raise ValueError(f"ws: on {ws.device}, not GPU {dev}")
         wp, wn = ws.data_ptr(), ws.nbytes
     _call_on(dev, stream, lib().rfx_attn, qp, cache.ref(), batch.ref(), Hq, scale, window, sinks, op, _elem(out.dtype),
              wp, wn)

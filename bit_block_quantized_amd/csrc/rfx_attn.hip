@@ -58,14 +58,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
     typedef float fp __attribute__((ext_vector_type(PER)));
     const KvArgs &kv = a.kv;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int unit = blockIdx.x / (a.rows / 4), r = blockIdx.x % (a.rows / 4) * 4 + wave;
-    const int hk = unit % kv.Hk, rb = unit / kv.Hk % a.row_blocks, seq = unit / kv.Hk / a.row_blocks;
+    const int quads = a.rows / 4, unit = blockIdx.x >> __builtin_ctz(quads), r = (blockIdx.x & (quads - 1)) * 4 + wave;
+    const int u = kv.div_hk(unit), hk = kv.div_hk.rem(unit, u), seq = a.div_rb(u), rb = a.div_rb.rem(u, seq);
     const Seq sq = load_seq(kv, seq);
     const int nrows = sq.nq * kv.G, row0 = rb * a.rows, row = row0 + r;
     if (row >= nrows)
         return;
     const int row_end = min(nrows, row0 + a.rows);
-    const KeyTiles kt = key_tiles(a.bn, sq.p0 + row0 / kv.G, sq.p0 + (row_end - 1) / kv.G, sq.kv, a.window, a.sinks);
+    const KeyTiles kt = key_tiles(a.bn, sq.p0 + kv.div_g(row0), sq.p0 + kv.div_g(row_end - 1), sq.kv, a.window, a.sinks);
     int per, active;
     split_tiles(a, kt.n, per, active);
     if (active == 1)
@@ -106,7 +106,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
     if (d >= kv.D)
         return;
     const float inv = l > 0.f ? 1.0f / l : 0.f;
-    const size_t at = ((size_t)(sq.t0 + row / kv.G) * kv.Hq + hk * kv.G + row % kv.G) * kv.D + d;
+    const int tok = kv.div_g(row);
+    const size_t at = ((size_t)(sq.t0 + tok) * kv.Hq + hk * kv.G + kv.div_g.rem(row, tok)) * kv.D + d;
     if (a.out_f32) {
         *reinterpret_cast<fp *>(static_cast<float *>(a.out) + at) = sum * inv;
     } else {
@@ -236,6 +237,9 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     a.rows = p.rows;
     a.bn = p.bn;
     a.min_tiles = p.min_tiles;
+    a.div_s = Div(p.S);
+    a.div_rb = Div(p.row_blocks);
+    a.div_mt = Div(p.min_tiles);
     if (p.S > 1) {
         a.part = static_cast<float *>(ws);
         a.stat = reinterpret_cast<float *>(static_cast<char *>(ws) + p.part);

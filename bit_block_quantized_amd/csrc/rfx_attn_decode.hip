@@ -54,14 +54,15 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const KvArgs &kv = a.kv;
-    const int split = blockIdx.x % a.S, unit = blockIdx.x / a.S, hk = unit % kv.Hk, seq = unit / kv.Hk;
+    const int unit = a.div_s(blockIdx.x), split = a.div_s.rem(blockIdx.x, unit);
+    const int seq = kv.div_hk(unit), hk = kv.div_hk.rem(unit, seq);
     const int D = kv.D;
 
     const Seq sq = load_seq(kv, seq);
     const int nrows = min(sq.nq * kv.G, NR * 16);
     if (nrows <= 0)
         return;
-    const int p_lo = sq.p0, p_hi = sq.p0 + (nrows - 1) / kv.G;
+    const int p_lo = sq.p0, p_hi = sq.p0 + kv.div_g(nrows - 1);
     const KeyTiles kt = key_tiles(BN, p_lo, p_hi, sq.kv, a.window, a.sinks);
     int per, active;
     split_tiles(a, kt.n, per, active);
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     int pos[NR];
 #pragma unroll
     for (int n = 0; n < NR; n++) {
-        const int row = 16 * n + r16, rr = min(row, nrows - 1), tok = rr / kv.G, head = hk * kv.G + rr % kv.G;
+        const int row = 16 * n + r16, rr = min(row, nrows - 1), tok = kv.div_g(rr), head = hk * kv.G + kv.div_g.rem(rr, tok);
         pos[n] = sq.p0 + tok;
         const uint16_t *qp = a.q + ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
 #pragma unroll
@@ -153,7 +154,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
             const int id = BIG ? ids : __shfl(ids, key, 64);
             const uint16_t *p = kv.v + ((size_t)(usable(id) ? id : 0) * kv.Hk + hk) * head_stride +
                                 (size_t)((key0 + key) & pm) * D;
-            vf[i] = *reinterpret_cast<const u4 *>(p + vch);
+            // read once: not kept in the caches (the keys are, whose lines two
+            // loads share): 301 to 277 us on a 1.6 GB cache
+            vf[i] = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p + vch));
         }
     };
 
@@ -327,7 +330,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         if (row >= nrows)
             continue;
         const float inv = rl > 0.f ? 1.0f / rl : 0.f; // a row that sees nothing is zero
-        const size_t at = ((size_t)(sq.t0 + row / kv.G) * kv.Hq + hk * kv.G + row % kv.G) * D;
+        const int tok = kv.div_g(row);
+        const size_t at = ((size_t)(sq.t0 + tok) * kv.Hq + hk * kv.G + kv.div_g.rem(row, tok)) * D;
         for (int d = 4 * (threadIdx.x & 15); d < D; d += 64) {
             f32x4 o = *reinterpret_cast<const f32x4 *>(o_lds + r * OP + d);
 #pragma unroll

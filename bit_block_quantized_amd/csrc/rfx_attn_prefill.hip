@@ -68,13 +68,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     const KvArgs &kv = a.kv;
     // kv heads vary fastest: workgroups go round the XCDs in order, so with
     // eight kv heads each XCD's L2 holds one head's keys and values
-    int b = blockIdx.x;
-    const int hk = b % kv.Hk;
-    b /= kv.Hk;
-    const int split = b % a.S;
-    b /= a.S;
-    const int rb = a.row_blocks - 1 - b % a.row_blocks; // the longest first
-    const int seq = b / a.row_blocks;
+    const int b = kv.div_hk(blockIdx.x);
+    const int hk = kv.div_hk.rem(blockIdx.x, b);
+    const int us = a.div_s(b), split = a.div_s.rem(b, us);
+    const int seq = a.div_rb(us), rb = a.row_blocks - 1 - a.div_rb.rem(us, seq); // the longest first
     const int unit = (seq * a.row_blocks + rb) * kv.Hk + hk;
     const int D = kv.D;
     const int window = a.window ? a.window : 1 << 30; // positions are below 2^30
@@ -84,7 +81,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     if (row0 >= nrows)
         return;
     const int row_end = min(nrows, row0 + kRows);
-    const KeyTiles kt = key_tiles(BN, sq.p0 + row0 / kv.G, sq.p0 + (row_end - 1) / kv.G, sq.kv, a.window, a.sinks);
+    const KeyTiles kt = key_tiles(BN, sq.p0 + kv.div_g(row0), sq.p0 + kv.div_g(row_end - 1), sq.kv, a.window, a.sinks);
     int per, active;
     split_tiles(a, kt.n, per, active);
     if (split >= active)
@@ -94,10 +91,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     // the wave's rows
     const int wrow = row0 + 32 * wave;
     const bool wave_on = wrow < nrows;
-    const int row = min(wrow + r32, nrows - 1), tok = row / kv.G, head = hk * kv.G + row % kv.G;
+    const int row = min(wrow + r32, nrows - 1), tok = kv.div_g(row), head = hk * kv.G + kv.div_g.rem(row, tok);
     const bool row_ok = wrow + r32 < nrows;
     const int pos = sq.p0 + tok;
-    const int w_lo = sq.p0 + min(wrow, nrows - 1) / kv.G, w_hi = sq.p0 + min(wrow + 31, nrows - 1) / kv.G;
+    const int w_lo = sq.p0 + kv.div_g(min(wrow, nrows - 1)), w_hi = sq.p0 + kv.div_g(min(wrow + 31, nrows - 1));
     const size_t at = ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
     u4 qf[NC];
 #pragma unroll
@@ -242,6 +239,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
                     acc[i] *= f;
                 m = mn;
             }
+            __builtin_amdgcn_s_setprio(1); // the other wave of the SIMD waits rather than this one: 587 to 572 us
             const float off = m == -INFINITY ? 0.f : T::BIAS - a.c * m;
 #pragma unroll
             for (int k = 0; k < NK; k++)
@@ -272,6 +270,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
                     }
                 }
         }
+        __builtin_amdgcn_s_setprio(0);
         store_tile(tn, (t + 1) & 1);
         __syncthreads();
     }

@@ -23,6 +23,20 @@ constexpr int kMaxTokens = 1 << 23; // a launch of one 256-thread workgroup per 
 int check_kv(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads, const char *who);
 
 
+// Division of 0 <= n < 2^31 by a number known at launch, as a multiplication
+// (the compiler's sequence for an unknown divisor is some 30 operations, and
+// the kernels' setup has several in a row).
+struct Div {
+    uint32_t d, mul, shift;
+    Div() = default;
+    explicit Div(uint32_t v) : d(v), shift(v > 1 ? 32 - __builtin_clz(v - 1) : 0)
+    {
+        mul = (uint32_t)((((1ull << shift) - v) << 32) / v + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+    __device__ __forceinline__ int rem(int n, int q) const { return n - q * (int)d; }
+};
+
 // Cache and batch as the kernels take them.
 struct KvArgs {
     uint16_t *k, *v; // [n_pages][Hk][page][D]
@@ -30,6 +44,7 @@ struct KvArgs {
     int n_seq, n_tokens, max_q, stride;
     int n_pages, page_shift;
     int Hq, Hk, G, D;
+    Div div_g, div_hk; // by G and Hk
 };
 
 inline KvArgs kv_args(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
@@ -50,6 +65,8 @@ inline KvArgs kv_args(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
     a.Hk = C->n_kv_heads;
     a.G = n_heads / C->n_kv_heads;
     a.D = C->head_dim;
+    a.div_g = Div(a.G);
+    a.div_hk = Div(a.Hk);
     return a;
 }
 
@@ -66,6 +83,7 @@ struct AttnArgs {
     int rows;          // rows of a block
     int bn;            // keys of a tile
     int min_tiles;     // key tiles a split takes at least
+    Div div_s, div_rb, div_mt; // by S, row_blocks and min_tiles
     // workspace, where S > 1, by unit = (seq * row_blocks + block) * Hk + hk:
     float *part;       // [unit][split][rows][DP] unnormalized results
     float *stat;       // [unit][split][rows][2] their maxima and sums
@@ -234,8 +252,14 @@ __device__ __forceinline__ KeyTiles key_tiles(int bn, int p_lo, int p_hi, int kv
 // grid's S splits (one, with no tiles, for a block that sees no key).
 __device__ __forceinline__ void split_tiles(const AttnArgs &a, int n, int &per, int &active)
 {
-    per = max(a.min_tiles, (n + a.S - 1) / a.S);
-    active = max(1, (n + per - 1) / per);
+    per = a.div_s(n + a.S - 1);
+    if (per >= a.min_tiles) {
+        // S splits, or fewer by rounding: per is not known at launch
+        active = max(1, (n + per - 1) / per);
+    } else {
+        per = a.min_tiles;
+        active = max(1, a.div_mt(n + per - 1));
+    }
 }
 
 // First key of the i-th tile.
