@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int BN = 32;                  // keys per wave and tile
+constexpr int kWaitVmcnt0 = 0x0F70;     // s_waitcnt vmcnt(0)
 
 // LDS bytes: each wave's V piece, reused for the waves' join
 // ([wave][16 rows][DP + 4] floats).
@@ -57,6 +58,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     const int unit = a.div_s(blockIdx.x), split = a.div_s.rem(blockIdx.x, unit);
     const int seq = kv.div_hk(unit), hk = kv.div_hk.rem(unit, seq);
     const int D = kv.D;
+    const int window = a.window ? a.window : 1 << 30; // positions are below 2^30
 
     const Seq sq = load_seq(kv, seq);
     const int nrows = min(sq.nq * kv.G, NR * 16);
@@ -179,10 +181,16 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         const int tn = t + kWaves < t_end ? t + kWaves : t; // the next tile, or this one again
         const int key_n = tile_key<BN>(kt, tn);
         const int cur_ids = cur;
+        int nn = 0; // small pages: the ids after next, ahead of the loads they must not wait for
+        if constexpr (!BIG)
+            nn = ids_small(min(t + 2 * kWaves, t_end - 1));
         if constexpr (BIG) {
             if ((tn - ids_at) / kWaves >= 64) {
                 ids = ids_big(tn);
                 ids_at = tn;
+                // waited for here, or the compiler waits for every load of
+                // the loop wherever it reads an id
+                __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
             }
             nxt = __builtin_amdgcn_readlane(ids, (tn - ids_at) / kWaves);
         }
@@ -212,18 +220,17 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         // a tile that some row sees only in part, or whose page ids are not
         // all good (in the small-page case every tile is checked for that)
         const bool page_bad = BIG ? !usable(cur_ids) : __ballot(!usable(cur_ids)) != 0;
-        const bool edge = key0 + BN - 1 > p_lo || key0 + BN > kt.hi ||
-                          (a.window && key0 <= p_hi - a.window && key0 + BN > a.sinks) || page_bad;
-        if (edge) {
+        const bool edge = (key0 + BN - 1 > p_lo) | (key0 + BN > kt.hi) | ((key0 <= p_hi - window) & (key0 + BN > a.sinks)) | page_bad;
+        if (edge) { // no branches inside: the compiler's waits for the loads in flight would cover all of them
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int v = 0; v < 4; v++) {
-                    const int key = key0 + 8 * g4 + 4 * j + v;
-                    const bool good = usable(BIG ? cur_ids : __shfl(cur_ids, 8 * g4 + 4 * j + v, 64)) && key < kt.hi;
+                    const int kk = 8 * g4 + 4 * j + v, key = key0 + kk;
+                    const bool good = usable(BIG ? cur_ids : __shfl(cur_ids, kk, 64)) & (key < kt.hi);
 #pragma unroll
                     for (int n = 0; n < NR; n++) {
-                        const bool seen = good && key <= pos[n] && (!a.window || key > pos[n] - a.window || key < a.sinks);
+                        const bool seen = good & (key <= pos[n]) & ((key > pos[n] - window) | (key < a.sinks));
                         s[n][j][v] = seen ? s[n][j][v] : -INFINITY;
                     }
                 }
@@ -231,10 +238,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int kk = row_key(i * RPI + vrow), key = key0 + kk;
-                const bool any = usable(BIG ? cur_ids : __shfl(cur_ids, kk, 64)) && key < kt.hi &&
-                                 (key >= kt.lo || key < kt.sk);
-                if (!any)
-                    vf[i] = (u4){0, 0, 0, 0};
+                const bool any = usable(BIG ? cur_ids : __shfl(cur_ids, kk, 64)) & (key < kt.hi) & ((key >= kt.lo) | (key < kt.sk));
+                const uint32_t keep = any ? ~0u : 0u;
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    vf[i][e] &= keep;
             }
         }
 
@@ -289,7 +297,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         __builtin_amdgcn_wave_barrier();
         cur = nxt;
         if constexpr (!BIG)
-            nxt = ids_small(min(t + 2 * kWaves, t_end - 1));
+            nxt = nn;
     }
 
     // the waves' sums joined in wave order
