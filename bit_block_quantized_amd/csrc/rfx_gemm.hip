@@ -48,6 +48,7 @@ struct GemmArgs {
     float *y;            // [q][N]
     float *part;         // [split][q][N4] where splits > 1
     int N4;
+    bool vec;            // y and resid rows are 16-byte aligned
     EpiArgs epi;
 };
 
@@ -160,6 +161,34 @@ __device__ __forceinline__ void gemm_half(const WHalf<F> (&w)[M], const char *fr
     }
 }
 
+// Four rows of one column, bias added, to y.
+__device__ __forceinline__ void finish_rows(const GemmArgs &a, f32x4 z, int col, int row, int left, bool quad)
+{
+    const size_t at = (size_t)col * a.N + row;
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+    if (a.epi.resid) {
+        if (quad) {
+            r = *reinterpret_cast<const f32x4 *>(a.epi.resid + at);
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; v++)
+                if (v < left)
+                    r[v] = a.epi.resid[at + v];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; v++)
+        z[v] = activate(z[v], a.epi.act) + r[v];
+    if (quad) {
+        *reinterpret_cast<f32x4 *>(a.y + at) = z;
+    } else {
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+            if (v < left)
+                a.y[at + v] = z[v];
+    }
+}
+
 template <int F, int NT>
 __global__ __launch_bounds__(kThreads, NT == 4 ? 4 : 2) void gemm_kernel(GemmArgs a)
 {
@@ -181,7 +210,6 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 4 : 2) void gemm_kernel(GemmArg
     const int s_begin = a.S * sp / a.splits, s_end = a.S * (sp + 1) / a.splits;
 
     const int row0 = rb * kRows + 16 * M * wave;
-    const bool rows_ok = row0 < a.N;
     const uint8_t *tb[M];
     int rin[M];
 #pragma unroll
@@ -232,25 +260,42 @@ __global__ __launch_bounds__(kThreads, NT == 4 ? 4 : 2) void gemm_kernel(GemmArg
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
     }
-    if (!rows_ok)
-        return;
+    // The block's results through LDS ([column][row], the loop's buffers; the
+    // pitch puts the four column groups of a store on different banks), so
+    // that bias, residual and result are read and written four rows a lane,
+    // whole lines at a time.
+    constexpr int OP = kRows + 4;
+    static_assert(COLS * OP * 4 <= 2 * (kFrag + kSx), "results fit the loop's buffers");
+    float *o = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int m = 0; m < M; m++) {
-        const int row = row0 + 16 * m + (lane & 15);
-        if (row >= a.N)
-            continue;
+    for (int m = 0; m < M; m++)
 #pragma unroll
         for (int tt = 0; tt < NT; tt++)
 #pragma unroll
-            for (int v = 0; v < 4; v++) {
-                const int col = cb * COLS + 16 * tt + 4 * g + v;
-                if (col >= a.q)
-                    continue;
-                if (a.splits == 1)
-                    a.y[(size_t)col * a.N + row] = finish(a.epi, acc[m][tt][v], col, row, a.N);
-                else
-                    a.part[((size_t)sp * a.q + col) * a.N4 + row] = acc[m][tt][v];
-            }
+            for (int v = 0; v < 4; v++)
+                o[(16 * tt + 4 * g + v) * OP + 16 * M * wave + 16 * m + (lane & 15)] = acc[m][tt][v];
+    __syncthreads();
+    // wave w takes columns w, w + 8, ...; lane l rows 4 l .. + 3
+    const int row = rb * kRows + 4 * lane, left = a.N - row;
+    if (left <= 0)
+        return;
+    const int c_end = min(COLS, a.q - cb * COLS);
+    if (a.splits > 1) {
+        for (int c = wave; c < c_end; c += kWaves) // rows up to N4 exist
+            *reinterpret_cast<f32x4 *>(a.part + ((size_t)sp * a.q + cb * COLS + c) * a.N4 + row) =
+                *reinterpret_cast<const f32x4 *>(o + c * OP + 4 * lane);
+        return;
+    }
+    const bool quad = left >= 4 && a.vec; // four rows at a time, 16-byte aligned
+    f32x4 bias = {0.f, 0.f, 0.f, 0.f};
+    if (a.epi.bias)
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+            bias[v] = a.epi.bias[min(row + v, a.N - 1)];
+#pragma unroll 4
+    for (int c = wave; c < c_end; c += kWaves) {
+        const f32x4 z = *reinterpret_cast<const f32x4 *>(o + c * OP + 4 * lane) + bias;
+        finish_rows(a, z, cb * COLS + c, row, left, quad);
     }
 }
 
@@ -268,10 +313,12 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs a)
 #pragma unroll 4
     for (int s = 1; s < a.splits; s++)
         sum += *reinterpret_cast<const f32x4 *>(p + s * stride);
+    if (a.epi.bias)
 #pragma unroll
-    for (int v = 0; v < 4; v++)
-        if (row + v < a.N)
-            a.y[(size_t)col * a.N + row + v] = finish(a.epi, sum[v], col, row + v, a.N);
+        for (int v = 0; v < 4; v++)
+            sum[v] += a.epi.bias[min(row + v, a.N - 1)];
+    const int left = a.N - row;
+    finish_rows(a, sum, col, row, left, left >= 4 && a.vec);
 }
 
 // The first bytes of a workspace belong to the GEMV form's exchange slots,
@@ -383,6 +430,7 @@ int rfx_gemm(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t
     a.part = reinterpret_cast<float *>(w + p.xh + p.sx);
     a.y = y;
     a.epi = e;
+    a.vec = W->rows % 4 == 0 && !((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(resid)) & 15);
     const int64_t frags = (int64_t)(p.qp / 16) * 8 * a.S;
     hipLaunchKernelGGL(gemm_columns_kernel, dim3((unsigned)((frags + 3) / 4)), dim3(256), 0, hs, xq, xs, q, W->cols / 32,
                        8 * a.S, p.qp, W->fmt == RFX_FP4, const_cast<uint16_t *>(a.xh), const_cast<float *>(a.sx));
