@@ -40,7 +40,25 @@ constexpr int lds_bytes()
 // pitch of 2 D + 32 bytes the groups' rows fall on different banks.
 __device__ __forceinline__ int row_key(int r) { return (r & 3) + 8 * ((r >> 2) & 3) + 4 * (r >> 4); }
 
-template <class T, int DP, int NR, bool BIG>
+// The largest of the four lanes l % 16, one of each group of 16.
+__device__ __forceinline__ float max_groups(float x)
+{
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// How a tile's keys lie in pages. kOne: pages of 32 tokens or more, a tile
+// in one; kTwo: pages of 16, two per tile; both with heads of exactly DP
+// elements, so that a tile's addresses are one or two uniform bases, offsets
+// that the lane keeps, and immediates (few waves run at once in a small
+// call, and one wave issues an instruction every 8 cycles: the loop's length
+// in instructions is its time). kAny: smaller pages, or heads that do not
+// fill DP.
+enum Pages { kOne, kTwo, kAny };
+
+template <class T, int DP, int NR, Pages PG>
 __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 {
     constexpr int NC = DP / 32;         // K steps of the score product
@@ -57,7 +75,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     const KvArgs &kv = a.kv;
     const int unit = a.div_s(blockIdx.x), split = a.div_s.rem(blockIdx.x, unit);
     const int seq = kv.div_hk(unit), hk = kv.div_hk.rem(unit, seq);
-    const int D = kv.D;
+    const int D = PG == kAny ? kv.D : DP;
     const int window = a.window ? a.window : 1 << 30; // positions are below 2^30
 
     const Seq sq = load_seq(kv, seq);
@@ -103,75 +121,84 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     const int32_t *table = kv.table + (size_t)seq * kv.stride;
     const int last_key = max(0, kt.hi - 1);
     const int ps = kv.page_shift, pm = (1 << ps) - 1;
-    const size_t head_stride = (size_t)D << ps;             // elements of one head of a page
+    const unsigned page_elems = (unsigned)kv.Hk * D << ps;  // at most 2^30
+    const size_t head_off = (size_t)hk * D << ps;
     const int ka = 8 * (r16 >> 2) + (r16 & 3);              // the lane's keys of a tile: ka and ka + 4
     const int vrow = lane / CH, vch = 8 * (lane % CH) < D ? 8 * (lane % CH) : 0;
     char *vbuf = smem + wave * (BN * VP);
-
-    // Page ids. Pages of 32 keys or more: one id per tile; lane i holds the
-    // id of the wave's i-th next tile, refilled every 64 tiles. Smaller
-    // pages: lane i holds the id of key i % 32 of one tile.
-    const auto ids_big = [&](int t) {
-        const int key = min(tile_key<BN>(kt, min(t + kWaves * lane, max(kt.n - 1, 0))), last_key);
-        return table[key >> ps];
-    };
-    const auto ids_small = [&](int t) {
-        const int key = min(tile_key<BN>(kt, t) + (lane & 31), last_key);
-        return table[key >> ps];
-    };
     const auto usable = [&](int id) { return (unsigned)id < (unsigned)kv.n_pages; };
 
+    // Page ids. kOne, kTwo: lane i holds the i-th id of the wave's next
+    // tiles, refilled when they run out; id[h] is uniform. kAny: lane i holds
+    // the id of key i % 32 of one tile.
+    constexpr int HALVES = PG == kTwo ? 2 : 1;
+    struct Ids {
+        int id[HALVES];
+    };
+    int ids = 0, ids_at = 0;   // ids of tiles ids_at, ids_at + kWaves, ...
+    const auto fill_ids = [&](int t) {
+        const int key = min(tile_key<BN>(kt, min(t + kWaves * (lane / HALVES), kt.n - 1)) + 16 * (lane % HALVES), last_key);
+        ids = table[key >> ps];
+        ids_at = t;
+    };
+    const auto uniform_ids = [&](int t) {
+        Ids u;
+#pragma unroll
+        for (int h = 0; h < HALVES; h++)
+            u.id[h] = __builtin_amdgcn_readlane(ids, HALVES * ((t - ids_at) / kWaves) + h);
+        return u;
+    };
+    const auto lane_ids = [&](int t) { return Ids{{table[min(tile_key<BN>(kt, t) + (lane & 31), last_key) >> ps]}}; };
+    // the first element of this head in the page, and of the tile's slots there
+    const auto base = [&](const uint16_t *cache, int id, int key0) {
+        return cache + head_off + (size_t)(unsigned)(usable(id) ? id : 0) * page_elems + (PG == kAny ? 0 : (key0 & pm) * D);
+    };
+
     u4 kf[2][NC], vf[NV];
-    // The loads of tile t; addresses are always inside the cache.
-    const auto load_k = [&](int key0, int ids) {
-        if constexpr (BIG) {
-            const uint16_t *p = kv.k + ((size_t)(usable(ids) ? ids : 0) * kv.Hk + hk) * head_stride;
+    // The loads of a tile; addresses are always inside the cache.
+    const auto load_k = [&](int key0, const Ids &u) {
+        const uint16_t *p;
+        if constexpr (PG == kOne)
+            p = base(kv.k, u.id[0], key0) + (unsigned)(ka * D + 8 * g4);
+        else if constexpr (PG == kTwo)
+            p = (r16 < 8 ? base(kv.k, u.id[0], 0) : base(kv.k, u.id[1], 0)) + (unsigned)((ka & 15) * D + 8 * g4);
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const uint16_t *kp = p + (size_t)((key0 + ka + 4 * j) & pm) * D;
+        for (int j = 0; j < 2; j++) {
+            if constexpr (PG == kAny)
+                p = base(kv.k, __shfl(u.id[0], ka + 4 * j, 64), 0) + (unsigned)(((key0 + ka + 4 * j) & pm) * D);
 #pragma unroll
-                for (int c = 0; c < NC; c++) {
-                    const int d = 32 * c + 8 * g4;
-                    kf[j][c] = *reinterpret_cast<const u4 *>(kp + (d < D ? d : 0));
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const int id = __shfl(ids, ka + 4 * j, 64);
-                const uint16_t *kp = kv.k + ((size_t)(usable(id) ? id : 0) * kv.Hk + hk) * head_stride +
-                                     (size_t)((key0 + ka + 4 * j) & pm) * D;
-#pragma unroll
-                for (int c = 0; c < NC; c++) {
-                    const int d = 32 * c + 8 * g4;
-                    kf[j][c] = *reinterpret_cast<const u4 *>(kp + (d < D ? d : 0));
-                }
+            for (int c = 0; c < NC; c++) {
+                const int d = 32 * c + 8 * g4;
+                kf[j][c] = *reinterpret_cast<const u4 *>(p + (PG == kAny ? (d < D ? d : 0) : 4 * j * D + 32 * c));
             }
         }
     };
-    const auto load_v = [&](int key0, int ids) {
+    // Values are read once and not kept in the caches (the keys are, whose
+    // lines two loads share): 301 to 277 us on a 1.6 GB cache.
+    const auto load_v = [&](int key0, const Ids &u) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const int key = row_key(i * RPI + vrow);
-            const int id = BIG ? ids : __shfl(ids, key, 64);
-            const uint16_t *p = kv.v + ((size_t)(usable(id) ? id : 0) * kv.Hk + hk) * head_stride +
-                                (size_t)((key0 + key) & pm) * D;
-            // read once: not kept in the caches (the keys are, whose lines two
-            // loads share): 301 to 277 us on a 1.6 GB cache
-            vf[i] = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p + vch));
+            // the key's part that the lane decides and the load's own
+            const int kl = row_key(vrow), ki = row_key(i * RPI);
+            const uint16_t *p;
+            if constexpr (PG == kOne)
+                p = base(kv.v, u.id[0], key0) + ki * D + (unsigned)(kl * D + vch);
+            else if constexpr (PG == kTwo)
+                p = base(kv.v, u.id[ki >> 4], 0) + (ki & 15) * D + (unsigned)(kl * D + vch);
+            else
+                p = base(kv.v, __shfl(u.id[0], kl + ki, 64), 0) + (unsigned)(((key0 + kl + ki) & pm) * D + vch);
+            vf[i] = __builtin_nontemporal_load(reinterpret_cast<const u4 *>(p));
         }
     };
 
-    int ids = 0, ids_at = 0;   // BIG: ids of tiles ids_at, ids_at + 4, ...
-    int cur = 0, nxt = 0;      // ids of the tile in the registers, and of the next
+    Ids cur{}, nxt{};          // ids of the tile in the registers, and of the next
     if (t_begin < t_end) {
-        if constexpr (BIG) {
-            ids = ids_big(t_begin);
-            ids_at = t_begin;
-            cur = __builtin_amdgcn_readlane(ids, 0);
+        if constexpr (PG == kAny) {
+            cur = lane_ids(t_begin);
+            nxt = lane_ids(min(t_begin + kWaves, t_end - 1));
         } else {
-            cur = ids_small(t_begin);
-            nxt = ids_small(min(t_begin + kWaves, t_end - 1));
+            fill_ids(t_begin);
+            cur = uniform_ids(t_begin);
         }
         load_k(tile_key<BN>(kt, t_begin), cur);
         load_v(tile_key<BN>(kt, t_begin), cur);
@@ -180,24 +207,22 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         const int key0 = tile_key<BN>(kt, t);
         const int tn = t + kWaves < t_end ? t + kWaves : t; // the next tile, or this one again
         const int key_n = tile_key<BN>(kt, tn);
-        const int cur_ids = cur;
-        int nn = 0; // small pages: the ids after next, ahead of the loads they must not wait for
-        if constexpr (!BIG)
-            nn = ids_small(min(t + 2 * kWaves, t_end - 1));
-        if constexpr (BIG) {
-            if ((tn - ids_at) / kWaves >= 64) {
-                ids = ids_big(tn);
-                ids_at = tn;
+        Ids nn{}; // kAny: the ids after next, ahead of the loads they must not wait for
+        if constexpr (PG == kAny) {
+            nn = lane_ids(min(t + 2 * kWaves, t_end - 1));
+        } else {
+            if ((tn - ids_at) / kWaves >= 64 / HALVES) {
+                fill_ids(tn);
                 // waited for here, or the compiler waits for every load of
                 // the loop wherever it reads an id
                 __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
             }
-            nxt = __builtin_amdgcn_readlane(ids, (tn - ids_at) / kWaves);
+            nxt = uniform_ids(tn);
         }
 
         // scores: register v of s[n][j] is key key0 + 8 (l / 16) + 4 j + v
         f32x4 s[NR][2];
-        if (D != DP) { // elements past D in the last K step
+        if (PG == kAny && D != DP) { // elements past D in the last K steps
 #pragma unroll
             for (int c = 0; c < NC; c++)
                 if (32 * c + 8 * g4 >= D)
@@ -219,7 +244,19 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 
         // a tile that some row sees only in part, or whose page ids are not
         // all good (in the small-page case every tile is checked for that)
-        const bool page_bad = BIG ? !usable(cur_ids) : __ballot(!usable(cur_ids)) != 0;
+        bool page_bad = !usable(cur.id[0]);
+        if constexpr (PG == kTwo)
+            page_bad |= !usable(cur.id[1]);
+        if constexpr (PG == kAny)
+            page_bad = __ballot(page_bad) != 0;
+        const auto page_good = [&](int kk) { // kk < 32: key of the tile
+            if constexpr (PG == kOne)
+                return usable(cur.id[0]);
+            else if constexpr (PG == kTwo)
+                return kk < 16 ? usable(cur.id[0]) : usable(cur.id[1]);
+            else
+                return usable(__shfl(cur.id[0], kk, 64));
+        };
         const bool edge = (key0 + BN - 1 > p_lo) | (key0 + BN > kt.hi) | ((key0 <= p_hi - window) & (key0 + BN > a.sinks)) | page_bad;
         if (edge) { // no branches inside: the compiler's waits for the loads in flight would cover all of them
 #pragma unroll
@@ -227,7 +264,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 #pragma unroll
                 for (int v = 0; v < 4; v++) {
                     const int kk = 8 * g4 + 4 * j + v, key = key0 + kk;
-                    const bool good = usable(BIG ? cur_ids : __shfl(cur_ids, kk, 64)) & (key < kt.hi);
+                    const bool good = page_good(kk) & (key < kt.hi);
 #pragma unroll
                     for (int n = 0; n < NR; n++) {
                         const bool seen = good & (key <= pos[n]) & ((key > pos[n] - window) | (key < a.sinks));
@@ -238,7 +275,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int kk = row_key(i * RPI + vrow), key = key0 + kk;
-                const bool any = usable(BIG ? cur_ids : __shfl(cur_ids, kk, 64)) & (key < kt.hi) & ((key >= kt.lo) | (key < kt.sk));
+                const bool any = page_good(kk) & (key < kt.hi) & ((key >= kt.lo) | (key < kt.sk));
                 const uint32_t keep = any ? ~0u : 0u;
 #pragma unroll
                 for (int e = 0; e < 4; e++)
@@ -251,19 +288,18 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         for (int n = 0; n < NR; n++) {
             float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
                               fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float mn = fmaxf(m[n], top);
-            if (__any(mn > m[n])) {
+            top = max_groups(top);
+            // weights may grow to 2^LAG before the sums are rescaled
+            if (__any(a.c * (top - m[n]) > T::LAG)) {
                 // nothing seen yet: the sums are zero, and so is the factor
-                const float f = m[n] == -INFINITY ? 0.f : fast_exp2(a.c * (m[n] - mn));
+                const float mn = fmaxf(m[n], top), f = m[n] == -INFINITY ? 0.f : fast_exp2(a.c * (m[n] - mn));
                 l[n] *= f;
 #pragma unroll
                 for (int i = 0; i < NV; i++)
                     acc[n][i] *= f;
                 m[n] = mn;
             }
-            const float off = mn == -INFINITY ? 0.f : T::BIAS - a.c * mn;
+            const float off = m[n] == -INFINITY ? 0.f : T::BIAS - a.c * m[n];
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; i++) {
@@ -296,7 +332,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         cur = nxt;
-        if constexpr (!BIG)
+        if constexpr (PG == kAny)
             nxt = nn;
     }
 
@@ -364,10 +400,13 @@ template <class T, int DP, int NR>
 int launch(const AttnArgs &a, hipStream_t st)
 {
     const unsigned grid = (unsigned)a.kv.n_seq * a.kv.Hk * a.S;
-    if (a.kv.page_shift >= 5)
-        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, true>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    const dim3 block(64 * kWaves);
+    if (a.kv.D != DP || a.kv.page_shift < 4)
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kAny>), dim3(grid), block, 0, st, a);
+    else if (a.kv.page_shift == 4)
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kTwo>), dim3(grid), block, 0, st, a);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, false>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kOne>), dim3(grid), block, 0, st, a);
     return hip_status("attn decode launch");
 }
 

@@ -56,6 +56,9 @@ DECODE = [
     ([(4, 100)], 4, 1, 200, 4),
     ([(2, 90), (2, 64)], 2, 2, 8, 256),
     ([(1, 77)] * 9, 20, 4, 120, 2),
+    ([(2, 300), (1, 50)], 8, 2, 256, 16),
+    ([(1, 2500), (4, 1000)], 8, 2, 128, 16),
+    ([(1, 9000)], 2, 1, 64, 128),
 ]
 
 
@@ -135,7 +138,7 @@ def test_rows_before_the_first_token(rows, page):
 
 
 @pytest.mark.parametrize("rows", [1, 70])
-@pytest.mark.parametrize("page", [2, 32])
+@pytest.mark.parametrize("page", [2, 16, 32])
 def test_bad_pages_are_not_visible(rows, page):
     """A page id outside the cache: its keys count as masked; a sequence with
     no good page is zero."""
@@ -160,14 +163,15 @@ def test_bad_pages_are_not_visible(rows, page):
 
 
 @pytest.mark.parametrize("rows", [1, 50])
-def test_masked_nan_stays_out(rows):
+@pytest.mark.parametrize("page", [4, 16, 64])
+def test_masked_nan_stays_out(rows, page):
     """NaN and infinity in keys and values that every row's window leaves
     out, beside the visible ones of the same page and tile."""
     need_gpu()
-    b = Batch([(rows, 333)], 64, 1, 64, "f16", seed=8)
+    b = Batch([(rows, 333)], page, 1, 64, "f16", seed=8)
     lo = 333 - rows - 20 + 1
     for p in range(3, lo):
-        at = int(b.table[0, p // 64]), slice(None), p % 64
+        at = int(b.table[0, p // page]), slice(None), p % page
         b.k[at] = float("nan") if p % 2 else float("inf")
         b.v[at] = float("-inf") if p % 2 else float("nan")
     q = torch.randn((rows, 4, 64), generator=torch.Generator().manual_seed(8)).to(b.dtype)
