@@ -140,7 +140,7 @@ struct Plan {
     bool decode;
     int row_tiles;   // decode: 16-row tiles per workgroup
     int row_blocks;
-    int S, min_tiles;
+    int S, min_tiles, one_tiles;
     int rows, bn;    // rows of a block, keys of a tile
     int64_t units;   // (sequence, row block, kv head)
     size_t part, stat;
@@ -161,11 +161,16 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
     p.row_tiles = p.rows / 16;
     p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
     p.bn = p.decode || dp == 256 ? 32 : 64;
-    p.min_tiles = p.decode ? 8 : 4;
+    // measured in us, one sequence, 8 kv heads, 512 / 700 / 1537 keys: 16
+    // tiles (of 32 keys) unsplit 8.9 and as two splits 10.0; 22 tiles 9.0 as
+    // six splits and 11.3 unsplit; 49 tiles 9.8 as 13 splits, 10.6 as seven.
+    // Prompt chunks of 300 new tokens: 5 tiles (of 64) 15.5 unsplit, 20.2 split.
+    p.min_tiles = p.decode ? 4 : 2;
+    p.one_tiles = p.decode ? 16 : 6;
     const int64_t tiles = ceil_div((int64_t)B->table_stride * C->page_size, p.bn);
     p.units = (int64_t)B->n_seq * C->n_kv_heads * p.row_blocks;
     const int64_t want = 2 * 256 / (p.units < 512 ? p.units : 512);
-    const int64_t most = ceil_div(tiles, p.min_tiles);
+    const int64_t most = tiles <= p.one_tiles ? 1 : ceil_div(tiles, p.min_tiles);
     p.S = (int)(want < most ? want : most);
     p.S = p.S < 1 ? 1 : p.S > kMaxSplits ? kMaxSplits : p.S;
     if (p.S > 1) {
@@ -237,9 +242,11 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     a.rows = p.rows;
     a.bn = p.bn;
     a.min_tiles = p.min_tiles;
+    a.one_tiles = p.one_tiles;
+    a.cap_shift = p.rows == 16 ? 5 : 3;
     a.div_s = Div(p.S);
     a.div_rb = Div(p.row_blocks);
-    a.div_mt = Div(p.min_tiles);
+    a.div_units = Div((uint32_t)p.units);
     if (p.S > 1) {
         a.part = static_cast<float *>(ws);
         a.stat = reinterpret_cast<float *>(static_cast<char *>(ws) + p.part);

@@ -66,11 +66,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prefill_kern
     const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, hl = lane >> 5, i16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const KvArgs &kv = a.kv;
-    // kv heads vary fastest: workgroups go round the XCDs in order, so with
-    // eight kv heads each XCD's L2 holds one head's keys and values
-    const int b = kv.div_hk(blockIdx.x);
-    const int hk = kv.div_hk.rem(blockIdx.x, b);
-    const int us = a.div_s(b), split = a.div_s.rem(b, us);
+    // Splits vary slowest (see the decode kernel). kv heads vary fastest:
+    // workgroups go round the XCDs in order, so with eight kv heads each
+    // XCD's L2 holds one head's keys and values.
+    const int split = a.div_units(blockIdx.x), b = a.div_units.rem(blockIdx.x, split);
+    const int us = kv.div_hk(b), hk = kv.div_hk.rem(b, us);
     const int seq = a.div_rb(us), rb = a.row_blocks - 1 - a.div_rb.rem(us, seq); // the longest first
     const int unit = (seq * a.row_blocks + rb) * kv.Hk + hk;
     const int D = kv.D;

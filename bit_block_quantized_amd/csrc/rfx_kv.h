@@ -83,7 +83,9 @@ struct AttnArgs {
     int rows;          // rows of a block
     int bn;            // keys of a tile
     int min_tiles;     // key tiles a split takes at least
-    Div div_s, div_rb, div_mt; // by S, row_blocks and min_tiles
+    int one_tiles;     // up to so many key tiles are not split
+    int cap_shift;     // see split_tiles
+    Div div_s, div_rb, div_units; // by S, row_blocks and units
     // workspace, where S > 1, by unit = (seq * row_blocks + block) * Hk + hk:
     float *part;       // [unit][split][rows][DP] unnormalized results
     float *stat;       // [unit][split][rows][2] their maxima and sums
@@ -249,17 +251,18 @@ __device__ __forceinline__ KeyTiles key_tiles(int bn, int p_lo, int p_hi, int kv
 }
 
 // How a block's n key tiles are split: `per` tiles each over `active` of the
-// grid's S splits (one, with no tiles, for a block that sees no key).
+// grid's S splits. Few tiles are not split (joining costs more), and a split
+// takes n / 2^cap_shift tiles, though not fewer than min_tiles nor, for
+// that, more than 16: joining costs by splits and rows.
 __device__ __forceinline__ void split_tiles(const AttnArgs &a, int n, int &per, int &active)
 {
-    per = a.div_s(n + a.S - 1);
-    if (per >= a.min_tiles) {
-        // S splits, or fewer by rounding: per is not known at launch
-        active = max(1, (n + per - 1) / per);
-    } else {
-        per = a.min_tiles;
-        active = max(1, a.div_mt(n + per - 1));
+    if (n <= a.one_tiles || a.S == 1) {
+        per = n;
+        active = 1;
+        return;
     }
+    per = max(a.div_s(n + a.S - 1), max(a.min_tiles, min((n + (1 << a.cap_shift) - 1) >> a.cap_shift, 16)));
+    active = (n + per - 1) / per;
 }
 
 // First key of the i-th tile.
