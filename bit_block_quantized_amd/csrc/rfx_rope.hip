@@ -10,7 +10,11 @@
 // are in one lane. A lane turns the same four pairs in every head of its
 // token, so it evaluates its four angles once: position * inv_freq / 2 pi in
 // fp64, of which the whole turns are dropped before the rest goes to fp32
-// (at position 2^20 an fp32 product would be off by 0.06 rad).
+// (at position 2^20 an fp32 product would be off by 0.06 rad) and to the
+// hardware's sine and cosine of turns (off by at most 2^-22, measured
+// over 2^24 arguments; the result is rounded to 8 or 11 bits).
+#include <type_traits>
+
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -47,9 +51,29 @@ __device__ __forceinline__ int find_seq(const int32_t *q_off, int n, int t)
     return t >= first && t < last ? lo : -1;
 }
 
+// Sum over the LPH (8, 16 or 32) lanes of a head: neighbours, pairs and
+// halves by the vector pipe's own lane exchanges.
+template <int LPH>
+__device__ __forceinline__ float head_sum(float x)
+{
+    const auto add = [&](auto ctrl) {
+        x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    add(std::integral_constant<int, 0xB1>{});  // lanes 1 0 3 2
+    add(std::integral_constant<int, 0x4E>{});  // lanes 2 3 0 1
+    add(std::integral_constant<int, 0x141>{}); // 7 - i of 8
+    if (LPH >= 16)
+        add(std::integral_constant<int, 0x140>{}); // 15 - i of 16
+    if (LPH == 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return x;
+}
+
 // One workgroup of four waves per token and share (blockIdx.y) of its
 // heads; a wave takes 64 / LPH heads at a time: queries, keys, then values.
-template <class T, int LPH>
+template <class T, int LPH, bool NT>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
 {
     constexpr int HPW = 64 / LPH;
@@ -70,8 +94,17 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
         return h < Hq ? a.q + t * a.qs + h * D : h < Hq + Hk ? a.k + t * a.ks + (h - Hq) * D : a.v + t * a.vs + (h - Hq - Hk) * D;
     };
     const float *p = source(min(h, H - 1));
-    f32x4 x0 = *reinterpret_cast<const f32x4 *>(p + (on ? e0 : 0));
-    f32x4 x1 = *reinterpret_cast<const f32x4 *>(p + (on ? e1 : 0));
+    const auto load = [&](int e) {
+        const f32x4 *q = reinterpret_cast<const f32x4 *>(p + (on ? e : 0));
+        return NT ? __builtin_nontemporal_load(q) : *q;
+    };
+    const auto store = [&](uint16_t *q, auto v) {
+        if (NT)
+            __builtin_nontemporal_store(v, reinterpret_cast<decltype(v) *>(q));
+        else
+            *reinterpret_cast<decltype(v) *>(q) = v;
+    };
+    f32x4 x0 = load(e0), x1 = load(e1);
 
     const int s = find_seq(a.kv.q_off, a.kv.n_seq, t);
     if (s < 0)
@@ -90,7 +123,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
         for (int i = 0; i < 4; i++) {
             const double turns = (double)pos * a.inv_freq[4 * l + i] * 0.15915494309189533577;
             const float f = (float)(turns - rint(turns)); // -0.5 .. 0.5
-            sincospif(2.0f * f, &sn[i], &cs[i]);
+            sn[i] = __builtin_amdgcn_sinf(f); // of turns
+            cs[i] = __builtin_amdgcn_cosf(f);
         }
     }
     if (on && a.wq) {
@@ -102,23 +136,22 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
         wk1 = *reinterpret_cast<const f32x4 *>(a.wk + e1);
     }
 
+    const float inv_d = 1.0f / (float)D;
     for (int base = h - lane / LPH; base < H; base += step, h += step) {
         f32x4 y0 = x0, y1 = x1;
         const int hn = min(h + step, H - 1); // the next head's loads, always in bounds
         p = source(hn);
-        x0 = *reinterpret_cast<const f32x4 *>(p + (on ? e0 : 0));
-        x1 = *reinterpret_cast<const f32x4 *>(p + (on ? e1 : 0));
+        x0 = load(e0);
+        x1 = load(e1);
         const bool is_q = h < Hq, is_v = h >= Hq + Hk;
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; i++)
             ss += on ? y0[i] * y0[i] + y1[i] * y1[i] : 0.f;
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1)
-            ss += __shfl_xor(ss, o, 64);
+        ss = head_sum<LPH>(ss);
         if (!is_v) {
             const bool norm = is_q ? a.wq != nullptr : a.wk != nullptr;
-            const float r = norm ? 1.0f / sqrtf(ss / (float)D + a.eps) : 1.0f;
+            const float r = norm ? __builtin_amdgcn_rsqf(ss * inv_d + a.eps) : 1.0f; // to 2^-22
             const f32x4 w0 = is_q ? wq0 : wk0, w1 = is_q ? wq1 : wk1;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -151,10 +184,10 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
         // one rounding to the cache's type, to nearest even
         const u2 r0 = {T::pack(y0[0], y0[1]), T::pack(y0[2], y0[3])}, r1 = {T::pack(y1[0], y1[1]), T::pack(y1[2], y1[3])};
         if (halves) {
-            *reinterpret_cast<u2 *>(o + e0) = r0;
-            *reinterpret_cast<u2 *>(o + e1) = r1;
+            store(o + e0, r0);
+            store(o + e1, r1);
         } else {
-            *reinterpret_cast<u4 *>(o + e0) = (u4){r0.x, r0.y, r1.x, r1.y};
+            store(o + e0, (u4){r0.x, r0.y, r1.x, r1.y});
         }
     }
 }
@@ -168,13 +201,23 @@ int launch(const RopeArgs &a, hipStream_t st)
     // few tokens: a token's heads over several workgroups, one pass each;
     // with many, one workgroup per token evaluates the angles once per wave
     const int passes = (H + per - 1) / per;
-    const dim3 grid(a.kv.n_tokens, a.kv.n_tokens < 512 ? passes : 1);
-    if (lph == 8)
-        hipLaunchKernelGGL((rope_kernel<T, 8>), grid, dim3(256), 0, st, a);
-    else if (lph == 16)
-        hipLaunchKernelGGL((rope_kernel<T, 16>), grid, dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((rope_kernel<T, 32>), grid, dim3(256), 0, st, a);
+    const bool few = a.kv.n_tokens < 512;
+    const dim3 grid(a.kv.n_tokens, few ? passes : 1), block(256);
+    // many tokens' rows are more than the caches hold until they are used:
+    // past them (79 to 71 us for 10858 tokens of 48 heads of 128)
+#define RFX_ROPE(LPH)                                                               \
+    if (few)                                                                        \
+        hipLaunchKernelGGL((rope_kernel<T, LPH, false>), grid, block, 0, st, a);    \
+    else                                                                            \
+        hipLaunchKernelGGL((rope_kernel<T, LPH, true>), grid, block, 0, st, a);
+    if (lph == 8) {
+        RFX_ROPE(8)
+    } else if (lph == 16) {
+        RFX_ROPE(16)
+    } else {
+        RFX_ROPE(32)
+    }
+#undef RFX_ROPE
     return hip_status("qk_norm_rope launch");
 }
 
