@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "librfx.so")
 
 SOURCES = ["rfx_host.cpp", "rfx_gemv.hip", "rfx_moe.hip", "rfx_moe_layer.hip", "rfx_prefill.hip", "rfx_probe.hip",
-           "rfx_gemm.hip", "rfx_rope.hip", "rfx_attn.hip", "rfx_attn_decode.hip", "rfx_attn_prefill.hip"]
+           "rfx_gemm.hip", "rfx_gemm_mx.hip", "rfx_rope.hip", "rfx_attn.hip", "rfx_attn_decode.hip", "rfx_attn_prefill.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

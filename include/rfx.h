@@ -252,9 +252,12 @@ int rfx_gemv_grouped(const rfx_gemv_job *jobs, int n_jobs, void *ws, size_t ws_b
 /* The product with its epilogue, for any number of columns:
  * y[j][n] = resid[j][n] + act(sum as in rfx_gemv + bias[n]).
  * Decode's projections (q <= 4) run on the GEMV kernels, the epilogue in
- * the lane that ends with the whole sum; prompts' (q > 4) on the matrix core,
- * one exact integer block dot per 32-weight block and column, scaled and
- * accumulated in fp32.
+ * the lane that ends with the whole sum; prompts' (q > 4) on the matrix core.
+ * There FP2 and FP3 take one exact integer block dot per 32-weight block and
+ * column, scaled and accumulated in fp32. FP4 takes each scaled activation as
+ * a sum of five 6-bit digits, which is within 2^-23.9 of its block's largest
+ * (or 2^-130, if that is more), and sums exact products in fp32; a block
+ * whose largest |xs code| is not finite makes its column NaN.
  * W: count must be 1; any format at q <= 4, RFX_FP2, RFX_FP3 or RFX_FP4 at
  * q > 4 (RFX_E_UNSUPPORTED otherwise). q 1..RFX_GEMM_MAX_Q. xq, xs and xsum
  * as for rfx_gemv. bias fp32 [N] or NULL; act: RFX_ACT_SILU is z / (1 +

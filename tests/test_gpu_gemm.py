@@ -166,3 +166,64 @@ def test_graph_replays(q):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(yg, ye), i
+
+
+def wide_case(q, rows, cols, seed):
+    """FP4 weights and activations whose block scales are far apart, codes of
+    every size (a block's largest from 1 to -128) and zero blocks."""
+    rng = np.random.default_rng(seed)
+    nb = cols // 32
+    c = Case(4, q, rows, cols, seed=seed)
+    W = inputgen.dense_weight(rows, cols, seed=seed) * np.repeat(2.0 ** rng.integers(-12, 13, (rows, nb)), 32, axis=1)
+    W = W.astype(np.float32)
+    c.dW = upload_matrix(torch, 4, W)
+    c.Wd = O.dequantize_matrix(4, O.quantize_matrix(4, W)).astype(np.float64)
+    amp = 2.0 ** rng.uniform(0, 7, (q, nb))
+    amp[rng.random((q, nb)) < 0.1] = 0
+    codes = np.round(rng.uniform(-1, 1, (q, nb, 32)) * amp[..., None])
+    codes[0, 0, 5] = -128
+    xs = (2.0 ** rng.uniform(-20, 20, (q, nb))).astype(np.float32)
+    xs[rng.random((q, nb)) < 0.05] = 0
+    if q > 1 and nb > 1:
+        xs[1, 1] = 1e-41  # subnormal
+    return c, codes.astype(np.int8), xs
+
+
+@pytest.mark.parametrize("q,rows,cols", [(5, 70, 32), (9, 100, 512), (40, 300, 800), (130, 600, 2080)])
+def test_fp4_digits_over_wide_scales(q, rows, cols):
+    """FP4's activations as sums of five digits: each is within 2^-23.9 of the
+    largest of its block after the fp32 rounding of code * scale (2^-24), the
+    ten products of a K tile round once each at no more than the tile's sum of
+    |w x|, and each of the tiles is added with one rounding: within
+    (tiles + 11) 2^-24 sum |w x| + 2^-23.9 sum_b max_b |x| sum_b |w|. Partials
+    of up to tiles / 2 splits add as many roundings."""
+    need_gpu()
+    say(f"gemm wide q={q} {rows}x{cols}")
+    c, codes, xs = wide_case(q, rows, cols, seed=q)
+    nb = cols // 32
+    c.xq = torch.from_numpy(codes.reshape(q, cols)).cuda()
+    c.xs = torch.from_numpy(xs).cuda()
+    c.xsum = torch.from_numpy(codes.astype(np.int32).sum(2).astype(np.int32)).cuda()
+    y = c.run()
+    xd = codes.astype(np.float64) * xs[..., None].astype(np.float64)
+    want = xd.reshape(q, cols) @ c.Wd.T
+    mag = np.abs(xd).reshape(q, cols) @ np.abs(c.Wd).T
+    top = np.abs(xd).max(2) @ np.abs(c.Wd).reshape(rows, nb, 32).sum(2).T
+    tiles = -(-cols // 256)
+    tol = 2.0 ** -24 * (1.5 * tiles + 11) * mag + 2.0 ** -23.9 * top + 1e-30
+    bad = ~(np.abs(y - want) <= tol)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outside, worst {(np.abs(y - want) / tol)[bad].max()} of its bound"
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+def test_fp4_scale_that_is_not_finite(value):
+    """A block whose largest value is not finite (3e38 * 127 neither) makes
+    its column NaN and no other."""
+    need_gpu()
+    c = Case(4, 20, 100, 512, seed=2)
+    c.xs[3, 4] = value
+    y = c.run()
+    assert np.isnan(y[3]).all() and np.isfinite(np.delete(y, 3, 0)).all()
+    keep = [j for j in range(20) if j != 3]
+    tol = 1.13 * 2.0 ** -24 * (512 // 32 + 2) * c.mag + 1e-30
+    assert (np.abs(y - c.z) <= tol)[keep].all()
