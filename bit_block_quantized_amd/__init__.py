@@ -287,6 +287,7 @@ class DeviceQMat:
     def __init__(self, fmt, rows, cols, data, count=1):
         self.fmt, self.rows, self.cols, self.count = fmt, rows, cols, count
         self.data = data  # torch uint8 tensor on the GPU (kept alive here)
+        self.index = None if data is None or isinstance(data, int) else data.get_device()
         self.c = QMat(fmt, rows, cols, count, _dptr(data))
 
     @classmethod
@@ -345,10 +346,12 @@ def gemm_workspace_bytes(W: DeviceQMat, q: int) -> int:
 
 
 def gemm(W: DeviceQMat, xq, xs, xsum, q, y, bias=None, act=ACT_NONE, resid=None, ws=None, stream=None):
-    """y = resid + act(W x + bias) for q columns (rfx_gemm)."""
+    """y = resid + act(W x + bias) for q columns (rfx_gemm), on W's device:
+    its current stream unless one is given."""
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().rfx_gemm(W.ref(), _dptr(xq), _dptr(xs), _dptr(xsum), q, _dptr(bias), act, _dptr(resid), _dptr(y),
-                          _dptr(ws), ws_bytes, _stream(stream)))
+    index = _torch().current_device() if W.index is None else W.index
+    _call_on(index, stream, lib().rfx_gemm, W.ref(), _dptr(xq), _dptr(xs), _dptr(xsum), q, _dptr(bias), act, _dptr(resid),
+             _dptr(y), _dptr(ws), ws_bytes)
 
 
 def gemv_jobs(jobs):

@@ -1,7 +1,11 @@
 """CPU tests of rfx_gemm's refusals and workspace sizes: every bad argument
 fails before any HIP call."""
 
+import contextlib
 import ctypes
+
+import pytest
+import torch
 
 import bit_block_quantized_amd as R
 
@@ -42,3 +46,37 @@ def test_workspace_sizes():
     assert all(R.lib().rfx_gemv_workspace_bytes(ctypes.byref(R.QMat(4, r, c, 1, P)), 4) <= 256 << 10
                for r in (1, 64, 777, 4096, 20000) for c in (32, 512, 4096, 65536))
     assert need(0) == need(65537) == need(9, fmt=8) == need(9, cols=33) == 0
+
+
+def test_weights_in_host_memory_are_refused():
+    W = R.DeviceQMat(4, 64, 32, torch.zeros(8704, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="host memory"):
+        R.gemm(W, P, P, P, 1, P)
+
+
+def test_weights_on_another_device(monkeypatch):
+    """The call runs with W's device current, on that device's stream."""
+    calls, entered = [], []
+
+    class Lib:
+        @staticmethod
+        def rfx_gemm(*args):
+            calls.append((list(entered), args[-1]))
+            return 0
+
+    @contextlib.contextmanager
+    def guard(index):
+        entered.append(index)
+        yield
+        entered.pop()
+
+    t = R._torch()
+    monkeypatch.setattr(R, "lib", lambda: Lib)
+    monkeypatch.setattr(t, "current_device", lambda: entered[-1] if entered else 0)
+    monkeypatch.setattr(t, "device_guard", guard)
+    monkeypatch.setattr(t, "raw_stream", lambda index: 100 + index)
+    W = R.DeviceQMat(4, 64, 32, P)
+    for index, stream in ((3, None), (0, None), (3, 7), (None, None)):
+        W.index = index
+        R.gemm(W, P, P, P, 1, P, stream=stream)
+    assert calls == [([3], 103), ([], 100), ([3], 7), ([], 100)]
