@@ -227,7 +227,8 @@ class DeviceAttention:
 
 class AttentionBuffers:
     """Device buffers for attention calls over batches of this shape
-    (n_tokens, max_q, sequences and page-table width as `batch` has them)."""
+    (n_tokens, max_q, sequences and page-table width as `batch` has them),
+    for any layer with this one's formats and sizes."""
 
     def __init__(self, attn: DeviceAttention, cache, batch, device="cuda"):
         import torch
@@ -252,23 +253,41 @@ class AttentionBuffers:
         mats = (attn.wq, attn.wk, attn.wv, attn.wo)
         self.ws_gemm = zeros(max(gemm_workspace_bytes(W, T) for W in mats))
         self.ws_attn = zeros(attn_workspace_bytes(cache, batch, attn.n_heads))
-        self.jobs = None
-        if T <= 4:  # decode: query, key and value projections in one launch
-            from . import gemv_jobs
-            self.jobs = gemv_jobs([(W, T, *self.x_act, y) for W, y in zip(mats, (self.q, self.k, self.v))])
-            self.ws_jobs = zeros(gemv_grouped_workspace_bytes(self.jobs))
+        if T <= 4:
+            self.ws_jobs = zeros(gemv_grouped_workspace_bytes(self._jobs(attn)))
+
+    def _jobs(self, attn):
+        """Decode's query, key and value projections, one launch."""
+        from . import gemv_jobs
+        return gemv_jobs([(W, self.q.shape[0], *self.x_act, y)
+                          for W, y in zip((attn.wq, attn.wk, attn.wv), (self.q, self.k, self.v))])
 
     def run(self, attn: DeviceAttention, x, cache, batch, resid=None, out=None, stream=None):
         """Projections, norm, rotation and cache append, attention, output
         projection for x (device fp32 [n_tokens][hidden]); y = resid +
         Attention(x) lands in `out` (default self.y)."""
+        from . import _torch, _want
+        t, T, dev = _torch(), batch.n_tokens, cache.index
+        y = self.y if out is None else out
+        if self.q.shape[0] != T:
+            raise ValueError(f"buffers for {self.q.shape[0]} tokens, the batch has {T}")
+        for name, a in (("x", x), ("out", y)) + ((("resid", resid),) if resid is not None else ()):
+            _want(a, name, t.f32, (T, attn.hidden), dev)
+        _want(self.q, "buffers", t.f32, (T, attn.n_heads, attn.head_dim), dev)
+        if attn.wq.index != dev:
+            raise ValueError(f"weights on GPU {attn.wq.index}, the cache is on GPU {dev}")
+        if dev >= 0 and t.current_device() != dev:
+            with t.device_guard(dev):
+                return self._run(attn, x, cache, batch, resid, y, stream)
+        return self._run(attn, x, cache, batch, resid, y, stream)
+
+    def _run(self, attn, x, cache, batch, resid, y, stream):
         from . import attn as attention
         from . import gemm, gemv_grouped, qk_norm_rope, quantize_act
         T = batch.n_tokens
-        y = self.y if out is None else out
         quantize_act(x, *self.x_act, stream)
-        if self.jobs is not None:
-            gemv_grouped(self.jobs, self.ws_jobs, stream)
+        if T <= 4:
+            gemv_grouped(self._jobs(attn), self.ws_jobs, stream)
         else:
             for W, o in ((attn.wq, self.q), (attn.wk, self.k), (attn.wv, self.v)):
                 gemm(W, *self.x_act, T, o, ws=self.ws_gemm, stream=stream)

@@ -115,3 +115,41 @@ def test_layer_refuses_mismatched_projections():
         R.DeviceAttention(layer.wq, layer.wq, layer.wv, layer.wo, HQ, HK, D, layer.inv_freq)
     with pytest.raises(ValueError):
         R.DeviceAttention(layer.wq, layer.wk, layer.wv, layer.wk, HQ, HK, D, layer.inv_freq)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [20, 13]])
+def test_layers_share_buffers(new):
+    """One set of buffers through two layers in turn, on a side stream: each
+    gives what it gives with buffers of its own."""
+    need_gpu()
+    layers = [build(i)[0] for i in range(2)]
+    table = torch.tensor([[3, 1, 6, 0], [2, 7, 5, 4]], dtype=torch.int32, device="cuda")
+    batch = batch_of(new, new, table)
+    x = torch.from_numpy(inputgen.raw_normal(3, (sum(new), H))).cuda()
+    caches = [new_cache() for _ in range(4)]
+    own = [R.AttentionBuffers(a, c, batch).run(a, x, c, batch).clone() for a, c in zip(layers, caches)]
+    side = torch.cuda.Stream()
+    shared = R.AttentionBuffers(layers[0], caches[2], batch)
+    side.wait_stream(torch.cuda.current_stream())
+    out = [torch.empty_like(x) for _ in layers]
+    for a, c, y in zip(layers, caches[2:], out):
+        shared.run(a, x, c, batch, out=y, stream=side)
+    side.synchronize()
+    assert not torch.equal(own[0], own[1])
+    for y, want in zip(out, own):
+        assert torch.equal(y, want)
+
+
+def test_buffers_refuse_other_shapes():
+    need_gpu()
+    layer, cache = build()[0], new_cache()
+    table = torch.tensor([[3, 1, 6, 0]], dtype=torch.int32, device="cuda")
+    small, large = batch_of([3], [3], table), batch_of([5], [5], table)
+    buf = R.AttentionBuffers(layer, cache, small)
+    x = torch.zeros(5, H, device="cuda")
+    for args, kw in (((x, cache, large), {}), ((x, cache, small), {}), ((x[:3, :32], cache, small), {}),
+                     ((x[:3].double(), cache, small), {}), ((x[:3], cache, small), dict(out=x)),
+                     ((x[:3], cache, small), dict(resid=x)), ((x[:3].cpu(), cache, small), {})):
+        with pytest.raises(ValueError):
+            buf.run(layer, *args, **kw)
+    buf.run(layer, x[:3], cache, small)
