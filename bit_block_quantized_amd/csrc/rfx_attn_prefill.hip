@@ -54,12 +54,13 @@ __device__ __forceinline__ float max_halves(float x)
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// Heads of 64 fit three waves per SIMD in 168 registers (six prompts with a
-// window, fp32 result: 266 to 241 us), of 128 two in 256.
-constexpr int waves_per_simd(int dp) { return dp <= 64 ? 3 : dp <= 128 ? 2 : 1; }
+// Heads of 64 fit three waves per SIMD in 168 registers, of 128 two in 256.
+// Six prompts with a window, fp16 with an fp32 result: 272 us with two waves,
+// 248 with three; with bf16's three terms 65 (2048 tokens) and 71.
+constexpr int waves_per_simd(int dp, int terms) { return dp <= 64 && terms < 3 ? 3 : dp <= 128 ? 2 : 1; }
 
 template <class T, int DP, int TERMS>
-__global__ __launch_bounds__(kThreads, waves_per_simd(DP)) void attn_prefill_kernel(AttnArgs a)
+__global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_prefill_kernel(AttnArgs a)
 {
     using L = Tile<DP>;
     constexpr int BN = L::BN, NC = DP / 16, ND = DP / 32, NK = BN / 32;
