@@ -388,7 +388,7 @@ def bench_prefill(torch, R, inputgen, layer, reps, tokens=2048, k=6):
             "timing": "HIP graph replay of route + FFN"}
 
 
-GEMV_SOURCES = ("rfx_decode.h", "rfx_gemv.hip", "rfx_internal.h", "rfx_mx4.h", "rfx_xtile.h")
+GEMV_SOURCES = ("rfx_decode.h", "rfx_epi.h", "rfx_gemv.hip", "rfx_internal.h", "rfx_mx4.h", "rfx_xtile.h")
 
 
 def kernel_sources_sha256():
@@ -616,9 +616,10 @@ def sources_sha256(names):
     return h.hexdigest()
 
 
-MOE_SOURCES = ("rfx_decode.h", "rfx_gemv.hip", "rfx_internal.h", "rfx_moe.hip", "rfx_moe_dev.h", "rfx_moe_ws.h",
-               "rfx_mx4.h", "rfx_xtile.h")
-PREFILL_SOURCES = ("rfx_decode.h", "rfx_internal.h", "rfx_moe.hip", "rfx_moe_dev.h", "rfx_moe_ws.h", "rfx_prefill.hip")
+MOE_SOURCES = ("rfx_decode.h", "rfx_epi.h", "rfx_gemv.hip", "rfx_internal.h", "rfx_moe.hip", "rfx_moe_dev.h",
+               "rfx_moe_ws.h", "rfx_mx4.h", "rfx_xtile.h")
+PREFILL_SOURCES = ("rfx_decode.h", "rfx_internal.h", "rfx_moe.hip", "rfx_moe_dev.h", "rfx_moe_ws.h", "rfx_prefill.hip",
+                   "rfx_wfrag.h")
 
 
 def profile_only(args, torch, R, inputgen):
