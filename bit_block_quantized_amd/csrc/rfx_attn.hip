@@ -146,6 +146,23 @@ struct Plan {
     size_t part, stat;
 };
 
+// The two-group prefill kernel (rows of 256, heads of 65 to 128 elements)
+// wants two workgroups per compute unit in turn or long runs of key tiles:
+// it starts and ends slower, alone on its compute unit. Measured in us, 32
+// heads of 128 over 8, against the four-wave kernel: 8192 tokens (1024
+// workgroups) 528 and 586, 4096 (512) 156 and 171, 1000 after 30000 (four
+// splits of 121 tiles) 494 and 547; but 2048 (256) 90 and 69, 256 after
+// 8000 (sixteen splits of 9 tiles) 62 and 57. Its list of page ids has to
+// fit the LDS.
+bool pair_rows(const rfx_kv_cache *C, const rfx_kv_batch *B, int64_t rows, int dp)
+{
+    const int64_t keys = (int64_t)B->table_stride * C->page_size;
+    if (dp != 128 || ceil_div(keys, C->page_size < 64 ? C->page_size : 64) > kPairIds)
+        return false;
+    const int64_t units = (int64_t)B->n_seq * C->n_kv_heads * ceil_div(rows, kPairRows);
+    return units >= 512 || ceil_div(keys, 64) / (512 / units) >= 64;
+}
+
 // The decode kernel serves up to 32 rows (new tokens x query heads of a kv
 // head) in one pass over the keys, 16 with heads over 128 elements (its
 // accumulators would not fit the registers); more rows go to the prefill
@@ -157,7 +174,7 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
     const int64_t rows = (int64_t)B->max_q * (n_heads / C->n_kv_heads);
     const int dp = C->head_dim <= 64 ? 64 : C->head_dim <= 128 ? 128 : 256;
     p.decode = rows <= (dp == 256 ? 16 : 32);
-    p.rows = p.decode ? (rows <= 16 ? 16 : 32) : 128;
+    p.rows = p.decode ? (rows <= 16 ? 16 : 32) : pair_rows(C, B, rows, dp) ? kPairRows : 128;
     p.row_tiles = p.rows / 16;
     p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
     p.bn = p.decode || dp == 256 ? 32 : 64;

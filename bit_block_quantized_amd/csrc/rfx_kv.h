@@ -91,6 +91,10 @@ struct AttnArgs {
     float *stat;       // [unit][split][rows][2] their maxima and sums
 };
 
+// The two-group prefill kernel: rows of a block, and the page ids that its
+// LDS holds (for 64 keys one of each page they touch).
+constexpr int kPairRows = 256, kPairIds = 4096;
+
 int attn_decode_launch(const AttnArgs &a, int type, int row_tiles, hipStream_t st);
 int attn_prefill_launch(const AttnArgs &a, int type, hipStream_t st);
 int attn_join_launch(const AttnArgs &a, int type, int64_t units, hipStream_t st);

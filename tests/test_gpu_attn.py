@@ -266,3 +266,94 @@ def test_cache_past_32_bit_offsets():
         n = R.attn_workspace_bytes(cache, batch, 16)
         R.attn(q[lo:hi].cuda(), cache, batch, o, 0.1, 0, 0, torch.zeros(max(n, 1), dtype=torch.uint8, device="cuda"))
         assert ((o.cpu().double() - ref[lo:hi]).abs() <= tol[lo:hi]).all()
+
+
+# Calls of 512 and more blocks of 256 rows, heads over 64: the kernel of two
+# wave groups. Rows over blocks, groups and waves
+# that are full, partial and empty; pages from one token to 128.
+MANY = [
+    ([(40, 40)] * 61 + [(300, 300), (0, 70), (33, 500)], 8, 8, 128, 16, 0, 0),
+    ([(33, 33 + 7 * i) for i in range(64)], 8, 8, 72, 64, 0, 0),
+    ([(35, 100 + 3 * i) for i in range(64)], 8, 8, 128, 1, 50, 3),
+    ([(70, 70 + i) for i in range(66)], 16, 8, 96, 32, 30, 0),
+    ([(200, 200), (1, 600), (257, 400), (64, 64)] + [(40, 300)] * 252, 2, 2, 128, 128, 129, 70),
+]
+# The same with split keys: tables of a capacity (more entries than needed)
+# that makes long runs.
+MANY_SPLIT = [
+    ([(40, 600)] * 32, 8, 8, 128, 64, 0, 0, 130),
+    ([(33, 900 - 9 * i) for i in range(64)], 4, 4, 80, 32, 0, 2, 260),
+    ([(70, 2000), (300, 1500)], 8, 4, 128, 128, 700, 90, 680),
+]
+
+
+@pytest.mark.parametrize("kind,out", [("bf16", "same"), ("bf16", "f32"), ("f16", "same"), ("f16", "f32")])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_two_groups(case, kind, out):
+    lens, heads, kv, dim, page, window, sinks = MANY[case]
+    check(lens, heads, kv, dim, page, kind, window, sinks, out=out, seed=300 + case, lead=case % 2, tail=case % 3)
+
+
+@pytest.mark.parametrize("kind,out", [("bf16", "same"), ("f16", "f32")])
+@pytest.mark.parametrize("case", range(len(MANY_SPLIT)))
+def test_two_groups_split_and_joined(case, kind, out):
+    lens, heads, kv, dim, page, window, sinks, more = MANY_SPLIT[case]
+    b, q, o = check(lens, heads, kv, dim, page, kind, window, sinks, out=out, seed=400 + case, extra_entries=more)
+    assert R.attn_workspace_bytes(b.cache, b.batch, heads) > 0
+    assert torch.equal(run(b, q, dim ** -0.5, window, sinks, out), o), "two runs differ"
+
+
+@pytest.mark.parametrize("page", [2, 16, 64, 128])
+def test_two_groups_bad_pages_and_nan(page):
+    """Bad page ids mask their keys, and what no row sees may be NaN, where
+    blocks of both groups are at work; two runs agree."""
+    need_gpu()
+    b = Batch([(34, 234)] * 64, page, 8, 128, "bf16", seed=21)
+    stride = b.table.shape[1]
+    for s in range(64):
+        for j in range(s % 3, stride, 3 + s % 2):
+            b.table[s, j] = (-1, b.n_pages, 1 << 30)[j % 3]
+    q = torch.randn((34 * 64, 8, 128), generator=torch.Generator().manual_seed(6)).to(b.dtype)
+    o = run(b, q, 0.1, window=60, sinks=5)
+    assert torch.equal(o, run(b, q, 0.1, window=60, sinks=5))
+    for s in range(0, 64, 7):
+        good = [(int(b.table[s, p // page]), p % page) if 0 <= int(b.table[s, p // page]) < b.n_pages else None for p in range(234)]
+        for i in (0, 15, 33):
+            pos = 200 + i
+            keys = [good[p] for p in range(pos + 1) if good[p] and (p > pos - 60 or p < 5)]
+            for h in (0, 7):
+                if not keys:
+                    assert not o[34 * s + i, h].any()
+                    continue
+                k = torch.stack([b.k[a, h, c] for a, c in keys]).double()
+                v = torch.stack([b.v[a, h, c] for a, c in keys]).double()
+                w = torch.softmax(k @ q[34 * s + i, h].double() * 0.1, 0)
+                # weights to 2^-15 (scores below 10, 128 products, 65 keys: see attn_bound)
+                assert ((o[34 * s + i, h].double() - w @ v).abs() <= 2.0 ** -15 * (w @ v.abs())).all(), (s, i, h)
+
+
+def test_two_groups_replayed():
+    """Captured and replayed while sequences shrink, against eager calls."""
+    need_gpu()
+    b = Batch([(40, 700)] * 64, 32, 8, 128, "f16", seed=22)
+    q = torch.randn((b.n_tokens, 8, 128), generator=torch.Generator().manual_seed(8)).to(b.dtype).cuda()
+    cache, batch = b.device(R)
+    og, oe = (torch.empty(q.shape, dtype=torch.float16, device="cuda") for _ in range(2))
+    n = R.attn_workspace_bytes(cache, batch, 8)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda") if n else None
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        R.attn(q, cache, batch, og, 0.1, 0, 0, ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        R.attn(q, cache, batch, og, 0.1, 0, 0, ws)
+    for i in range(4):
+        batch.kv_len.copy_((b.kv_len.cuda() - 150 * i).to(torch.int32))
+        R.attn(q, cache, batch, oe, 0.1, 0, 0, ws)
+        torch.cuda.synchronize()
+        og.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(og, oe), i
