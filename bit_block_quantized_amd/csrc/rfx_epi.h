@@ -23,7 +23,7 @@ namespace dev {
 __device__ __forceinline__ float activate(float z, int act)
 {
     switch (act) {
-    case RFX_ACT_RELU: return z > 0.0f ? z : 0.0f;
+    case RFX_ACT_RELU: return z <= 0.0f ? 0.0f : z; // NaN stays NaN
     case RFX_ACT_SILU: return z / (1.0f + expf(-z));
     case RFX_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
     case RFX_ACT_GELU_TANH: return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));

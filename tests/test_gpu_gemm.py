@@ -227,3 +227,14 @@ def test_fp4_scale_that_is_not_finite(value):
     keep = [j for j in range(20) if j != 3]
     tol = 1.13 * 2.0 ** -24 * (512 // 32 + 2) * c.mag + 1e-30
     assert (np.abs(y - c.z) <= tol)[keep].all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("q", [2, 40])
+def test_nan_reaches_the_result(act, q):
+    """A NaN before the activation is one after it, in its row only."""
+    need_gpu()
+    c = Case(4, q, 70, 512, seed=4)
+    c.bias[9] = np.nan
+    y = c.run(act, True)
+    assert np.isnan(y[:, 9]).all() and np.isfinite(np.delete(y, 9, 1)).all()
