@@ -581,6 +581,8 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
     op = _want(out, "out", out.dtype, shape, dev)
     if batch.index != dev:
         raise ValueError(f"batch on GPU {batch.index}, the cache is on GPU {dev}")
+    if window > 0x7fffffff or sinks > 0x7fffffff: # the C call's int would wrap
+        raise ValueError(f"window {window}, sinks {sinks}: below 2^31")
     wp, wn = None, 0
     if ws is not None:
         if ws.get_device() != dev:

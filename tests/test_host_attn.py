@@ -133,3 +133,13 @@ def test_binding_checks_tensors():
 def test_rope_inv_freq():
     f = R.rope_inv_freq(8, 16.0)
     assert f.tolist() == [1.0, 0.5, 0.25, 0.125]
+
+
+def test_binding_refuses_windows_past_32_bits():
+    c = R.DeviceKVCache(*(torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16) for _ in range(2)))
+    b = R.KVBatch(torch.tensor([0, 1], dtype=torch.int32), torch.tensor([1], dtype=torch.int32),
+                  torch.zeros(1, 4, dtype=torch.int32), 1, 1)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    for kw in (dict(window=1 << 32), dict(window=5, sinks=(1 << 31) + 7)):
+        with pytest.raises(ValueError, match="below 2"):
+            R.attn(q, c, b, torch.zeros(1, 4, 64), 0.125, **kw)
