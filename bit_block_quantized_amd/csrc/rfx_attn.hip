@@ -60,20 +60,25 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int quads = a.rows / 4, unit = blockIdx.x >> __builtin_ctz(quads), r = (blockIdx.x & (quads - 1)) * 4 + wave;
     const int u = kv.div_hk(unit), hk = kv.div_hk.rem(unit, u), seq = a.div_rb(u), rb = a.div_rb.rem(u, seq);
+    // The first partials and the statistics of all splits are read before it
+    // is known how many there are, beside the lengths (one round trip to
+    // memory where each waiting for the one before made three). What no split
+    // wrote may be anything and is selected away, not multiplied.
+    const size_t slot = (size_t)unit * a.S * a.rows + r;
+    const float *p = a.part + slot * DP + PER * lane;
+    const size_t stride = (size_t)a.rows * DP;
+    const f2 any = *reinterpret_cast<const f2 *>(a.stat + (slot + (size_t)min(lane, a.S - 1) * a.rows) * 2);
+    fp x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        x[i] = *reinterpret_cast<const fp *>(p + min(i, a.S - 1) * stride);
     const Seq sq = load_seq(kv, seq);
     const int nrows = sq.nq * kv.G, row0 = rb * a.rows, row = row0 + r;
-    if (row >= nrows)
-        return;
     const int row_end = min(nrows, row0 + a.rows);
-    const KeyTiles kt = key_tiles(a.bn, sq.p0 + kv.div_g(row0), sq.p0 + kv.div_g(row_end - 1), sq.kv, a.window, a.sinks);
+    const KeyTiles kt = key_tiles(a.bn, sq.p0 + kv.div_g(row0), sq.p0 + kv.div_g(max(0, row_end - 1)), sq.kv, a.window, a.sinks);
     int per, active;
     split_tiles(a, kt.n, per, active);
-    if (active == 1)
-        return;
-    const size_t slot = (size_t)unit * a.S * a.rows + r;
-    f2 st = {-INFINITY, 0.f};
-    if (lane < active)
-        st = *reinterpret_cast<const f2 *>(a.stat + (slot + (size_t)lane * a.rows) * 2);
+    const f2 st = {lane < active ? any.x : -INFINITY, lane < active ? any.y : 0.f};
     float m = st.x;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
@@ -87,21 +92,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
 #pragma unroll
     for (int i = 0; i < PER; i++)
         sum[i] = 0.f;
-    const float *p = a.part + slot * DP + PER * lane;
-    const size_t stride = (size_t)a.rows * DP;
-    // eight partials' loads at a time; past the last, the last again with
-    // factor zero
     for (int s = 0; s < active; s += 8) {
-        fp x[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            x[i] = *reinterpret_cast<const fp *>(p + min(s + i, active - 1) * stride);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const float w = s + i < active ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(s + i, 63))) : 0.f;
-            sum += x[i] * w;
+            const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(s + i, 63)));
+            if (s + i < active)
+                sum += x[i] * w;
         }
+        // eight partials' loads at a time; past the last, the last again
+        if (s + 8 < active)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x[i] = *reinterpret_cast<const fp *>(p + min(s + 8 + i, active - 1) * stride);
     }
+    if (row >= nrows || active == 1)
+        return;
     const int d = PER * lane;
     if (d >= kv.D)
         return;

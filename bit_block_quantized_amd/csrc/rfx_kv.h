@@ -201,14 +201,6 @@ __device__ __forceinline__ u2 lds_read_tr(const char *p)
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uint32_t)(uintptr_t)p));
 }
 
-// A direct load into LDS: lane l's 16 bytes land at dst + 16 l.
-__device__ __forceinline__ void lds_load16(const void *src, void *dst)
-{
-    typedef const __attribute__((address_space(1))) void *gptr;
-    typedef __attribute__((address_space(3))) void *lptr;
-    __builtin_amdgcn_global_load_lds((gptr)(uintptr_t)src, (lptr)(uint32_t)(uintptr_t)dst, 16, 0, 0);
-}
-
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // One sequence as a workgroup sees it. nq new tokens (rows t0 ..), the first
