@@ -242,7 +242,10 @@ struct Plan {
 // Columns per workgroup: the fewest 16-column tiles (1, 2, 4 or 8) that take
 // all columns, so that few columns keep registers and LDS for more
 // workgroups. K is split until every compute unit has one workgroup (two
-// below eight tiles), but not below two K tiles each.
+// below eight tiles), down to one K tile each, FP4 to two where it has more
+// than four: in us, one and two tiles each, FP3 1024 x 1024 with 6 and 200
+// columns 11.4 and 13.3, 18.7 and 23.9, 4096 x 4096 with 64 22.8 and 24.4;
+// FP4 1024 x 1024 with 64 12.9 and 14.2, but 4096 x 4096 with 64 20.1 and 18.4.
 GemmShape f16_shape(int tiles)
 {
     const int nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
@@ -259,7 +262,8 @@ Plan plan(int fmt, int64_t N, int64_t K, int q)
     p.qp = p.col_blocks * p.g.tiles * 16;
     const int64_t blocks = (int64_t)p.row_blocks * p.col_blocks, S = ceil_div(K, kTileCols);
     int64_t splits = p.g.want / blocks;
-    splits = splits > S / 2 ? S / 2 : splits;
+    const int64_t most = fmt == RFX_FP4 && S > 4 ? S / 2 : S;
+    splits = splits > most ? most : splits;
     p.splits = (int)(splits < 1 ? 1 : splits);
     p.N4 = (int)((N + 3) / 4 * 4);
     p.xh = align256((size_t)(p.qp / 16) * S * p.g.frag);
