@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -492,6 +493,7 @@ class DeviceKVCache:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n_pages, n_kv_heads, page_size, head_dim
         self.c = KVCacheC(_elem(k.dtype), n_kv_heads, head_dim, page_size, n_pages, 0,
                           _want(k, "k", k.dtype, k.shape, self.index), _want(v, "v", k.dtype, k.shape, self.index))
+        self.c_ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -519,6 +521,7 @@ class KVBatch:
         self.c = KVBatchC(n_seq, n_tokens, max_q, stride, _want(q_off, "q_off", i32, (n_seq + 1,), dev),
                           _want(kv_len, "kv_len", i32, (n_seq,), dev),
                           _want(page_table, "page_table", i32, (n_seq, stride), dev))
+        self.c_ref = ctypes.byref(self.c)
 
     def ref(self):
         return ctypes.byref(self.c)
@@ -533,14 +536,29 @@ def rope_inv_freq(rot_dim, base=10000.0):
 def _head_rows(t, name, shape, index):
     """Address and row stride of float32 [n_tokens][heads][dim]; rows may be
     part of longer ones (a fused projection's output)."""
-    row, head, one = t.stride()
     if t.dtype is not _Torch.f32 or t.shape != shape:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, float32 {shape} wanted")
-    if one != 1 or (head != shape[2] and shape[1] > 1):
-        raise ValueError(f"{name}: heads of a row are not contiguous (strides {t.stride()})")
     if t.get_device() != index:
         raise ValueError(f"{name}: on {t.device}, not GPU {index}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
+    row, head, one = t.stride()
+    if one != 1 or (head != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: heads of a row are not contiguous (strides {t.stride()})")
     return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _want_vec(t, name, dtype, n, index):
+    """Address of n contiguous elements, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
+    return _want(t, name, dtype, (n,), index)
+
+
+# rfx_qk_rope, packed in one go: a ctypes structure's fields cost twice as much
+_pack_qk_rope = struct.Struct("3P3q3Pf3i").pack
 
 
 def qk_norm_rope(q, k, v, cache: DeviceKVCache, batch: KVBatch, q_out, inv_freq, q_weight=None, k_weight=None,
@@ -551,17 +569,18 @@ def qk_norm_rope(q, k, v, cache: DeviceKVCache, batch: KVBatch, q_out, inv_freq,
     [rot_dim / 2] (see rope_inv_freq); weights float32 [head_dim] or None."""
     T, D, Hk, dev = batch.n_tokens, cache.head_dim, cache.n_kv_heads, cache.index
     Hq = q.shape[1]
+    kv_shape = (T, Hk, D)
     qp, qs = _head_rows(q, "q", (T, Hq, D), dev)
-    kp, ks = _head_rows(k, "k", (T, Hk, D), dev)
-    vp, vs = _head_rows(v, "v", (T, Hk, D), dev)
+    kp, ks = _head_rows(k, "k", kv_shape, dev)
+    vp, vs = _head_rows(v, "v", kv_shape, dev)
     if batch.index != dev:
         raise ValueError(f"batch on GPU {batch.index}, the cache is on GPU {dev}")
-    half = inv_freq.shape[0]
-    args = QkRopeC(qp, kp, vp, qs, ks, vs, _want(inv_freq, "inv_freq", _Torch.f64, (half,), dev),
-                   None if q_weight is None else _want(q_weight, "q_weight", _Torch.f32, (D,), dev),
-                   None if k_weight is None else _want(k_weight, "k_weight", _Torch.f32, (D,), dev),
-                   eps, Hq, 2 * half, interleaved)
-    _call_on(dev, stream, lib().rfx_qk_norm_rope, ctypes.byref(args), cache.ref(), batch.ref(),
+    half = inv_freq.numel()
+    f32 = _Torch.f32
+    args = _pack_qk_rope(qp, kp, vp, qs, ks, vs, _want_vec(inv_freq, "inv_freq", _Torch.f64, half, dev),
+                         _want_vec(q_weight, "q_weight", f32, D, dev), _want_vec(k_weight, "k_weight", f32, D, dev),
+                         eps, Hq, 2 * half, interleaved)
+    _call_on(dev, stream, lib().rfx_qk_norm_rope, args, cache.c_ref, batch.c_ref,
              _want(q_out, "q_out", cache.dtype, (T, Hq, D), dev))
 
 
@@ -588,7 +607,7 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
         if ws.get_device() != dev:
             raise ValueError(f"ws: on {ws.device}, not GPU {dev}")
         wp, wn = ws.data_ptr(), ws.nbytes
-    _call_on(dev, stream, lib().rfx_attn, qp, cache.ref(), batch.ref(), Hq, scale, window, sinks, op, _elem(out.dtype),
+    _call_on(dev, stream, lib().rfx_attn, qp, cache.c_ref, batch.c_ref, Hq, scale, window, sinks, op, _elem(out.dtype),
              wp, wn)
 
 

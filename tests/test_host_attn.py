@@ -143,3 +143,9 @@ def test_binding_refuses_windows_past_32_bits():
     for kw in (dict(window=1 << 32), dict(window=5, sinks=(1 << 31) + 7)):
         with pytest.raises(ValueError, match="below 2"):
             R.attn(q, c, b, torch.zeros(1, 4, 64), 0.125, **kw)
+
+
+def test_packed_rope_arguments_are_the_structure():
+    a = rope(q_stride=520, k_stride=136, v_stride=144, eps=1e-5, n_heads=12, rot_dim=40, interleaved=True)
+    packed = R._pack_qk_rope(P, P, P, 520, 136, 144, P, P, 0, 1e-5, 12, 40, True)
+    assert packed == bytes(a) and len(packed) == ctypes.sizeof(R.QkRopeC)
