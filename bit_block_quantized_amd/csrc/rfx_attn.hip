@@ -155,8 +155,8 @@ struct Plan {
 // wants two workgroups per compute unit in turn or long runs of key tiles:
 // it starts and ends slower, alone on its compute unit. Measured in us, 32
 // heads of 128 over 8, against the four-wave kernel: 8192 tokens (1024
-// workgroups) 528 and 586, 4096 (512) 156 and 171, 1000 after 30000 (four
-// splits of 121 tiles) 494 and 547; but 2048 (256) 90 and 69, 256 after
+// workgroups) 500 and 586, 4096 (512) 145 and 171, 1000 after 30000 (four
+// splits of 121 tiles) 466 and 547; but 2048 (256) 90 and 69, 256 after
 // 8000 (sixteen splits of 9 tiles) 62 and 57. Its list of page ids has to
 // fit the LDS.
 bool pair_rows(const rfx_kv_cache *C, const rfx_kv_batch *B, int64_t rows, int dp)

@@ -22,8 +22,6 @@
 // that type (its own rounding is as large), and the row sums are of the
 // rounded ones; for an fp32 result they are carried as the sum of TERMS
 // values, and the sums are of the fp32 weights.
-#include <type_traits>
-
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -322,13 +320,16 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
 // half a tile apart. While one group's waves run the products of PV (tile j)
 // and QK (tile j + 1) with the tiles' staging between them, the other's run
 // the softmax of theirs, so that the matrix and the vector pipe of a SIMD
-// have one wave each; a barrier ends every phase. The staging of a key tile
-// serves twice the rows. 8192 tokens of 32 heads of 128 over 8, bf16: 527 us
-// (1040 TFLOP/s), 586 with the kernel above, whose two waves per SIMD meet
-// on the same pipe as often as not. A phase takes about 1850 cycles where
-// its products alone take 1024: the product wave's other 120 instructions
-// and its first reads of LDS (150 cycles) do not all fit beside them, and a
-// wave on its own issues a vector operation every eight cycles.
+// have one wave each; a barrier ends every phase. A key tile's staging serves
+// twice the rows. Three buffers: a tile is in LDS a tile ahead of its
+// products, so that their first operands are read during the softmax before
+// (514 us with two buffers and those reads at the start of the products).
+// 8192 tokens of 32 heads of 128 over 8, bf16: 500 us (1100 TFLOP/s), 586 with
+// the kernel above, whose two waves per SIMD meet on the same pipe as often
+// as not. Where the staging and the packing of weights stand, and a shorter
+// path for tiles without a mask, move this by less than 1 %: it is near the
+// power that bounds the products alone (a large library product reaches 1371
+// TFLOP/s).
 __device__ __forceinline__ void phase_end()
 {
     asm volatile("" ::: "memory");
@@ -345,7 +346,7 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
     constexpr int DP = 128;
     using L = Tile<DP, 512>;
     constexpr int BN = L::BN, NC = DP / 16, ND = DP / 32, NK = BN / 32, ROWS = kPairRows;
-    __shared__ __align__(16) char smem[2 * L::buf];
+    __shared__ __align__(16) char smem[3 * L::buf];
     __shared__ int s_ids[kPairIds];  // page ids of the tiles, `ept` each, 0 for unusable ones
     __shared__ unsigned s_bad[kPairIds / 32]; // a bit for each of those
     __shared__ unsigned s_any_bad;
@@ -459,23 +460,23 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
         }
     };
     char *const kbase = smem, *const vbase = smem + BN * L::KP;
-    const auto store_rows = [&](char *base, int pitch, int j, const u4 (&x)[L::NL]) { // into its buffer, j & 1
+    const auto store_rows = [&](char *base, int pitch, const u4 (&x)[L::NL]) {
 #pragma unroll
         for (int i = 0; i < L::NL; i++)
-            *reinterpret_cast<u4 *>(base + (j & 1) * L::buf + (i * L::KPI + skey) * pitch + 16 * sch) = x[i];
+            *reinterpret_cast<u4 *>(base + (i * L::KPI + skey) * pitch + 16 * sch) = x[i];
     };
-    // Staging beside the products of tile j: keys of j + 1 and values of j
-    // to LDS, the next ones' loads.
+    // Tile j lives in buffer j % 3. Staging beside the products of tile j:
+    // keys of j + 2 and values of j + 1 to LDS, the next ones' loads.
     const auto stage_clear = [&](int j) {
-        clear_rows(j + 1, kx);
-        clear_rows(j, vx);
+        clear_rows(j + 2, kx);
+        clear_rows(j + 1, vx);
     };
-    const auto stage = [&](int j, int part) {
+    const auto stage = [&](int j, int part, int kbuf, int vbuf) {
         if (part == 0)
-            store_rows(kbase, L::KP, j + 1, kx);
+            store_rows(kbase + kbuf, L::KP, kx);
         if (part == 1) {
-            store_rows(vbase, L::VP, j, vx);
-            read_ids(j + 2);
+            store_rows(vbase + vbuf, L::VP, vx);
+            read_ids(j + 3);
         }
         if (part == 2) {
 #pragma unroll
@@ -484,21 +485,21 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
             load_values();
         }
         if (part == 3)
-            load_keys(j + 2);
+            load_keys(j + 3);
     };
 
     f32x16 s[NK];
     u4 pt[2][TERMS];
     // Fragments are read one step of four products ahead.
     u4 fr[2][4];
-    const auto read_k = [&](int j, int st, u4 (&f)[4]) {
-        const char *kb = kbase + (j & 1) * L::buf + r32 * L::KP + 16 * hl;
+    const auto read_k = [&](int buf, int st, u4 (&f)[4]) {
+        const char *kb = kbase + buf + r32 * L::KP + 16 * hl;
 #pragma unroll
         for (int i = 0; i < 4; i++)
             f[i] = *reinterpret_cast<const u4 *>(kb + 32 * (i & 1) * L::KP + 32 * (2 * st + (i >> 1)));
     };
-    const auto read_v = [&](int j, int st, u4 (&f)[4]) {
-        const char *vr = vbase + (j & 1) * L::buf + (16 * st + 4 * hl + (i16 >> 2)) * L::VP + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
+    const auto read_v = [&](int buf, int st, u4 (&f)[4]) {
+        const char *vr = vbase + buf + (16 * st + 4 * hl + (i16 >> 2)) * L::VP + 32 * ((lane >> 4) & 1) + 8 * (i16 & 3);
 #pragma unroll
         for (int i = 0; i < ND; i++) {
             const u2 x = lds_read_tr(vr + 64 * i), y = lds_read_tr(vr + 8 * L::VP + 64 * i);
@@ -514,7 +515,9 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    const auto scores = [&](int j) { // read_k(j, 0, fr[0]) is done
+    // Tile j's, with its staging (to the keys' buffer kbuf and the values'
+    // vbuf); read_k(buf, 0, fr[0]) is done.
+    const auto scores = [&](int buf, int j, int kbuf, int vbuf) {
 #pragma unroll
         for (int k = 0; k < NK; k++)
 #pragma unroll
@@ -523,10 +526,11 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
 #pragma unroll
         for (int st = 0; st < NC / 2; st++) {
             if (st + 1 < NC / 2)
-                read_k(j, st + 1, fr[~st & 1]);
+                read_k(buf, st + 1, fr[~st & 1]);
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 s[i & 1] = T::mma32(fr[st & 1][i], qf[2 * st + (i >> 1)], s[i & 1]);
+            stage(j, st, kbuf, vbuf);
             mix(4);
         }
     };
@@ -594,19 +598,15 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
                 s[k][v] = fast_exp2(fmaf(a.c, s[k][v], off));
         pack(0);
     };
-    // staged: with tile j + 1's staging
-    const auto results = [&](int j, auto staged) {
-        read_v(j, 0, fr[0]);
-        __builtin_amdgcn_sched_barrier(0);
+    // Tile j's, buffer b0, the next tile's b1; read_v(b0, 0, fr[0]) is done.
+    const auto results = [&](int b0, int b1) {
 #pragma unroll
         for (int st = 0; st < 2 * NK; st++) {
             if (st + 1 < 2 * NK) {
-                read_v(j, st + 1, fr[~st & 1]);
+                read_v(b0, st + 1, fr[~st & 1]);
                 pack(st + 1);
             } else
-                read_k(j + 1, 0, fr[0]); // for the scores that follow (at the end: of the other buffer, unused)
-            if constexpr (decltype(staged)::value)
-                stage(j + 1, st);
+                read_k(b1, 0, fr[0]); // for the scores that follow (at the end unused)
 #pragma unroll
             for (int i = 0; i < ND; i++)
 #pragma unroll
@@ -617,39 +617,47 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
     };
 
     if (n > 0) {
-        const auto stage_all = [&](int j) {
-#pragma unroll
-            for (int part = 0; part < 4; part++)
-                stage(j, part);
-        };
+        int b0 = 0, b1 = L::buf, b2 = 2 * L::buf;
         read_ids(0);
         load_keys(0);
         clear_rows(0, kx);
-        store_rows(kbase, L::KP, 0, kx);
-        stage(-1, 2);
+        store_rows(kbase + b0, L::KP, kx);
+        stage(-2, 2, 0, 0); // values of tile 0
         read_ids(1);
         load_keys(1);
+        clear_rows(0, vx);
+        store_rows(vbase + b0, L::VP, vx);
+        clear_rows(1, kx);
+        store_rows(kbase + b1, L::KP, kx);
+        stage(-1, 2, 0, 0); // values of tile 1
+        read_ids(2);
+        load_keys(2);
         phase_end();
         if (grp) // group 1 runs one phase behind
             phase_end();
         stage_clear(0);
-        stage_all(0);
-        read_k(0, 0, fr[0]);
-        scores(0);
+        read_k(b0, 0, fr[0]);
+        scores(b0, 0, b2, b1);
         for (int j = 0; j + 1 < n; j++) {
             phase_end();
+            read_v(b0, 0, fr[0]);
             weights(j);
             stage_clear(j + 1);
             phase_end();
             __builtin_amdgcn_s_setprio(1);
-            results(j, std::true_type());
-            scores(j + 1);
+            results(b0, b1);
+            scores(b1, j + 1, b0, b2);
             __builtin_amdgcn_s_setprio(0);
+            const int t = b0;
+            b0 = b1;
+            b1 = b2;
+            b2 = t;
         }
         phase_end();
+        read_v(b0, 0, fr[0]);
         weights(n - 1);
         phase_end();
-        results(n - 1, std::false_type());
+        results(b0, b1);
         if (grp == 0)
             phase_end();
     }
