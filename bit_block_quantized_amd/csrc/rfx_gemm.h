@@ -28,7 +28,7 @@ struct GemmArgs {
 struct GemmShape {
     int rows, tiles, frag, scale, want;
 };
-GemmShape gemm_mx_shape(int64_t N, int tiles);
+GemmShape gemm_mx_shape(int64_t N, int64_t S, int tiles);
 
 int gemm_mx_launch(const GemmArgs &a, const GemmShape &g, const int8_t *xq, const float *xs, int nb, hipStream_t st);
 

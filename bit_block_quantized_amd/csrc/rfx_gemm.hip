@@ -241,14 +241,19 @@ struct Plan {
 
 // Columns per workgroup: the fewest 16-column tiles (1, 2, 4 or 8) that take
 // all columns, so that few columns keep registers and LDS for more
-// workgroups. K is split until every compute unit has one workgroup (two
+// workgroups; fewer where even one K tile each would leave a quarter of the
+// compute units idle (us, fewer and fewest: FP3 1024 x 1024 with 64 and 200
+// columns 12.0 and 15.7, 13.3 and 18.7; FP4 2048 x 2048 with 64 12.0 and
+// 15.6; FP3 7168 x 2048 with 32, 224 workgroups, 18.7 and 15.8). K is split until every compute unit has one workgroup (two
 // below eight tiles), down to one K tile each, FP4 to two where it has more
 // than four: in us, one and two tiles each, FP3 1024 x 1024 with 6 and 200
 // columns 11.4 and 13.3, 18.7 and 23.9, 4096 x 4096 with 64 22.8 and 24.4;
 // FP4 1024 x 1024 with 64 12.9 and 14.2, but 4096 x 4096 with 64 20.1 and 18.4.
-GemmShape f16_shape(int tiles)
+GemmShape f16_shape(int64_t N, int64_t S, int tiles)
 {
-    const int nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+    int nt = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+    while (nt > 1 && ceil_div(N, kRows) * ceil_div(tiles, nt) * S < 192)
+        nt /= 2;
     return {kRows, nt, 8 * 1024, 8 * 64, nt == 8 ? 256 : 512};
 }
 
@@ -256,11 +261,12 @@ Plan plan(int fmt, int64_t N, int64_t K, int q)
 {
     Plan p{};
     const int tiles = (q + 15) / 16;
-    p.g = fmt == RFX_FP4 ? gemm_mx_shape(N, tiles) : f16_shape(tiles);
+    const int64_t S = ceil_div(K, kTileCols);
+    p.g = fmt == RFX_FP4 ? gemm_mx_shape(N, S, tiles) : f16_shape(N, S, tiles);
     p.row_blocks = (int)ceil_div(N, p.g.rows);
     p.col_blocks = (tiles + p.g.tiles - 1) / p.g.tiles;
     p.qp = p.col_blocks * p.g.tiles * 16;
-    const int64_t blocks = (int64_t)p.row_blocks * p.col_blocks, S = ceil_div(K, kTileCols);
+    const int64_t blocks = (int64_t)p.row_blocks * p.col_blocks;
     int64_t splits = p.g.want / blocks;
     const int64_t most = fmt == RFX_FP4 && S > 4 ? S / 2 : S;
     splits = splits > most ? most : splits;

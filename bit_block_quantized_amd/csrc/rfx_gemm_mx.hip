@@ -268,12 +268,15 @@ void launch(const GemmArgs &a, hipStream_t st)
 namespace rfx {
 
 // 512 rows per workgroup where they still occupy three quarters of the
-// compute units: 2048 columns of 4096 x 7168 (256 workgroups) took 164 us
+// compute units (fewer columns where not even one K tile each fills them,
+// as in the f16 form): 2048 columns of 4096 x 7168 (256 workgroups) took 164 us
 // against 187 with 256 rows, 1024 of 7168 x 2048 (224) 54 against 63, but 512
 // of it (112) 42 against 34 and 1024 of 4096 x 7168 (128) 99 against 97.
-GemmShape gemm_mx_shape(int64_t N, int tiles)
+GemmShape gemm_mx_shape(int64_t N, int64_t S, int tiles)
 {
-    const int ct = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;
+    int ct = tiles <= 1 ? 1 : tiles <= 2 ? 2 : 4;
+    while (ct > 1 && ceil_div(N, 256) * ceil_div(tiles, ct) * S < 192)
+        ct /= 2;
     const bool tall = ct == 4 && ceil_div(N, 512) * ((tiles + 3) / 4) >= 192;
     return {tall ? 512 : ct == 1 ? 128 : 256, ct, kFragBytes, kScaleBytes, ct == 4 ? 256 : 512};
 }

@@ -238,3 +238,17 @@ def test_nan_reaches_the_result(act, q):
     c.bias[9] = np.nan
     y = c.run(act, True)
     assert np.isnan(y[:, 9]).all() and np.isfinite(np.delete(y, 9, 1)).all()
+
+
+@pytest.mark.parametrize("fmt", [2, 3, 4])
+@pytest.mark.parametrize("q,rows,cols", [(30, 2900, 4192), (64, 2100, 5600), (100, 1300, 4128), (260, 1100, 3200),
+                                         (1400, 4100, 64)])
+def test_many_columns_that_fill_the_device(fmt, q, rows, cols):
+    """Sizes at which workgroups take 32 to 128 columns (smaller matrices
+    take fewer per workgroup), and FP4's 512 rows."""
+    need_gpu()
+    say(f"gemm fmt={fmt} q={q} {rows}x{cols}")
+    c = Case(fmt, q, rows, cols, seed=q)
+    c.check(c.run())
+    act = ACTS[q % 5]
+    c.check(c.run(act, True, True), act, True, True)
