@@ -188,9 +188,12 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
     // six splits and 11.3 unsplit; 49 tiles 9.8 as 13 splits, 10.6 as seven.
     // Prompt chunks of 300 new tokens: 5 tiles (of 64) 15.5 unsplit, 20.2 split.
     p.min_tiles = p.decode ? 4 : 2;
-    p.one_tiles = p.decode ? 16 : 6;
-    const int64_t tiles = ceil_div((int64_t)B->table_stride * C->page_size, p.bn);
+    // The join reads every row of every split: 256 new tokens after 200 (64
+    // units, 8 tiles) 20.4 unsplit and 27.0 as four splits, 12 after 500 (8
+    // units, 8 tiles) 17.9 and 12.2.
     p.units = (int64_t)B->n_seq * C->n_kv_heads * p.row_blocks;
+    p.one_tiles = p.decode ? 16 : p.units >= 64 ? 8 : 6;
+    const int64_t tiles = ceil_div((int64_t)B->table_stride * C->page_size, p.bn);
     const int64_t want = 2 * 256 / (p.units < 512 ? p.units : 512);
     const int64_t most = tiles <= p.one_tiles ? 1 : ceil_div(tiles, p.min_tiles);
     p.S = (int)(want < most ? want : most);
