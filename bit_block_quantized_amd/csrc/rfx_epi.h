@@ -3,11 +3,17 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "rfx.h"
 
 namespace rfx {
+
+// The split-K exchange slots that a single GEMV needs at most: row groups x
+// (splits - 1) x 4 columns x 256 bytes, which is 329 KiB (47 groups, eight
+// splits); rfx_gemv.hip checks it against the split rule.
+constexpr size_t kGemvSlotBytes = 384u << 10;
 
 struct EpiArgs {
     const float *bias;  // [N] or null

@@ -227,9 +227,8 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs a)
     finish_rows(a, sum, col, row, left, left >= 4 && a.vec);
 }
 
-// The first bytes of a workspace belong to the GEMV form's exchange slots,
-// which every call leaves zero; the rest needs no initialisation.
-constexpr size_t kSlotBytes = 256u << 10;
+// The first kGemvSlotBytes of a workspace belong to the GEMV form's exchange
+// slots, which every call leaves zero; the rest needs no initialisation.
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -275,7 +274,7 @@ Plan plan(int fmt, int64_t N, int64_t K, int q)
     p.xh = align256((size_t)(p.qp / 16) * S * p.g.frag);
     p.sx = align256((size_t)(p.qp / 16) * S * p.g.scale);
     p.part = p.splits > 1 ? align256((size_t)p.splits * q * p.N4 * 4) : 0;
-    p.bytes = kSlotBytes + p.xh + p.sx + p.part;
+    p.bytes = kGemvSlotBytes + p.xh + p.sx + p.part;
     return p;
 }
 
@@ -353,7 +352,7 @@ int rfx_gemm(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t
     a.splits = p.splits;
     a.qp = p.qp;
     a.N4 = p.N4;
-    char *w = static_cast<char *>(ws) + kSlotBytes;
+    char *w = static_cast<char *>(ws) + kGemvSlotBytes;
     a.xh = reinterpret_cast<const uint8_t *>(w);
     a.sx = w + p.xh;
     a.part = reinterpret_cast<float *>(w + p.xh + p.sx);

@@ -597,7 +597,7 @@ struct LaunchShape {
 
 // Enough waves to give every SIMD a few, each wave one to two tiles; split
 // K across workgroups only when the row groups alone cannot fill 256 CUs.
-LaunchShape choose_shape(int G, int S)
+constexpr LaunchShape choose_shape(int G, int S)
 {
     LaunchShape sh{1, 4};
     const int target_waves = 3072; // 1024 SIMDs x 3
@@ -613,12 +613,25 @@ LaunchShape choose_shape(int G, int S)
     return sh;
 }
 
-size_t workspace_for(int G, int P, int q)
+constexpr size_t workspace_for(int G, int P, int q)
 {
     if (P <= 1)
         return 0;
     return (size_t)G * (P - 1) * q * 64 * sizeof(unsigned);
 }
+
+// The most that any shape needs: from 256 row groups on K is not split, and
+// more tiles never mean fewer splits.
+constexpr size_t most_slot_bytes()
+{
+    size_t most = 0;
+    for (int G = 1; G <= 256; G++) {
+        const size_t n = workspace_for(G, choose_shape(G, 1 << 20).P, 4);
+        most = n > most ? n : most;
+    }
+    return most;
+}
+static_assert(choose_shape(256, 1 << 20).P == 1 && most_slot_bytes() <= kGemvSlotBytes, "a single GEMV's slots");
 
 template <int FMT, bool DOTS, bool FULL>
 int launch_q(const GemvArgs &a, int q, int G, int W, hipStream_t st)

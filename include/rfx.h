@@ -266,7 +266,7 @@ int rfx_gemv_grouped(const rfx_gemv_job *jobs, int n_jobs, void *ws, size_t ws_b
  * and may be y itself. y fp32 [q][N] overlaps no other argument.
  * ws: zero-filled workspace of rfx_gemm_workspace_bytes(W, q) bytes, 256-B
  * aligned (NULL allowed when that is 0). Calls of any W and q may use the
- * same one in turn: its first 256 KiB are left zero, the rest needs no
+ * same one in turn: its first 384 KiB are left zero, the rest needs no
  * initialisation and holds anything afterwards. Launches that share it must
  * not overlap. Results are deterministic (fixed-order sums).
  * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_UNSUPPORTED, RFX_E_WORKSPACE,

@@ -252,3 +252,17 @@ def test_many_columns_that_fill_the_device(fmt, q, rows, cols):
     c.check(c.run())
     act = ACTS[q % 5]
     c.check(c.run(act, True, True), act, True, True)
+
+
+@pytest.mark.parametrize("rows,cols", [(2560, 8192), (5632, 4096), (3008, 8192)])
+def test_workspace_shared_where_slots_are_many(rows, cols):
+    """The same where the GEMV form's exchange slots take the most: a call of
+    64 columns writes its operands behind them."""
+    need_gpu()
+    few, many = Case(4, 4, rows, cols, seed=1), Case(4, 64, rows, cols, seed=2)
+    ws = torch.zeros(max(R.gemm_workspace_bytes(c.dW, c.q) for c in (few, many)), dtype=torch.uint8, device="cuda")
+    first = few.run(ws=ws)
+    few.check(first)
+    for _ in range(2):
+        many.check(many.run(ws=ws))
+        assert np.array_equal(few.run(ws=ws), first)

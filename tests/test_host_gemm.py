@@ -80,3 +80,14 @@ def test_weights_on_another_device(monkeypatch):
         W.index = index
         R.gemm(W, P, P, P, 1, P, stream=stream)
     assert calls == [([3], 103), ([], 100), ([3], 7), ([], 100)]
+
+
+def test_slots_of_every_shape_fit_in_front_of_the_operands():
+    """A workspace's first part is the GEMV form's, whatever its shape: what a
+    call with more columns reserves in front of its operands (here one K tile
+    of one column tile, FP2: 8 KiB of codes and 512 bytes of scales) holds the
+    exchange slots of every matrix with four columns."""
+    reserved = need(5, fmt=2, rows=1, cols=32) - 8192 - 512
+    most = max(need(4, rows=rows, cols=cols) for rows in range(1, 64 * 400, 64) for cols in (512, 1024, 2048, 4096, 8192, 1 << 20))
+    assert most == 47 * 7 * 4 * 256
+    assert most <= reserved
