@@ -192,6 +192,10 @@ class DeviceAttention:
 
     def __init__(self, wq, wk, wv, wo, n_heads, n_kv_heads, head_dim, inv_freq, q_norm=None, k_norm=None, eps=1e-6,
                  interleaved=False, window=0, sinks=0, scale=None):
+        if n_kv_heads < 1 or n_heads < 1 or n_heads % n_kv_heads:
+            raise ValueError(f"{n_heads} heads over {n_kv_heads} kv heads")
+        if window < 0 or sinks < 0 or not eps >= 0 or not (scale is None or scale > 0):
+            raise ValueError(f"window {window}, sinks {sinks}, eps {eps}, scale {scale}")
         self.wq, self.wk, self.wv, self.wo = wq, wk, wv, wo
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, n_kv_heads, head_dim
         for W, rows, name in ((wq, n_heads, "wq"), (wk, n_kv_heads, "wk"), (wv, n_kv_heads, "wv")):
@@ -246,6 +250,7 @@ class AttentionBuffers:
         def zeros(n):
             return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
+        self.sizes = self._sizes(attn)
         self.x_act, self.o_act = act(H), act(O)
         self.q, self.k, self.v = (empty(T, h, D) for h in (attn.n_heads, attn.n_kv_heads, attn.n_kv_heads))
         self.q16 = empty(T, attn.n_heads, D, dtype=cache.dtype)
@@ -253,8 +258,11 @@ class AttentionBuffers:
         mats = (attn.wq, attn.wk, attn.wv, attn.wo)
         self.ws_gemm = zeros(max(gemm_workspace_bytes(W, T) for W in mats))
         self.ws_attn = zeros(attn_workspace_bytes(cache, batch, attn.n_heads))
-        if T <= 4:
-            self.ws_jobs = zeros(gemv_grouped_workspace_bytes(self._jobs(attn)))
+        self.ws_jobs = zeros(gemv_grouped_workspace_bytes(self._jobs(attn))) if T <= 4 else None
+
+    @staticmethod
+    def _sizes(attn):
+        return attn.hidden, attn.n_heads, attn.n_kv_heads, attn.head_dim
 
     def _jobs(self, attn):
         """Decode's query, key and value projections, one launch."""
@@ -265,21 +273,45 @@ class AttentionBuffers:
     def run(self, attn: DeviceAttention, x, cache, batch, resid=None, out=None, stream=None):
         """Projections, norm, rotation and cache append, attention, output
         projection for x (device fp32 [n_tokens][hidden]); y = resid +
-        Attention(x) lands in `out` (default self.y)."""
-        from . import _torch, _want
-        t, T, dev = _torch(), batch.n_tokens, cache.index
+        Attention(x) lands in `out` (default self.y). What does not fit these
+        buffers is refused before anything is launched."""
+        from . import _torch
+        t, dev = _torch(), cache.index
         y = self.y if out is None else out
-        if self.q.shape[0] != T:
-            raise ValueError(f"buffers for {self.q.shape[0]} tokens, the batch has {T}")
-        for name, a in (("x", x), ("out", y)) + ((("resid", resid),) if resid is not None else ()):
-            _want(a, name, t.f32, (T, attn.hidden), dev)
-        _want(self.q, "buffers", t.f32, (T, attn.n_heads, attn.head_dim), dev)
-        if attn.wq.index != dev:
-            raise ValueError(f"weights on GPU {attn.wq.index}, the cache is on GPU {dev}")
+        self._check(attn, x, cache, batch, resid, y)
         if dev >= 0 and t.current_device() != dev:
             with t.device_guard(dev):
                 return self._run(attn, x, cache, batch, resid, y, stream)
         return self._run(attn, x, cache, batch, resid, y, stream)
+
+    def _check(self, attn, x, cache, batch, resid, y):
+        """The projections do not know how large their results' buffers are,
+        and the append changes the cache: everything is looked at first."""
+        from . import (_torch, _want, _want_vec, attn_workspace_bytes, gemm_workspace_bytes,
+                       gemv_grouped_workspace_bytes)
+        t, T, dev = _torch(), batch.n_tokens, cache.index
+        if self.q.shape[0] != T:
+            raise ValueError(f"buffers for {self.q.shape[0]} tokens, the batch has {T}")
+        if self._sizes(attn) != self.sizes:
+            raise ValueError(f"buffers for (hidden, heads, kv heads, head size) {self.sizes}, the layer has {self._sizes(attn)}")
+        if (cache.n_kv_heads, cache.head_dim, cache.dtype) != (attn.n_kv_heads, attn.head_dim, self.q16.dtype):
+            raise ValueError(f"cache of {cache.n_kv_heads} heads of {cache.head_dim} in {cache.dtype}, {attn.n_kv_heads} of "
+                             f"{attn.head_dim} in {self.q16.dtype} wanted")
+        for name, index in (("buffers", self.q.get_device()), ("batch", batch.index), ("wq", attn.wq.index),
+                            ("wk", attn.wk.index), ("wv", attn.wv.index), ("wo", attn.wo.index)):
+            if index != dev:
+                raise ValueError(f"{name} on GPU {index}, the cache is on GPU {dev}")
+        for name, a in (("x", x), ("out", y)) + ((("resid", resid),) if resid is not None else ()):
+            _want(a, name, t.f32, (T, attn.hidden), dev)
+        _want_vec(attn.inv_freq, "inv_freq", t.f64, attn.inv_freq.numel(), dev)
+        for name, w in (("q_norm", attn.q_norm), ("k_norm", attn.k_norm)):
+            _want_vec(w, name, t.f32, attn.head_dim, dev)
+        mats = (attn.wo,) if T <= 4 else (attn.wq, attn.wk, attn.wv, attn.wo)
+        for name, ws, need in (("attention", self.ws_attn, attn_workspace_bytes(cache, batch, attn.n_heads)),
+                               ("projections", self.ws_gemm, max(gemm_workspace_bytes(W, T) for W in mats)),
+                               ("projections", self.ws_jobs, gemv_grouped_workspace_bytes(self._jobs(attn)) if T <= 4 else 0)):
+            if need > (0 if ws is None else ws.nbytes):
+                raise ValueError(f"buffers have {0 if ws is None else ws.nbytes} bytes of workspace for the {name}, {need} wanted")
 
     def _run(self, attn, x, cache, batch, resid, y, stream):
         from . import attn as attention
