@@ -203,8 +203,10 @@ __device__ __forceinline__ u2 lds_read_tr(const char *p)
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// One sequence as a workgroup sees it. nq new tokens (rows t0 ..), the first
-// at position p0; kv cached tokens. nq <= 0: nothing to do.
+// One sequence as a workgroup sees it, for the append and for attention. nq
+// new tokens (rows t0 .., at most max_q), the first at position p0; kv cached
+// tokens. nq = 0: none, or its rows leave the arrays, or its tokens the table
+// (a position that was moved inside would overwrite an older token's slot).
 struct Seq {
     int t0, nq, p0, kv;
 };
@@ -215,9 +217,10 @@ __device__ __forceinline__ Seq load_seq(const KvArgs &a, int s)
     const int t0 = __builtin_amdgcn_readfirstlane(a.q_off[s]);
     const int t1 = __builtin_amdgcn_readfirstlane(a.q_off[s + 1]);
     const int len = __builtin_amdgcn_readfirstlane(a.kv_len[s]);
+    const int room = a.stride << a.page_shift;
     q.t0 = t0;
-    q.kv = max(0, min(len, a.stride << a.page_shift));
-    const bool ok = t0 >= 0 && t1 > t0 && t1 <= a.n_tokens;
+    q.kv = max(0, min(len, room));
+    const bool ok = t0 >= 0 && t1 > t0 && t1 <= a.n_tokens && len <= room;
     q.nq = ok ? min(t1 - t0, a.max_q) : 0;
     q.p0 = ok ? q.kv - (t1 - t0) : 0;
     return q;

@@ -109,8 +109,11 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
     const int s = find_seq(a.kv.q_off, a.kv.n_seq, t);
     if (s < 0)
         return; // rows of no sequence stay as they are
-    const int pos = a.kv.kv_len[s] - (a.kv.q_off[s + 1] - t);
-    // the cache row of the new token: none if it falls outside the table
+    const Seq sq = load_seq(a.kv, s);
+    if (sq.nq <= 0)
+        return;
+    const int pos = sq.p0 + (t - sq.t0);
+    // the cache row of the new token: none before the first position
     const int pg = pos >> a.kv.page_shift;
     const int id = pos >= 0 && pg < a.kv.stride ? a.kv.table[(size_t)s * a.kv.stride + pg] : -1;
     const bool put = id >= 0 && id < a.kv.n_pages;

@@ -468,12 +468,14 @@ typedef struct rfx_kv_cache {
  * Token p of sequence s is slot p % page_size of page page_table[s *
  * table_stride + p / page_size]. The arrays are on the device and may change
  * between replays of a captured graph; the kernels stay inside the buffers
- * whatever they hold: rows outside 0..n_tokens - 1, tokens past the table
- * and pages outside 0..n_pages - 1 are neither read nor written (such a key
- * is not visible; a sequence whose rows leave 0..n_tokens - 1 is skipped),
- * and kv_len counts as at most table_stride * page_size. Rows of no
+ * whatever they hold: pages outside 0..n_pages - 1 are neither read nor
+ * written (such a key is not visible). A sequence whose rows leave
+ * 0..n_tokens - 1, or whose kv_len is more than its table holds (table_stride
+ * * page_size), is skipped by every entry point: nothing of it is appended,
+ * and its rows keep what their outputs hold. A negative kv_len counts as 0,
+ * and a token before position 0 is not appended and sees nothing. Rows of no
  * sequence, before q_off[0] or from q_off[n_seq] on, keep what their outputs
- * hold. table_stride * page_size <= 2^30; n_tokens and max_q <= 2^23. */
+ * hold too. table_stride * page_size <= 2^30; n_tokens and max_q <= 2^23. */
 typedef struct rfx_kv_batch {
     int32_t n_seq;             /* >= 1 */
     int32_t n_tokens;          /* rows of the token arrays, >= 0 */

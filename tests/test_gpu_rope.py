@@ -156,3 +156,60 @@ def test_append_then_attend():
     full = step(cache(), 0, T)
     # both are within attn_bound of the definition (scores below 20, 13 keys): 2^-14 between them
     assert torch.allclose(torch.cat(outs), full, rtol=0, atol=2.0 ** -14 * 5)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+@pytest.mark.parametrize("over", [1, 3, 1 << 30, (1 << 31) - 1 - 64])
+def test_append_and_attention_agree_on_sequences(new, over):
+    """Sequences whose tokens leave their table, or whose rows leave the
+    arrays, are skipped by the append and by attention alike; the others, with
+    negative positions among them, are served."""
+    need_gpu()
+    H, K, D, page, width = 4, 2, 64, 16, 4
+    room = width * page
+    lens = [(new, 50), (new, room), (new, new - 1), (new, 60), (new, 33)]
+    b = Batch(lens, page, K, D, "bf16", seed=5, extra_entries=0)
+    assert b.table.shape[1] == width
+    b.table[:] = torch.arange(5 * width, dtype=torch.int32).view(5, width)  # every entry is a page
+    b.n_pages = 5 * width
+    b.k, b.v = (torch.randn((b.n_pages, K, page, D), generator=torch.Generator().manual_seed(7 + i)).to(b.dtype) for i in range(2))
+    b.kv_len[1] = room + over
+    b.n_tokens -= 1  # the last sequence's last row is outside
+    cache, batch = b.device(R)
+    T = b.n_tokens
+    x = torch.randn((T, H + 2 * K, D), generator=torch.Generator().manual_seed(8))
+    inv = torch.from_numpy(R.rope_inv_freq(D))
+    q16 = torch.full((T, H, D), 7.0, dtype=b.dtype, device="cuda")
+    R.qk_norm_rope(*x.cuda().split((H, K, K), 1), cache, batch, q16, inv.cuda())
+    pos = torch.tensor([t - new + i for _, t in lens for i in range(new)])[:T]
+    seq = torch.arange(5).repeat_interleave(new)[:T]
+    live = (seq == 0) | (seq == 2) | (seq == 3)
+    ref, mag = rotate_exact(x[:, :H], None, 0.0, pos, inv, False)
+    out = q16.cpu()
+    assert close(out[live], ref[live], mag[live], b.dtype).all() and (out[~live] == 7).all()
+    put = live & (pos >= 0)
+    want = b.k.clone(), b.v.clone()
+    ref, mag = rotate_exact(x[:, H:H + K], None, 0.0, pos, inv, False)
+    ids, slot = b.table[seq[put], pos[put] // page].long(), pos[put] % page
+    k, v = b.kd.cpu(), b.vd.cpu()
+    assert close(k[ids, :, slot], ref[put], mag[put], b.dtype).all()
+    want[0][ids, :, slot] = k[ids, :, slot]
+    want[1][ids, :, slot] = x[put, H + K:].to(b.dtype)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1]), "other cache slots changed"
+    o = torch.full((T, H, D), 7.0, device="cuda")
+    n = R.attn_workspace_bytes(cache, batch, H)
+    R.attn(q16, cache, batch, o, 0.125, ws=torch.zeros(n, dtype=torch.uint8, device="cuda") if n else None)
+    o = o.cpu()
+    assert (o[~live] == 7).all() and not o[live & (pos < 0)].any()
+    for s in (0, 2, 3):
+        for i in (0, new - 1):
+            r, p = s * new + i, lens[s][1] - new + i
+            if p < 0:
+                continue
+            j = torch.arange(p + 1)
+            page_of, at = b.table[s, j // page].long(), j % page
+            for h in (0, H - 1):
+                kk, vv = (c[page_of, h // 2, at].double() for c in (k, v))
+                w = torch.softmax(kk @ out[r, h].double() * 0.125, 0)
+                # attn_bound's terms: 2 (72 * 20 + 16 + 64) 2^-24 with sums of |q k| / 8 below 20, 64 products and keys
+                assert ((o[r, h].double() - w @ vv).abs() <= 2.0 ** -12 * (w @ vv.abs())).all(), (s, i, h)
