@@ -199,6 +199,15 @@ class _Torch:
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         cls.f32 = torch.float32
 
+    @staticmethod
+    def on_stream(stream):
+        """torch's own work goes to this stream (of the current device) too:
+        None, a Stream or a handle, as the entry points take them."""
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        return torch.cuda.stream(stream)
+
 
 def _torch():
     if _Torch.f32 is None:

@@ -273,8 +273,10 @@ class AttentionBuffers:
     def run(self, attn: DeviceAttention, x, cache, batch, resid=None, out=None, stream=None):
         """Projections, norm, rotation and cache append, attention, output
         projection for x (device fp32 [n_tokens][hidden]); y = resid +
-        Attention(x) lands in `out` (default self.y). What does not fit these
-        buffers is refused before anything is launched."""
+        Attention(x) lands in `out` (default self.y). Rows that attention
+        leaves (of no sequence, of a skipped one, past max_q) have Attention(x)
+        = 0. What does not fit these buffers is refused before anything is
+        launched."""
         from . import _torch
         t, dev = _torch(), cache.index
         y = self.y if out is None else out
@@ -314,6 +316,7 @@ class AttentionBuffers:
                 raise ValueError(f"buffers have {0 if ws is None else ws.nbytes} bytes of workspace for the {name}, {need} wanted")
 
     def _run(self, attn, x, cache, batch, resid, y, stream):
+        from . import _torch
         from . import attn as attention
         from . import gemm, gemv_grouped, qk_norm_rope, quantize_act
         T = batch.n_tokens
@@ -325,6 +328,8 @@ class AttentionBuffers:
                 gemm(W, *self.x_act, T, o, ws=self.ws_gemm, stream=stream)
         qk_norm_rope(self.q, self.k, self.v, cache, batch, self.q16, attn.inv_freq, attn.q_norm, attn.k_norm, attn.eps,
                      attn.interleaved, stream)
+        with _torch().on_stream(stream): # the rows that attention leaves must not carry an earlier call's on
+            self.o.zero_()
         attention(self.q16, cache, batch, self.o, attn.scale, attn.window, attn.sinks, self.ws_attn, stream)
         quantize_act(self.o.view(T, -1), *self.o_act, stream)
         gemm(attn.wo, *self.o_act, T, y, resid=resid, ws=self.ws_gemm, stream=stream)

@@ -153,3 +153,42 @@ def test_buffers_refuse_other_shapes():
         with pytest.raises(ValueError):
             buf.run(layer, *args, **kw)
     buf.run(layer, x[:3], cache, small)
+
+
+@pytest.mark.parametrize("T,new", [(4, [1, 1]), (40, [20, 3])])
+@pytest.mark.parametrize("how", ["current", "stream", "handle"])
+def test_rows_of_no_sequence_get_the_residual_alone(T, new, how):
+    """Padding rows, and rows past max_q, of a batch whose buffers held a full
+    batch before: what attention leaves does not reach the result."""
+    need_gpu()
+    layer = build()[0]
+    table = torch.tensor([[3, 1, 6, 0], [2, 7, 5, 4]], dtype=torch.int32, device="cuda")
+    x = torch.from_numpy(inputgen.raw_normal(3, (T, H))).cuda()
+
+    def batch(lead, new, max_q):
+        off = torch.tensor(np.concatenate([[lead], lead + np.cumsum(new)]), dtype=torch.int32, device="cuda")
+        return R.KVBatch(off, torch.tensor(new, dtype=torch.int32, device="cuda"), table, T, max_q)
+
+    full, part = batch(0, [T // 2, T - T // 2], T), batch(1, new, T)
+    cache = new_cache()
+    buf = R.AttentionBuffers(layer, cache, full)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    stream = {"current": None, "stream": side, "handle": side.cuda_stream}[how]
+    out = torch.empty_like(x)
+    live = torch.zeros(T, dtype=torch.bool)
+    live[1:1 + sum(new)] = True
+    for resid in (None, x):
+        buf.run(layer, x, cache, full, stream=stream)
+        buf.run(layer, x, cache, part, resid, out, stream)
+        torch.cuda.synchronize()
+        want = torch.zeros_like(x) if resid is None else x
+        assert torch.equal(out[~live.cuda()], want[~live.cuda()])
+        assert (out[live.cuda()] != want[live.cuda()]).any(1).all()
+    short = batch(0, [T // 2, T - T // 2], 1)
+    buf.run(layer, x, cache, full, stream=stream)
+    buf.run(layer, x, cache, short, out=out, stream=stream)
+    torch.cuda.synchronize()
+    first = torch.zeros(T, dtype=torch.bool, device="cuda")
+    first[[0, T // 2]] = True
+    assert not out[~first].any() and out[first].any(1).all()
