@@ -234,8 +234,8 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     int st = check_kv(C, B, n_heads, "rfx_attn");
     if (st)
         return st;
-    if (!(scale > 0.0f) || std::isinf(scale))
-        return fail(RFX_E_INVAL, "rfx_attn: scale=%g (positive and finite)", (double)scale);
+    if (!(scale > 0.0f) || scale > 0x1p127f)
+        return fail(RFX_E_INVAL, "rfx_attn: scale=%g (positive, at most 2^127)", (double)scale);
     if (window < 0 || sinks < 0)
         return fail(RFX_E_INVAL, "rfx_attn: window=%d sinks=%d", window, sinks);
     if (out_type != RFX_F32 && out_type != C->type)
@@ -259,7 +259,7 @@ int rfx_attn(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, int n_
     a.q = static_cast<const uint16_t *>(q);
     a.out = out;
     a.out_f32 = out_type == RFX_F32;
-    a.c = scale * 1.4426950408889634f;
+    a.c = scale * 1.4426950408889634f; // finite
     a.window = window < 1 << 30 ? window : 1 << 30; // positions are below 2^30: differences stay in 32 bits
     a.sinks = sinks;
     a.S = p.S;

@@ -112,8 +112,10 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 
     f32x4 acc[NR][NV];
     float m[NR], l[NR];
+    bool far[NR]; // uniform
 #pragma unroll
     for (int n = 0; n < NR; n++) {
+        far[n] = false;
         m[n] = -INFINITY;
         l[n] = 0.f;
 #pragma unroll
@@ -301,8 +303,16 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
                 for (int i = 0; i < NV; i++)
                     acc[n][i] *= f;
                 m[n] = mn;
+                far[n] = __any((mn != -INFINITY) & (a.c * fabsf(mn) > kFar));
             }
-            const float off = m[n] == -INFINITY ? 0.f : T::BIAS - a.c * m[n];
+            float off = m[n] == -INFINITY ? 0.f : T::BIAS - a.c * m[n];
+            if (far[n]) {
+                const float sub = m[n] == -INFINITY ? 0.f : m[n];
+                off = T::BIAS;
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    s[n][i >> 2][i & 3] -= sub;
+            }
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; i++) {

@@ -54,6 +54,18 @@ __device__ __forceinline__ float max_halves(float x)
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// The row's maximum off its scores; nothing where it has seen none.
+template <int NK>
+__device__ __forceinline__ void subtract_max(f32x16 (&s)[NK], float m)
+{
+    const float sub = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < NK; k++)
+#pragma unroll
+        for (int v = 0; v < 16; v++)
+            s[k][v] -= sub;
+}
+
 // Heads of 64 fit three waves per SIMD in 168 registers, of 128 two in 256.
 // Six prompts with a window, fp16 with an fp32 result: 272 us with two waves,
 // 248 with three; with bf16's three terms 65 (2048 tokens) and 71.
@@ -116,6 +128,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
         for (int v = 0; v < 16; v++)
             acc[i][v] = 0.f;
     float m = -INFINITY, l = 0.f;
+    bool far = false; // uniform
 
     // Page ids go through LDS, those of `ids_n` tiles from tile ids_at on, so
     // that a tile's loads need no other global load first.
@@ -243,9 +256,14 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
                 for (int i = 0; i < ND; i++)
                     acc[i] *= f;
                 m = mn;
+                far = __any((mn != -INFINITY) & (a.c * fabsf(mn) > kFar));
             }
             __builtin_amdgcn_s_setprio(1); // the other wave of the SIMD waits rather than this one: 587 to 572 us
-            const float off = m == -INFINITY ? 0.f : T::BIAS - a.c * m;
+            float off = m == -INFINITY ? 0.f : T::BIAS - a.c * m;
+            if (far) {
+                off = T::BIAS;
+                subtract_max<NK>(s, m);
+            }
 #pragma unroll
             for (int k = 0; k < NK; k++)
 #pragma unroll
@@ -394,6 +412,7 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
         for (int v = 0; v < 16; v++)
             acc[i][v] = 0.f;
     float m = -INFINITY, l = 0.f;
+    bool far = false; // uniform
 
     const int32_t *table = kv.table + (size_t)seq * kv.stride;
     const int last_key = max(0, kt.hi - 1), ps = kv.page_shift, pm = (1 << ps) - 1;
@@ -589,8 +608,13 @@ __global__ __launch_bounds__(512, 2) void attn_pair_kernel(AttnArgs a)
             for (int i = 0; i < ND; i++)
                 acc[i] *= f;
             m = mn;
+            far = __any((mn != -INFINITY) & (a.c * fabsf(mn) > kFar));
         }
-        const float off = m == -INFINITY ? 0.f : T::BIAS - a.c * m;
+        float off = m == -INFINITY ? 0.f : T::BIAS - a.c * m;
+        if (far) {
+            off = T::BIAS;
+            subtract_max<NK>(s, m);
+        }
 #pragma unroll
         for (int k = 0; k < NK; k++)
 #pragma unroll

@@ -201,6 +201,13 @@ __device__ __forceinline__ u2 lds_read_tr(const char *p)
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lptr)(uint32_t)(uintptr_t)p));
 }
 
+// A weight is exp2(c s - c m + BIAS), one fused operation per score. Where c m
+// is large its rounding (2^-24 of it) moves all of a row's weights by one
+// factor, which overflows fp16 from c m = 2^26 on, and by another one once m
+// rises. From here on (an error of 2^-12 up to here) m is subtracted from the
+// scores first.
+constexpr float kFar = 4096.0f;
+
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // One sequence as a workgroup sees it, for the append and for attention. nq

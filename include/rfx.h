@@ -518,7 +518,8 @@ int rfx_qk_norm_rope(const rfx_qk_rope *args, const rfx_kv_cache *cache, const r
  * the cache's type. Scores, softmax and sums are fp32; for an fp32 result
  * the softmax weights enter the matrix core as two (fp16) or three (bf16)
  * terms, for a 16-bit result of more than a few rows per kv head as one.
- * Cached keys and values that a sequence's tokens see are assumed finite; a
+ * Cached keys and values that a sequence's tokens see are assumed finite, and
+ * so are the fp32 scores q k^T (of any size); a
  * key outside every row's window, and every slot past kv_len, may hold
  * anything. Results do not depend on timing: splits of the keys are joined
  * in a fixed order.
@@ -528,7 +529,7 @@ int rfx_qk_norm_rope(const rfx_qk_rope *args, const rfx_kv_cache *cache, const r
  * call (so it is not one to share with an entry point that needs its
  * workspace zero). A workspace must not be shared by calls that can run
  * concurrently, graphs captured with it included.
- * scale > 0. One launch, and a second one where keys are split.
+ * 0 < scale <= 2^127. One launch, and a second one where keys are split.
  * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
 size_t rfx_attn_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads);
 int rfx_attn(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads, float scale,

@@ -357,3 +357,60 @@ def test_two_groups_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(og, oe), i
+
+
+# (lens, heads, kv_heads, dim, page): every kernel, unsplit and split
+FAR = [
+    ([(1, 300), (1, 1), (1, 40)], 4, 2, 64, 16),
+    ([(4, 900), (2, 2)], 8, 1, 128, 32),
+    ([(1, 5000)], 8, 1, 64, 64),
+    ([(3, 200)], 5, 1, 80, 4),
+    ([(60, 500), (33, 33)], 8, 2, 128, 16),
+    ([(40, 400)], 4, 2, 64, 64),
+    ([(30, 200)], 2, 1, 256, 32),
+    ([(40, 6000)], 8, 1, 128, 32),
+    ([(40, 300)] * 64, 8, 8, 128, 64),
+]
+
+
+@pytest.mark.parametrize("kind,log_q,log_k,log_unit,scale", [
+    ("f16", 6, 5, 0, 0.5), ("f16", 11, 11, 0, 0.5), ("f16", 12, 12, 2, 0.25), ("f16", 15, 15, 8, 2.0 ** -9), ("f16", 15, 15, 8, 1.0),
+    ("bf16", 11, 11, 0, 0.5), ("bf16", 20, 20, 18, 2.0 ** -20), ("bf16", 20, 20, 18, 1.0), ("bf16", 62, 62, 102, 8.0)])
+@pytest.mark.parametrize("case", range(len(FAR)))
+def test_scores_far_from_zero(case, kind, log_q, log_k, log_unit, scale):
+    """Scores that are all near 1.875 * 2^(log_q + log_k), of either sign, and
+    differ by whole units: element 0 makes the offset, 15 elements of -2 .. 2
+    times 2^(log_unit / 2) the differences, so that every partial sum is a
+    whole number of units below 2^24 and the scores are exact in fp32. What is
+    left is the weights' arithmetic: c to a half step, c (s - m) + BIAS
+    rounded once (at most 150 + 15 in size where the weight counts), or, up to
+    |c m| = 2^12, one of its two terms rounded there; exp2 and the sums as in
+    attn_bound; and weights below fp16's smallest, 2^-35 of the largest."""
+    need_gpu()
+    lens, heads, kv, dim, page = FAR[case]
+    say(f"attn far {lens[:3]} {kind} 2^{log_q + log_k} unit 2^{log_unit} scale {scale}")
+    b = Batch(lens, page, kv, dim, kind, seed=500 + case)
+    g = torch.Generator().manual_seed(case)
+    uq, uk = 2.0 ** (log_unit // 2), 2.0 ** (log_unit - log_unit // 2)
+
+    def small(shape, unit, lead):
+        x = torch.zeros(shape)
+        x[..., 1:min(16, dim)] = torch.randint(-2, 3, (*shape[:-1], min(16, dim) - 1), generator=g) * unit
+        x[..., 0] = lead
+        return x.to(b.dtype)
+
+    for sign in (1.0, -1.0):
+        b.k = torch.where(b.used[:, None, :, None], small(b.k.shape, uk, 1.25 * 2.0 ** log_k), float("nan")).to(b.dtype)
+        q = small((b.n_tokens, heads, dim), uq, sign * 1.5 * 2.0 ** log_q)
+        ref, mag, _ = attn_exact(b, q, scale)
+        top = float(b.v.double().nan_to_num(0).abs().max())
+        L = max(t for _, t in lens)
+        for out in ("f32", "same"):
+            o = run(b, q, scale, out=out).double()
+            rel = 2 * ((1.5 * 150 + 15) * 2.0 ** -24 + 2.0 ** -12 + 8 * 2.0 ** -23 + L * 2.0 ** -24)
+            half = torch.finfo(b.dtype).eps / 2
+            tol = (rel + (half if out == "same" and b.max_q * (heads // kv) > 16 else 0)) * mag + L * 2.0 ** -35 * top
+            if out == "same":
+                tol = tol + half * (ref.abs() + tol) + 2.0 ** -25
+            bad = ~((o - ref).abs() <= tol)
+            assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside, first {o[bad][0]} for {ref[bad][0]} ({sign} {out})"

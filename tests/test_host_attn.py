@@ -149,3 +149,8 @@ def test_packed_rope_arguments_are_the_structure():
     a = rope(q_stride=520, k_stride=136, v_stride=144, eps=1e-5, n_heads=12, rot_dim=40, interleaved=True)
     packed = R._pack_qk_rope(P, P, P, 520, 136, 144, P, P, 0, 1e-5, 12, 40, True)
     assert packed == bytes(a) and len(packed) == ctypes.sizeof(R.QkRopeC)
+
+
+def test_scale_that_overflows_with_log2_e():
+    assert attn_status(cache(), batch(n_tokens=0), scale=1.5 * 2.0 ** 127) == INVAL
+    assert attn_status(cache(), batch(n_tokens=0), scale=2.0 ** 127) == 0
