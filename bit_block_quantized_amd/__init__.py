@@ -191,7 +191,7 @@ class _Torch:
     @classmethod
     def load(cls):
         import torch
-        cls.f64, cls.i32 = torch.float64, torch.int32
+        cls.f64, cls.i32, cls.i8 = torch.float64, torch.int32, torch.int8
         cls.elem = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
         cls.current_device, cls.device_guard = torch.cuda.current_device, torch.cuda.device
         # the handle itself, without a Stream object around it, where torch has that
@@ -299,6 +299,7 @@ class DeviceQMat:
         self.data = data  # torch uint8 tensor on the GPU (kept alive here)
         self.index = None if data is None or isinstance(data, int) else data.get_device()
         self.c = QMat(fmt, rows, cols, count, _dptr(data))
+        self.c_ref = ctypes.byref(self.c)
 
     @classmethod
     def from_host(cls, fmt, rows, cols, tiled: np.ndarray, count=1, device="cuda"):
@@ -355,13 +356,44 @@ def gemm_workspace_bytes(W: DeviceQMat, q: int) -> int:
     return int(lib().rfx_gemm_workspace_bytes(W.ref(), q))
 
 
+def _room(t, name, dtype, nbytes, index):
+    """Address of a contiguous tensor of this dtype and at least this size on
+    the device of this index; an address or None as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is dtype and t.nbytes >= nbytes and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or t.nbytes < nbytes:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, {dtype} of {nbytes // t.element_size()} elements wanted")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    raise ValueError(f"{name}: on {t.device}, not GPU {index}")
+
+
+def _workspace(ws, index):
+    """Address and size of a workspace tensor on the device of this index."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != index:
+        raise ValueError(f"ws: on {ws.device}, not GPU {index}")
+    if not ws.is_contiguous():
+        raise ValueError("ws: not contiguous")
+    return ws.data_ptr(), ws.nbytes
+
+
 def gemm(W: DeviceQMat, xq, xs, xsum, q, y, bias=None, act=ACT_NONE, resid=None, ws=None, stream=None):
     """y = resid + act(W x + bias) for q columns (rfx_gemm), on W's device:
-    its current stream unless one is given."""
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    index = _torch().current_device() if W.index is None else W.index
-    _call_on(index, stream, lib().rfx_gemm, W.ref(), _dptr(xq), _dptr(xs), _dptr(xsum), q, _dptr(bias), act, _dptr(resid),
-             _dptr(y), _dptr(ws), ws_bytes)
+    its current stream unless one is given. xq int8 [q][cols], xs float32 and
+    xsum int32 [q][cols / 32], bias float32 [rows], y and resid float32
+    [q][rows], contiguous and at least as large; a bare address is taken as it
+    is."""
+    t = _torch()
+    index = t.current_device() if W.index is None else W.index
+    f32, codes, out = t.f32, q * W.cols, 4 * q * W.rows
+    wp, wn = _workspace(ws, index)
+    _call_on(index, stream, lib().rfx_gemm, W.c_ref, _room(xq, "xq", t.i8, codes, index), _room(xs, "xs", f32, codes // 8, index),
+             _room(xsum, "xsum", t.i32, codes // 8, index), q, _room(bias, "bias", f32, 4 * W.rows, index), act,
+             _room(resid, "resid", f32, out, index), _room(y, "y", f32, out, index), wp, wn)
 
 
 def gemv_jobs(jobs):
@@ -611,11 +643,7 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
         raise ValueError(f"batch on GPU {batch.index}, the cache is on GPU {dev}")
     if window > 0x7fffffff or sinks > 0x7fffffff: # the C call's int would wrap
         raise ValueError(f"window {window}, sinks {sinks}: below 2^31")
-    wp, wn = None, 0
-    if ws is not None:
-        if ws.get_device() != dev:
-            raise ValueError(f"ws: on {ws.device}, not GPU {dev}")
-        wp, wn = ws.data_ptr(), ws.nbytes
+    wp, wn = _workspace(ws, dev)
     _call_on(dev, stream, lib().rfx_attn, qp, cache.c_ref, batch.c_ref, Hq, scale, window, sinks, op, _elem(out.dtype),
              wp, wn)
 

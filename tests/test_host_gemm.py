@@ -91,3 +91,46 @@ def test_slots_of_every_shape_fit_in_front_of_the_operands():
     most = max(need(4, rows=rows, cols=cols) for rows in range(1, 64 * 400, 64) for cols in (512, 1024, 2048, 4096, 8192, 1 << 20))
     assert most == 47 * 7 * 4 * 256
     assert most <= reserved
+
+
+@pytest.mark.parametrize("q", [3, 40])
+def test_binding_checks_tensors(q, monkeypatch):
+    """Tensors of another type, size, layout or device are refused before the
+    call; larger ones (a buffer's first rows) and bare addresses are taken."""
+    calls = []
+
+    class Lib:
+        @staticmethod
+        def rfx_gemm(*args):
+            calls.append(args)
+            return 0
+
+    W = R.DeviceQMat(4, 100, 64, torch.zeros(1, dtype=torch.uint8))
+    ok = dict(xq=torch.zeros(q, 64, dtype=torch.int8), xs=torch.zeros(q, 2), xsum=torch.zeros(q, 2, dtype=torch.int32), q=q,
+              y=torch.zeros(q, 100), bias=torch.zeros(100), resid=torch.zeros(q, 100), ws=torch.zeros(256, dtype=torch.uint8))
+    bad = [dict(xq=ok["xq"].to(torch.uint8)), dict(xq=ok["xq"][:-1]), dict(xq=torch.zeros(64, q, dtype=torch.int8).t()),
+           dict(xs=ok["xs"].double()), dict(xs=ok["xs"][:, :1]), dict(xs=torch.zeros(2, q).t()),
+           dict(xsum=ok["xsum"].long()), dict(xsum=ok["xsum"][1:]), dict(y=ok["y"].half()), dict(y=ok["y"][1:]),
+           dict(y=torch.zeros(100, q).t()), dict(y=torch.zeros(q, 200)[:, ::2]), dict(bias=ok["bias"][:99]),
+           dict(bias=ok["bias"].bfloat16()), dict(bias=torch.zeros(200)[::2]), dict(resid=ok["resid"][1:]),
+           dict(resid=ok["resid"].double()), dict(resid=torch.zeros(100, q).t()), dict(resid=torch.zeros(100).expand(q, 100)),
+           dict(ws=torch.zeros(512, dtype=torch.uint8)[::2])]
+    monkeypatch.setattr(R, "lib", lambda: Lib)
+    monkeypatch.setattr(R, "_call_on", lambda index, stream, fn, *args: fn(*args))
+    for kw in bad:
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            R.gemm(W, **{**ok, **kw})
+    W.index = 3
+    for name in ok:
+        if name != "q": # the others are where the weights are
+            monkeypatch.setattr(torch.Tensor, "get_device", lambda t, _bad=ok[name]: 2 if t is _bad else 3)
+            with pytest.raises(ValueError, match=name):
+                R.gemm(W, **ok)
+    assert not calls
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 3)
+    R.gemm(W, **ok)
+    R.gemm(W, **{**ok, "xq": torch.zeros(q + 5, 64, dtype=torch.int8), "y": torch.zeros(q, 10, 10), "bias": None, "resid": None,
+                 "ws": None})
+    R.gemm(W, P, P, P, q, P, resid=P)
+    assert len(calls) == 3 and calls[0][8] == ok["y"].data_ptr() and calls[1][9:] == (None, 0)
+    assert calls[2][1:4] == (P, P, P) and calls[2][7:9] == (P, P)
