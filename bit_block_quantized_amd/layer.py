@@ -280,13 +280,14 @@ class AttentionBuffers:
         from . import _torch
         t, dev = _torch(), cache.index
         y = self.y if out is None else out
-        self._check(attn, x, cache, batch, resid, y)
+        jobs = self._jobs(attn) if batch.n_tokens <= 4 else None
+        self._check(attn, x, cache, batch, resid, y, jobs)
         if dev >= 0 and t.current_device() != dev:
             with t.device_guard(dev):
-                return self._run(attn, x, cache, batch, resid, y, stream)
-        return self._run(attn, x, cache, batch, resid, y, stream)
+                return self._run(attn, x, cache, batch, resid, y, jobs, stream)
+        return self._run(attn, x, cache, batch, resid, y, jobs, stream)
 
-    def _check(self, attn, x, cache, batch, resid, y):
+    def _check(self, attn, x, cache, batch, resid, y, jobs):
         """The projections do not know how large their results' buffers are,
         and the append changes the cache: everything is looked at first."""
         from . import (_torch, _want, _want_vec, attn_workspace_bytes, gemm_workspace_bytes,
@@ -299,37 +300,43 @@ class AttentionBuffers:
         if (cache.n_kv_heads, cache.head_dim, cache.dtype) != (attn.n_kv_heads, attn.head_dim, self.q16.dtype):
             raise ValueError(f"cache of {cache.n_kv_heads} heads of {cache.head_dim} in {cache.dtype}, {attn.n_kv_heads} of "
                              f"{attn.head_dim} in {self.q16.dtype} wanted")
-        for name, index in (("buffers", self.q.get_device()), ("batch", batch.index), ("wq", attn.wq.index),
-                            ("wk", attn.wk.index), ("wv", attn.wv.index), ("wo", attn.wo.index)):
-            if index != dev:
-                raise ValueError(f"{name} on GPU {index}, the cache is on GPU {dev}")
-        for name, a in (("x", x), ("out", y)) + ((("resid", resid),) if resid is not None else ()):
-            _want(a, name, t.f32, (T, attn.hidden), dev)
+        places = self.q.get_device(), batch.index, attn.wq.index, attn.wk.index, attn.wv.index, attn.wo.index
+        if places.count(dev) != 6:
+            raise ValueError(f"buffers, batch, wq, wk, wv and wo on GPU {places}, the cache is on GPU {dev}")
+        shape = T, attn.hidden
+        _want(x, "x", t.f32, shape, dev)
+        _want(y, "out", t.f32, shape, dev)
+        if resid is not None:
+            _want(resid, "resid", t.f32, shape, dev)
         _want_vec(attn.inv_freq, "inv_freq", t.f64, attn.inv_freq.numel(), dev)
-        for name, w in (("q_norm", attn.q_norm), ("k_norm", attn.k_norm)):
-            _want_vec(w, name, t.f32, attn.head_dim, dev)
+        _want_vec(attn.q_norm, "q_norm", t.f32, attn.head_dim, dev)
+        _want_vec(attn.k_norm, "k_norm", t.f32, attn.head_dim, dev)
         mats = (attn.wo,) if T <= 4 else (attn.wq, attn.wk, attn.wv, attn.wo)
         for name, ws, need in (("attention", self.ws_attn, attn_workspace_bytes(cache, batch, attn.n_heads)),
                                ("projections", self.ws_gemm, max(gemm_workspace_bytes(W, T) for W in mats)),
-                               ("projections", self.ws_jobs, gemv_grouped_workspace_bytes(self._jobs(attn)) if T <= 4 else 0)):
+                               ("projections", self.ws_jobs, 0 if jobs is None else gemv_grouped_workspace_bytes(jobs))):
             if need > (0 if ws is None else ws.nbytes):
                 raise ValueError(f"buffers have {0 if ws is None else ws.nbytes} bytes of workspace for the {name}, {need} wanted")
 
-    def _run(self, attn, x, cache, batch, resid, y, stream):
+    def _run(self, attn, x, cache, batch, resid, y, jobs, stream):
         from . import _torch
         from . import attn as attention
         from . import gemm, gemv_grouped, qk_norm_rope, quantize_act
         T = batch.n_tokens
         quantize_act(x, *self.x_act, stream)
-        if T <= 4:
-            gemv_grouped(self._jobs(attn), self.ws_jobs, stream)
+        if jobs is not None:
+            gemv_grouped(jobs, self.ws_jobs, stream)
         else:
             for W, o in ((attn.wq, self.q), (attn.wk, self.k), (attn.wv, self.v)):
                 gemm(W, *self.x_act, T, o, ws=self.ws_gemm, stream=stream)
         qk_norm_rope(self.q, self.k, self.v, cache, batch, self.q16, attn.inv_freq, attn.q_norm, attn.k_norm, attn.eps,
                      attn.interleaved, stream)
-        with _torch().on_stream(stream): # the rows that attention leaves must not carry an earlier call's on
+        # the rows that attention leaves must not carry an earlier call's on
+        if stream is None:
             self.o.zero_()
+        else:
+            with _torch().on_stream(stream):
+                self.o.zero_()
         attention(self.q16, cache, batch, self.o, attn.scale, attn.window, attn.sinks, self.ws_attn, stream)
         quantize_act(self.o.view(T, -1), *self.o_act, stream)
         gemm(attn.wo, *self.o_act, T, y, resid=resid, ws=self.ws_gemm, stream=stream)
