@@ -297,7 +297,8 @@ class DeviceQMat:
     def __init__(self, fmt, rows, cols, data, count=1):
         self.fmt, self.rows, self.cols, self.count = fmt, rows, cols, count
         self.data = data  # torch uint8 tensor on the GPU (kept alive here)
-        self.index = None if data is None or isinstance(data, int) else data.get_device()
+        # the GPU it is on, None where it does not say (an address, an object with data_ptr() alone)
+        self.index = data.get_device() if hasattr(data, "get_device") else None
         self.c = QMat(fmt, rows, cols, count, _dptr(data))
         self.c_ref = ctypes.byref(self.c)
 

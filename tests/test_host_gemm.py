@@ -134,3 +134,15 @@ def test_binding_checks_tensors(q, monkeypatch):
     R.gemm(W, P, P, P, q, P, resid=P)
     assert len(calls) == 3 and calls[0][8] == ok["y"].data_ptr() and calls[1][9:] == (None, 0)
     assert calls[2][1:4] == (P, P, P) and calls[2][7:9] == (P, P)
+
+
+def test_weights_that_only_have_an_address():
+    """data may be any object with data_ptr(), an address or None."""
+    class Block:
+        @staticmethod
+        def data_ptr():
+            return P
+
+    assert [R.DeviceQMat(4, 64, 32, d).index for d in (Block(), P, None)] == [None] * 3
+    assert R.DeviceQMat(4, 64, 32, Block()).c.data == P
+    assert R.DeviceQMat(4, 64, 32, torch.zeros(8704, dtype=torch.uint8)).index == -1
