@@ -500,6 +500,13 @@ def _elem(dtype):
     return e
 
 
+def _int32(**values):
+    """ctypes wraps what an int32 does not hold."""
+    for name, v in values.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{name} {v}: from -2^31, below 2^31")
+
+
 def _want(t, name, dtype, shape, index):
     """Address of a contiguous tensor of this dtype and shape (a tuple) on
     the device of this index (-1: host memory)."""
@@ -556,6 +563,7 @@ class KVBatch:
 
     def __init__(self, q_off, kv_len, page_table, n_tokens, max_q):
         n_seq, stride = page_table.shape
+        _int32(n_tokens=n_tokens, max_q=max_q)
         self.q_off, self.kv_len, self.page_table = q_off, kv_len, page_table
         self.n_seq, self.n_tokens, self.max_q = n_seq, n_tokens, max_q
         self.index = dev = page_table.get_device()
@@ -642,8 +650,7 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
     op = _want(out, "out", out.dtype, shape, dev)
     if batch.index != dev:
         raise ValueError(f"batch on GPU {batch.index}, the cache is on GPU {dev}")
-    if window > 0x7fffffff or sinks > 0x7fffffff: # the C call's int would wrap
-        raise ValueError(f"window {window}, sinks {sinks}: below 2^31")
+    _int32(window=window, sinks=sinks)
     wp, wn = _workspace(ws, dev)
     _call_on(dev, stream, lib().rfx_attn, qp, cache.c_ref, batch.c_ref, Hq, scale, window, sinks, op, _elem(out.dtype),
              wp, wn)

@@ -154,3 +154,14 @@ def test_packed_rope_arguments_are_the_structure():
 def test_scale_that_overflows_with_log2_e():
     assert attn_status(cache(), batch(n_tokens=0), scale=1.5 * 2.0 ** 127) == INVAL
     assert attn_status(cache(), batch(n_tokens=0), scale=2.0 ** 127) == 0
+
+
+@pytest.mark.parametrize("value", [-(1 << 31) - 1, -(1 << 32) + 5, 1 << 31, (1 << 32) + 5])
+def test_binding_refuses_what_wraps_in_32_bits(value):
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    c, b, q, o = R.DeviceKVCache(k, k.clone()), R.KVBatch(i(2), i(1), i(1, 4), 1, 1), torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 4, 64)
+    for bad in (lambda: R.attn(q, c, b, o, 0.125, window=value), lambda: R.attn(q, c, b, o, 0.125, window=5, sinks=value),
+                lambda: R.KVBatch(i(2), i(1), i(1, 4), value, 1), lambda: R.KVBatch(i(2), i(1), i(1, 4), 1, value)):
+        with pytest.raises(ValueError, match="below 2"):
+            bad()
