@@ -846,10 +846,9 @@ bool balanced_order(GroupArgs &ga, int wgs)
 // ------------------------------------------------------------------
 // rfx_gemv_noalloc: rfx_gemv with its split-K exchange slots in a
 // file-scope device array instead of a caller workspace, for callers that
-// cannot allocate. The largest split choose_shape picks (row groups x
-// (P - 1) below 192, q <= 4) needs under 192 KiB of slots.
+// cannot allocate: as many bytes as any shape needs.
 // ------------------------------------------------------------------
-constexpr size_t kNoAllocBytes = 256u << 10;
+constexpr size_t kNoAllocBytes = kGemvSlotBytes;
 constexpr int kMaxDevices = 64;
 
 std::mutex g_scratch_mu;
@@ -1006,10 +1005,7 @@ int rfx_gemv_noalloc(const rfx_qmat *W, const int8_t *xq, const float *xs, const
         return fail(RFX_E_INVAL, "rfx_gemv_noalloc: q=%d (must be 1..4)", q);
     if ((st = check_act(xq, xs, xsum, true)) || (st = check_ptr(y, 4, "y")))
         return st;
-    const size_t need = rfx_gemv_workspace_bytes(W, q);
-    if (need > kNoAllocBytes)
-        return fail(RFX_E_WORKSPACE, "rfx_gemv_noalloc: this shape needs %zu bytes of scratch, more than its %zu",
-                    need, kNoAllocBytes);
+    const size_t need = rfx_gemv_workspace_bytes(W, q); // at most kNoAllocBytes
     void *ws = nullptr;
     if (need && (st = scratch_address(&ws, (hipStream_t)stream)))
         return st;

@@ -56,3 +56,20 @@ def test_gemv_noalloc_repeated_calls_leave_scratch_clear():
     first = outs[0].cpu().numpy()
     for y in outs[1:]:
         assert np.array_equal(y.cpu().numpy(), first)
+
+
+@pytest.mark.parametrize("N,K", [(2560, 8192), (5632, 4096), (3008, 8192)])
+def test_gemv_noalloc_where_slots_are_many(N, K):
+    """Shapes whose split takes more than 256 KiB of slots with four columns."""
+    torch = need_gpu()
+    W, x, dW, xq, xs, xsum = _case(torch, 4, 4, N, K, 330)
+    need = R.gemv_workspace_bytes(dW, 4)
+    assert need > 256 << 10
+    y = [torch.full((4, N), float("nan"), dtype=torch.float32, device="cuda") for _ in range(3)]
+    R.gemv(dW, xq, xs, xsum, 4, y[0], workspace(torch, need))
+    for out in y[1:]:
+        R.gemv_noalloc(dW, xq, xs, xsum, 4, out)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
+    oq, os_ = O.quantize_act(x)
+    assert rel_err(y[2].cpu().numpy(), O.gemv(4, O.quantize_matrix(4, W), oq, os_)) <= TOL
