@@ -280,6 +280,10 @@ Plan plan(int fmt, int64_t N, int64_t K, int q)
 
 bool many_ok(int fmt) { return fmt == RFX_FP2 || fmt == RFX_FP3 || fmt == RFX_FP4; }
 
+// What the kernels' 32-bit row numbers (rounded up to whole workgroups) and K
+// tile numbers (times up to 512 splits) hold.
+bool small_enough(const rfx_qmat *W) { return W->rows <= 1 << 30 && W->cols <= 1 << 29; }
+
 template <int F>
 int launch(const GemmArgs &a, int nt, const int8_t *xq, const float *xs, int nb, hipStream_t st)
 {
@@ -310,7 +314,7 @@ size_t rfx_gemm_workspace_bytes(const rfx_qmat *W, int q)
         return 0;
     if (q <= 4)
         return rfx_gemv_workspace_bytes(W, q);
-    return many_ok(W->fmt) ? plan(W->fmt, W->rows, W->cols, q).bytes : 0;
+    return many_ok(W->fmt) && small_enough(W) ? plan(W->fmt, W->rows, W->cols, q).bytes : 0;
 }
 
 int rfx_gemm(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t *xsum, int q, const float *bias, int act,
@@ -329,6 +333,9 @@ int rfx_gemm(const rfx_qmat *W, const int8_t *xq, const float *xs, const int32_t
         return st;
     if (q > 4 && !many_ok(W->fmt))
         return fail(RFX_E_UNSUPPORTED, "rfx_gemm: format %d with more than 4 columns (FP2, FP3 and FP4 only)", W->fmt);
+    if (q > 4 && !small_enough(W))
+        return fail(RFX_E_UNSUPPORTED, "rfx_gemm: %d x %d with more than 4 columns (at most 2^30 rows, 2^29 columns of W)",
+                    W->rows, W->cols);
     const size_t need = rfx_gemm_workspace_bytes(W, q);
     if (need) {
         if (!ws || ws_bytes < need)

@@ -258,8 +258,8 @@ int rfx_gemv_grouped(const rfx_gemv_job *jobs, int n_jobs, void *ws, size_t ws_b
  * a sum of five 6-bit digits, which is within 2^-23.9 of its block's largest
  * (or 2^-130, if that is more), and sums exact products in fp32; a block
  * whose largest |xs code| is not finite makes its column NaN.
- * W: count must be 1; any format at q <= 4, RFX_FP2, RFX_FP3 or RFX_FP4 at
- * q > 4 (RFX_E_UNSUPPORTED otherwise). q 1..RFX_GEMM_MAX_Q. xq, xs and xsum
+ * W: count must be 1; any format at q <= 4, RFX_FP2, RFX_FP3 or RFX_FP4 of at
+ * most 2^30 rows and 2^29 columns at q > 4 (RFX_E_UNSUPPORTED otherwise). q 1..RFX_GEMM_MAX_Q. xq, xs and xsum
  * as for rfx_gemv. bias fp32 [N] or NULL; act: RFX_ACT_SILU is z / (1 +
  * e^-z), RFX_ACT_GELU z Phi(z), RFX_ACT_GELU_TANH its tanh approximation 0.5
  * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))); resid fp32 [q][N] or NULL,

@@ -146,3 +146,12 @@ def test_weights_that_only_have_an_address():
     assert [R.DeviceQMat(4, 64, 32, d).index for d in (Block(), P, None)] == [None] * 3
     assert R.DeviceQMat(4, 64, 32, Block()).c.data == P
     assert R.DeviceQMat(4, 64, 32, torch.zeros(8704, dtype=torch.uint8)).index == -1
+
+
+@pytest.mark.parametrize("fmt", [2, 3, 4])
+def test_matrices_past_the_kernels_32_bit_numbers(fmt):
+    """Rows that do not fit 32 bits once rounded up, and K tiles times splits
+    past 2^31, are refused."""
+    for kw in (dict(rows=(1 << 30) + 1), dict(rows=(1 << 31) - 1, cols=32), dict(cols=(1 << 29) + 32, rows=1)):
+        assert need(5, fmt=fmt, **kw) == 0 and status(q=5, fmt=fmt, ws=P, ws_bytes=1 << 60, **kw) == UNSUPPORTED, kw
+    assert need(5, fmt=fmt, rows=1 << 30, cols=32) > 0 < need(5, fmt=fmt, rows=1, cols=1 << 29)
