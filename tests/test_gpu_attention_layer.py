@@ -192,3 +192,44 @@ def test_rows_of_no_sequence_get_the_residual_alone(T, new, how):
     first = torch.zeros(T, dtype=torch.bool, device="cuda")
     first[[0, T // 2]] = True
     assert not out[~first].any() and out[first].any(1).all()
+
+
+@pytest.mark.parametrize("new", [[1, 1], [20, 13]])
+def test_captured_and_replayed(new):
+    """The whole half captured once and replayed while the sequences grow,
+    and while one of them has no rows, with eager calls between: every replay
+    equals the eager result and leaves the same cache."""
+    need_gpu()
+    layer = build()[0]
+    table = torch.tensor([[3, 1, 6, 0], [2, 7, 5, 4]], dtype=torch.int32, device="cuda")
+    T = sum(new)
+    batch = batch_of(new, new, table)
+    x = torch.from_numpy(inputgen.raw_normal(3, (T, H))).cuda()
+    caches = [R.DeviceKVCache(*(torch.zeros((8, HK, 16, D), dtype=torch.float16, device="cuda") for _ in range(2))) for _ in range(2)]
+    bufs = [R.AttentionBuffers(layer, c, batch) for c in caches]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        bufs[0].run(layer, x, caches[0], batch, resid=x)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        yg = bufs[0].run(layer, x, caches[0], batch, resid=x)
+    off = batch.q_off.clone()
+    for i in range(5):
+        batch.kv_len.add_(3)
+        batch.q_off.copy_(off)
+        if i == 3: # the second sequence is away: its rows belong to none
+            batch.q_off[2] = batch.q_off[1]
+        x.copy_(torch.from_numpy(inputgen.raw_normal(30 + i, (T, H))))
+        for c in caches:
+            c.k.zero_(), c.v.zero_()
+        ye = bufs[1].run(layer, x, caches[1], batch, resid=x)
+        torch.cuda.synchronize()
+        yg.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(yg, ye), i
+        assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v), i
+        if i == 3:
+            assert torch.equal(yg[new[0]:], x[new[0]:])

@@ -414,3 +414,85 @@ def test_scores_far_from_zero(case, kind, log_q, log_k, log_unit, scale):
                 tol = tol + half * (ref.abs() + tol) + 2.0 ** -25
             bad = ~((o - ref).abs() <= tol)
             assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} outside, first {o[bad][0]} for {ref[bad][0]} ({sign} {out})"
+
+
+# Calls that the documentation allows and the lists above do not hold: heads
+# of every multiple of 8 among prompts, many heads on one kv head, the largest
+# pages, tables far wider than their sequences, windows as large as an int.
+WIDE = [
+    ([(70, 130), (3, 9)], 4, 2, 136, 16, 0, 0, 2),
+    ([(40, 200)], 2, 2, 200, 8, 33, 5, 2),
+    ([(65, 65)], 2, 1, 248, 64, 0, 0, 2),
+    ([(60, 300)], 4, 1, 8, 32, 0, 0, 2),
+    ([(33, 90)], 2, 1, 104, 1, 0, 0, 2),
+    ([(1, 300), (2, 40)], 1024, 1, 16, 16, 0, 0, 2),
+    ([(1, 5000), (50, 4100)], 4, 2, 64, 4096, 0, 0, 1),
+    ([(3, 90), (1, 700)], 8, 2, 128, 16, 0, 0, 9000),
+    ([(100, 100), (7, 400)], 8, 2, 128, 16, 0, 0, 9000),
+    ([(100, 100)], 4, 2, 128, 1, 0, 0, 5000),
+    ([(40, 40)] * 64, 8, 8, 128, 16, 0, 0, 4090),
+    ([(40, 40)] * 64, 8, 8, 128, 16, 0, 0, 4100),
+    ([(5, 300), (90, 200)], 4, 2, 64, 16, (1 << 31) - 1, (1 << 31) - 1, 2),
+    ([(2, 300), (1, 200)], 4, 2, 64, 16, (1 << 31) - 1, 7, 2),
+    ([(2, 300), (70, 200)], 4, 2, 64, 16, 5, (1 << 31) - 1, 2),
+]
+
+
+@pytest.mark.parametrize("kind,out", [("bf16", "same"), ("f16", "f32")])
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_wide_range(case, kind, out):
+    lens, heads, kv, dim, page, window, sinks, more = WIDE[case]
+    check(lens, heads, kv, dim, page, kind, window, sinks, out=out, seed=600 + case, extra_entries=more, tail=1)
+
+
+@pytest.mark.parametrize("rows", [1, 60])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_query_that_is_not_finite(rows, value):
+    """One query head with NaN or an infinity makes its own result NaN and
+    leaves every other as it is."""
+    need_gpu()
+    b = Batch([(rows, 700), (rows, 90)], 16, 2, 64, "bf16", seed=15)
+    q = torch.randn((2 * rows, 8, 64), generator=torch.Generator().manual_seed(8)).to(b.dtype)
+    ref, mag, dots = attn_exact(b, q, 0.125)
+    q[rows // 2, 3, 5] = value
+    o = run(b, q, 0.125)
+    assert torch.isnan(o[rows // 2, 3]).all()
+    ok = (o.double() - ref).abs() <= attn_bound(b, ref, mag, dots, o.dtype, False)
+    ok[rows // 2, 3] = True
+    assert ok.all()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_two_calls_at_once(rows):
+    """Two calls on two streams, each with its workspace, over one cache."""
+    need_gpu()
+    b = Batch([(rows, 3000)], 32, 1, 64, "f16", seed=16)
+    cache, batch = b.device(R)
+    n = R.attn_workspace_bytes(cache, batch, 8)
+    assert n > 0
+    q = [torch.randn((rows, 8, 64), generator=torch.Generator().manual_seed(i)).to(b.dtype).cuda() for i in range(2)]
+    want = [run(b, x, 0.125) for x in q]
+    cache, batch = b.device(R)
+    o = [torch.empty((rows, 8, 64), device="cuda") for _ in q]
+    ws = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            R.attn(q[i], cache, batch, o[i], 0.125, 0, 0, ws[i], stream=s)
+    torch.cuda.synchronize()
+    for got, w in zip(o, want):
+        assert torch.equal(got.cpu(), w)
+
+
+def test_sequences_that_share_pages():
+    """A common beginning: two sequences name the same pages, one a page
+    twice."""
+    need_gpu()
+    b = Batch([(2, 100), (40, 140)], 16, 2, 64, "bf16", seed=17)
+    b.table[0, :4] = b.table[1, :4]
+    b.table[1, 6] = b.table[1, 2]
+    q = torch.randn((42, 4, 64), generator=torch.Generator().manual_seed(8)).to(b.dtype)
+    o = run(b, q, 0.125)
+    ref, mag, dots = attn_exact(b, q, 0.125)
+    assert ((o.double() - ref).abs() <= attn_bound(b, ref, mag, dots, o.dtype, False)).all()

@@ -266,3 +266,34 @@ def test_workspace_shared_where_slots_are_many(rows, cols):
     for _ in range(2):
         many.check(many.run(ws=ws))
         assert np.array_equal(few.run(ws=ws), first)
+
+
+@pytest.mark.parametrize("fmt", [3, 4])
+@pytest.mark.parametrize("q", [2, 40])
+def test_unaligned_results_and_residuals(fmt, q):
+    """y, resid and bias at 4-byte addresses, with rows a multiple of four."""
+    need_gpu()
+    c = Case(fmt, q, 512, 544, seed=6)
+    bufs = [torch.full((q * 512 + 8,), 5.0, device="cuda") for _ in range(2)]
+    for at, ar in ((1, 0), (0, 3), (2, 1)):
+        y, r = (b[4 + o:4 + o + q * 512].view(q, 512) for b, o in zip(bufs, (at, ar)))
+        bufs[0].fill_(5.0)
+        r.copy_(torch.from_numpy(c.resid))
+        bias = torch.zeros(513, device="cuda")
+        bias[1:] = torch.from_numpy(c.bias)
+        R.gemm(c.dW, c.xq, c.xs, c.xsum, q, y, bias[1:], R.ACT_GELU, r, c.workspace())
+        c.check(y.cpu().numpy().astype(np.float64), "gelu", True, True)
+        assert (bufs[0][:4 + at] == 5).all() and (bufs[0][4 + at + q * 512:] == 5).all()
+
+
+@pytest.mark.parametrize("q", [4, 40])
+def test_buffers_larger_than_the_call(q):
+    """The first q columns of larger activation buffers."""
+    need_gpu()
+    c = Case(4, q + 9, 200, 1024, seed=6)
+    y = torch.full((q + 9, 200), 5.0, device="cuda")
+    n = R.gemm_workspace_bytes(c.dW, q)
+    R.gemm(c.dW, c.xq, c.xs, c.xsum, q, y, ws=torch.zeros(n, dtype=torch.uint8, device="cuda") if n else None)
+    assert (y[q:] == 5).all()
+    c.z, c.mag = c.z[:q], c.mag[:q]
+    c.check(y[:q].cpu().numpy().astype(np.float64))
