@@ -254,7 +254,9 @@ class AttentionBuffers:
         self.x_act, self.o_act = act(H), act(O)
         self.q, self.k, self.v = (empty(T, h, D) for h in (attn.n_heads, attn.n_kv_heads, attn.n_kv_heads))
         self.q16 = empty(T, attn.n_heads, D, dtype=cache.dtype)
-        self.o, self.y = empty(T, attn.n_heads, D), empty(T, H)
+        with torch.inference_mode(False): # run clears o, inside such a mode or not
+            self.o = empty(T, attn.n_heads, D)
+        self.y = empty(T, H)
         mats = (attn.wq, attn.wk, attn.wv, attn.wo)
         self.ws_gemm = zeros(max(gemm_workspace_bytes(W, T) for W in mats))
         self.ws_attn = zeros(attn_workspace_bytes(cache, batch, attn.n_heads))

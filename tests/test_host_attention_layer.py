@@ -101,6 +101,15 @@ def test_a_format_that_needs_more_workspace(T, launched):
         buf.run(large, torch.zeros(T, 64), cache(), batch(T))
 
 
+def test_buffers_made_in_inference_mode(launched):
+    with torch.inference_mode():
+        own, c, b, x = layer(), cache(), batch(3), torch.zeros(3, 64)
+        buf = R.AttentionBuffers(own, c, b, device="cpu")
+        buf.run(own, x, c, b)
+    buf.run(own, x, c, b)
+    assert launched.count("attn") == 2
+
+
 def test_layer_refuses_its_arguments():
     for kw in (dict(heads=4, kv_heads=3), dict(window=-1), dict(sinks=-1), dict(eps=-1.0), dict(eps=float("nan")),
                dict(scale=0.0), dict(scale=float("nan"))):
