@@ -158,7 +158,10 @@ struct Plan {
 // workgroups) 500 and 586, 4096 (512) 145 and 171, 1000 after 30000 (four
 // splits of 121 tiles) 466 and 547; but 2048 (256) 90 and 69, 256 after
 // 8000 (sixteen splits of 9 tiles) 62 and 57. Its list of page ids has to
-// fit the LDS.
+// fit the LDS. The host knows the table's width, not the lengths, and a width
+// far beyond them misleads it: 2048 tokens with a table for 131072 take this
+// kernel, 89 us where the exact table takes 64; and with pages of 16 a table
+// past 65536 tokens rules it out (8192 tokens 597 us, 515 with the exact one).
 bool pair_rows(const rfx_kv_cache *C, const rfx_kv_batch *B, int64_t rows, int dp)
 {
     const int64_t keys = (int64_t)B->table_stride * C->page_size;
@@ -172,7 +175,9 @@ bool pair_rows(const rfx_kv_cache *C, const rfx_kv_batch *B, int64_t rows, int d
 // head) in one pass over the keys, 16 with heads over 128 elements (its
 // accumulators would not fit the registers); more rows go to the prefill
 // kernel, whose matrix-core tiles have 32. Keys are split as far as needed
-// for about two workgroups per compute unit.
+// for about two workgroups per compute unit, by the table's width: where it
+// could hold enough to be split the join is launched, for short sequences too
+// (one token, 400 keys: 8.1 us, 10.5 with a table for 131072).
 Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, int n_heads)
 {
     Plan p{};

@@ -68,7 +68,10 @@ __device__ __forceinline__ void subtract_max(f32x16 (&s)[NK], float m)
 
 // Heads of 64 fit three waves per SIMD in 168 registers, of 128 two in 256.
 // Six prompts with a window, fp16 with an fp32 result: 272 us with two waves,
-// 248 with three; with bf16's three terms 65 (2048 tokens) and 71.
+// 248 with three; with bf16's three terms 65 (2048 tokens) and 71. Heads of 256
+// leave room for one: 2048 tokens, 16 heads over 2, bf16, two splits, 109 us
+// (315 TFLOP/s; 132 for an fp32 result), the matrix pipe 19 % busy and nothing
+// beside the wave that waits.
 constexpr int waves_per_simd(int dp, int terms) { return dp <= 64 && terms < 3 ? 3 : dp <= 128 ? 2 : 1; }
 
 template <class T, int DP, int TERMS>
@@ -345,9 +348,11 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
 // 8192 tokens of 32 heads of 128 over 8, bf16: 500 us (1100 TFLOP/s), 586 with
 // the kernel above, whose two waves per SIMD meet on the same pipe as often
 // as not. Where the staging and the packing of weights stand, and a shorter
-// path for tiles without a mask, move this by less than 1 %: it is near the
-// power that bounds the products alone (a large library product reaches 1371
-// TFLOP/s).
+// path for tiles without a mask, move this by less than 1 %. By counters the
+// matrix pipe is busy 58 % and the vector pipe 50 % of the time; what holds the
+// rest was not found (a large library product reaches 1371 TFLOP/s; power was
+// not recorded). An fp32 result (three terms, twice the products in all) takes
+// 864 us, the matrix pipe 74 % busy.
 __device__ __forceinline__ void phase_end()
 {
     asm volatile("" ::: "memory");

@@ -7,18 +7,19 @@
 // Per 32-weight block the product is the exact integer block dot D on
 // v_mfma_f32_16x16x32_f16 (both sides' codes as f16, sums below 2^24), then
 // acc += D * (weight scale * activation scale) in fp32, as in the prefill
-// FFN. Bound by the matrix pipe: 16 cycles for a 16 x 16 block product and 8
-// for its scale products (v_mfma_f32_4x4x1), beside 16 cycles of fused
-// multiply-adds and the weights' decode on the vector pipe. A wave therefore
-// takes two 16-row weight tiles, decoded in registers, against up to eight
-// 16-column tiles: the decode (about 15 operations per weight tile and
-// block) is spread over the columns, and each column fragment read from LDS
-// serves two products. A workgroup of eight waves covers 256 rows and up to
-// 128 columns; per 256-element K tile its column fragments arrive in LDS by
-// direct loads from a copy of the codes in fragment order, made by a first
-// launch ([column tile][block][lane] x 16 bytes of f16, zero past q and K, so
-// the loop has no bounds to check). 2048 columns of 4096 x 7168:
-// 212 us for FP2, 215 for FP3 (570 TFLOP/s).
+// FFN. A 16 x 16 block product takes the matrix pipe 16 cycles and its scale
+// products (v_mfma_f32_4x4x1) 8, beside 16 cycles of fused multiply-adds and
+// the weights' decode on the vector pipe. Neither pipe is full: by counters
+// the vector pipe is busy 56 % of the time, the matrix pipe 38 %, LDS 19 %, so
+// the two waves of a SIMD mostly take turns. A wave takes two 16-row weight
+// tiles, decoded in registers, against up to eight 16-column tiles: the decode
+// (about 15 operations per weight tile and block) is spread over the columns,
+// and each column fragment read from LDS serves two products. A workgroup of
+// eight waves covers 256 rows and up to 128 columns; per 256-element K tile its
+// column fragments arrive in LDS by direct loads from a copy of the codes in
+// fragment order, made by a first launch ([column tile][block][lane] x 16
+// bytes of f16, zero past q and K, so the loop has no bounds to check). 2048
+// columns of 4096 x 7168: 210 us for FP2, 209 for FP3 (575 TFLOP/s).
 // Few row and column blocks: K is split over workgroups, and a last launch
 // adds the partials in split order and applies the epilogue.
 #include "rfx_gemm.h"

@@ -206,8 +206,9 @@ int launch(const RopeArgs &a, hipStream_t st)
     const int passes = (H + per - 1) / per;
     const bool few = a.kv.n_tokens < 512;
     const dim3 grid(a.kv.n_tokens, few ? passes : 1), block(256);
-    // many tokens' rows are more than the caches hold until they are used:
-    // past them (79 to 71 us for 10858 tokens of 48 heads of 128)
+    // Many tokens' rows are more than the caches hold until they are used:
+    // past them (79 to 71 us for 10858 tokens of 48 heads of 128, the only
+    // size it was measured at; 512 tokens, 19 MB, would fit them).
 #define RFX_ROPE(LPH)                                                               \
     if (few)                                                                        \
         hipLaunchKernelGGL((rope_kernel<T, LPH, false>), grid, block, 0, st, a);    \

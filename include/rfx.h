@@ -259,8 +259,8 @@ int rfx_gemv_grouped(const rfx_gemv_job *jobs, int n_jobs, void *ws, size_t ws_b
  * (or 2^-130, if that is more), and sums exact products in fp32; a block
  * whose largest |xs code| is not finite makes its column NaN.
  * W: count must be 1; any format at q <= 4, RFX_FP2, RFX_FP3 or RFX_FP4 of at
- * most 2^30 rows and 2^29 columns at q > 4 (RFX_E_UNSUPPORTED otherwise). q 1..RFX_GEMM_MAX_Q. xq, xs and xsum
- * as for rfx_gemv. bias fp32 [N] or NULL; act: RFX_ACT_SILU is z / (1 +
+ * most 2^30 rows and 2^29 columns at q > 4 (RFX_E_UNSUPPORTED otherwise).
+ * q 1..RFX_GEMM_MAX_Q. xq, xs and xsum as for rfx_gemv. bias fp32 [N] or NULL; act: RFX_ACT_SILU is z / (1 +
  * e^-z), RFX_ACT_GELU z Phi(z), RFX_ACT_GELU_TANH its tanh approximation 0.5
  * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))); resid fp32 [q][N] or NULL,
  * and may be y itself. y fp32 [q][N] overlaps no other argument.
@@ -515,14 +515,16 @@ int rfx_qk_norm_rope(const rfx_qk_rope *args, const rfx_kv_cache *cache, const r
  * window or j < sinks (the first tokens, which stay visible). A row that
  * sees nothing is zero. q [n_tokens][n_heads][head_dim] in the cache's type;
  * out the same shape in out_type: RFX_F32 (what rfx_quantize_act takes) or
- * the cache's type. Scores, softmax and sums are fp32; for an fp32 result
- * the softmax weights enter the matrix core as two (fp16) or three (bf16)
- * terms, for a 16-bit result of more than a few rows per kv head as one.
+ * the cache's type; it overlaps no other argument. Scores, softmax and sums
+ * are fp32; for an fp32 result the softmax weights enter the matrix core as
+ * two (fp16) or three (bf16) terms, for a 16-bit result of more than 32 rows
+ * (new tokens x query heads) per kv head, 16 with heads over 128, as one: off
+ * by half a step of that type, as the result itself is. Who wants a 16-bit
+ * result of the full weights takes fp32 and rounds it.
  * Cached keys and values that a sequence's tokens see are assumed finite, and
- * so are the fp32 scores q k^T (of any size); a
- * key outside every row's window, and every slot past kv_len, may hold
- * anything. Results do not depend on timing: splits of the keys are joined
- * in a fixed order.
+ * so are the fp32 scores q k^T (of any size); a key outside every row's
+ * window, and every slot past kv_len, may hold anything. Results do not
+ * depend on timing: splits of the keys are joined in a fixed order.
  * ws: workspace of rfx_attn_workspace_bytes (which depends on n_seq, max_q,
  * table_stride, the page size and the heads), 256-B aligned, NULL allowed
  * when that is 0; it needs no initialisation and holds anything after the
