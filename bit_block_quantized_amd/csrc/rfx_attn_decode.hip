@@ -6,7 +6,7 @@
 // TB/s): every visible key and value is read once, for all rows of its kv
 // head. Smaller calls are bound by latency: four tokens of eight sequences of
 // 4000 to 8192 keys, 32 rows, take 22 us (and 4.5 for the join) for 90 MB with
-// the matrix pipe 12 % and the vector pipe 23 % busy; a wave's four tiles come
+// the matrix pipe 11 % and the vector pipe 21 % busy; a wave's four tiles come
 // after three dependent loads, one in flight at a time. A wave takes tiles of
 // 32 keys; its keys and values of the next tile are in flight while it
 // computes the current one.
