@@ -90,7 +90,20 @@ class QkRopeC(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
-# Element types of queries, cache and attention output.
+class NormC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("delta", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("delta_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("sum", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("xq", ctypes.c_void_p), ("xs", ctypes.c_void_p), ("xsum", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("q", ctypes.c_int32), ("cols", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class LogprobC(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("q", ctypes.c_int32), ("n_vocab", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("logprob", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("rank", ctypes.c_void_p), ("top_index", ctypes.c_void_p), ("top_logprob", ctypes.c_void_p)]
+
+
+# Element types of queries, cache, attention output and logits.
 F32, F16, BF16 = 0, 1, 2
 
 _P = ctypes.c_void_p
@@ -135,6 +148,9 @@ _SIGS = {
     "rfx_qk_norm_rope": ([_P, _P, _P, _P, _P], _I),
     "rfx_attn_workspace_bytes": ([_P, _P, _I], _SZ),
     "rfx_attn": ([_P, _P, _P, _I, _F, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "rfx_add_rms_norm": ([_P, _P], _I),
+    "rfx_token_logprobs_workspace_bytes": ([_I, _I, _I], _SZ),
+    "rfx_token_logprobs": ([_P, _I64, _P, _P, _P, _SZ, _P], _I),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -654,6 +670,107 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
     wp, wn = _workspace(ws, dev)
     _call_on(dev, stream, lib().rfx_attn, qp, cache.c_ref, batch.c_ref, Hq, scale, window, sinks, op, _elem(out.dtype),
              wp, wn)
+
+
+# ------------------------------------------- norm, log probabilities
+
+def _rows(t, name, shape, index):
+    """Address and row stride of float32 [q][cols]; rows may be part of
+    longer ones."""
+    if t.dtype is not _Torch.f32 or t.shape != shape:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, float32 {tuple(shape)} wanted")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, not GPU {index}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    row, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: elements of a row are not contiguous (strides {t.stride()})")
+    return t.data_ptr(), row if shape[0] > 1 else shape[1]
+
+
+# rfx_norm, packed in one go like rfx_qk_rope
+_pack_norm = struct.Struct("2P2q6Pf3i").pack
+
+
+def add_rms_norm(x, weight, eps, delta=None, out=None, y=None, xq=None, xs=None, xsum=None, stream=None):
+    """h = x + delta into `out`, its RMS norm times weight (None: 1) into y,
+    that row's 8-bit activations into xq, xs, xsum (rfx_add_rms_norm); what is
+    None is not written. x, delta: float32 [q][cols], rows may be strided; out
+    and y float32 [q][cols]; xq int8 [q][cols], xs float32 and xsum int32
+    [q][cols / 32]."""
+    t = _torch()
+    f32, shape, dev = t.f32, x.shape, x.get_device()
+    q, cols = shape
+    xp, x_stride = _rows(x, "x", shape, dev)
+    dp, d_stride = (0, 0) if delta is None else _rows(delta, "delta", shape, dev)
+    qp = sp = np_ = 0
+    if xq is not None:
+        blocks = (q, cols // 32)
+        qp = _want(xq, "xq", t.i8, shape, dev)
+        sp = _want(xs, "xs", f32, blocks, dev)
+        np_ = _want(xsum, "xsum", t.i32, blocks, dev)
+    elif xs is not None or xsum is not None:
+        raise ValueError("xs and xsum without xq")
+    wp = 0 if weight is None else _want(weight, "weight", f32, (cols,), dev)
+    op = 0 if out is None else _want(out, "out", f32, shape, dev)
+    yp = 0 if y is None else _want(y, "y", f32, shape, dev)
+    if q: # an empty tensor has no address
+        _call_on(dev, stream, lib().rfx_add_rms_norm,
+                 _pack_norm(xp, dp, x_stride, d_stride, wp, op, yp, qp, sp, np_, eps, q, cols, 0))
+
+
+def token_logprobs_workspace_bytes(q: int, n_vocab: int, top_k: int) -> int:
+    _int32(q=q, n_vocab=n_vocab, top_k=top_k)
+    return int(lib().rfx_token_logprobs_workspace_bytes(q, n_vocab, top_k))
+
+
+class LogprobBuffers:
+    """What rfx_token_logprobs says of q rows of n_vocab logits: logprob and
+    rank of the given tokens, lse and entropy [q], and the top_k largest
+    logits' top_index and top_logprob [q][top_k]; with its workspace."""
+
+    def __init__(self, q: int, n_vocab: int, top_k: int = 0, device="cuda"):
+        import torch
+        if q < 1 or n_vocab < 1 or not 0 <= top_k <= 64:
+            raise ValueError(f"q {q}, n_vocab {n_vocab}, top_k {top_k}")
+        need = token_logprobs_workspace_bytes(q, n_vocab, top_k)
+        if not need:
+            raise ValueError(f"q {q} (at most 65536), n_vocab {n_vocab} (at most 2^19)")
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.q, self.n_vocab, self.top_k = q, n_vocab, top_k
+        self.logprob, self.lse, self.entropy = empty(q), empty(q), empty(q)
+        self.rank = empty(q, dtype=torch.int32)
+        self.top_index, self.top_logprob = empty(q, top_k, dtype=torch.int32), empty(q, top_k)
+        self.ws = empty(need, dtype=torch.uint8)
+        self.index = self.ws.get_device()
+        top = [t.data_ptr() if top_k else None for t in (self.top_index, self.top_logprob)]
+        rest = [t.data_ptr() for t in (self.logprob, self.lse, self.entropy, self.rank)]
+        # per type, with tokens and without
+        self._c = {d: (LogprobC(e, q, n_vocab, top_k, *rest, *top), LogprobC(e, q, n_vocab, top_k, None, *rest[1:3], None, *top))
+                   for d, e in _torch().elem.items()}
+
+    def run(self, logits, tokens=None, stream=None):
+        """logits [q][n_vocab] in float32, float16 or bfloat16, rows may be
+        strided; tokens int32 [q], a token outside 0..n_vocab - 1 being none,
+        or None: then logprob and rank keep what they hold."""
+        c, dev = self._c.get(logits.dtype), self.index
+        if c is None or logits.shape != (self.q, self.n_vocab):
+            raise ValueError(f"logits: {logits.dtype} {tuple(logits.shape)}, {(self.q, self.n_vocab)} in float32, float16 or "
+                             "bfloat16 wanted")
+        if logits.get_device() != dev:
+            raise ValueError(f"logits: on {logits.device}, not GPU {dev}")
+        row, one = logits.stride()
+        if one != 1 and self.n_vocab > 1:
+            raise ValueError(f"logits: elements of a row are not contiguous (strides {logits.stride()})")
+        if tokens is not None:
+            tokens = _want(tokens, "tokens", _torch().i32, (self.q,), dev)
+        _call_on(dev, stream, lib().rfx_token_logprobs, logits.data_ptr(), row if self.q > 1 else self.n_vocab, tokens,
+                 ctypes.byref(c[tokens is None]), self.ws.data_ptr(), self.ws.nbytes)
+        return self
 
 
 from .layer import (AttentionBuffers, DeviceAttention, DeviceMoeLayer, MoeBuffers, PlacedMoeLayer,  # noqa: E402,F401

@@ -537,6 +537,71 @@ size_t rfx_attn_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *b
 int rfx_attn(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads, float scale,
              int window, int sinks, void *out, int out_type, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------ */
+/* Residual norm, adapters, log probabilities.                         */
+/* ------------------------------------------------------------------ */
+/* The residual's addition and the RMS norm before a half layer, with the
+ * activations as the packed products take them:
+ *   h = x + delta (fp32; x where delta is NULL),
+ *   y = h w / sqrt(mean(h^2) + eps) (w = 1 where weight is NULL),
+ * and of y per 32 elements s = max |y| * (1 / 127) (fp32; within one step of
+ * rfx_quantize_act's quotient), code = clamp(round half to even(y / s), -127,
+ * 127), s = 0 -> codes 0, and the codes' sum. The mean, the root and the
+ * products are fp64 and y is rounded to fp32 once, so results do not depend
+ * on the order of a sum. A row whose mean square and eps are zero gives y = 0.
+ * Any output may be NULL, but not all; xs and xsum are wanted with xq. sum
+ * [q][cols] takes h; it may be x or delta where their rows are contiguous,
+ * and so may y if it is not sum too. q may be 0; cols a multiple of 32, at
+ * most 2^20, q at most 2^21. One launch.
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_HIP. */
+typedef struct rfx_norm {
+    const float *x, *delta;           /* fp32 [q][cols], 16-B aligned; delta may be NULL */
+    int64_t x_stride, delta_stride;   /* elements between rows: multiples of 4, at least cols */
+    const float *weight;              /* fp32 [cols], 16-B aligned, or NULL */
+    float *sum, *y;                   /* fp32 [q][cols], 16-B aligned, or NULL */
+    int8_t *xq;                       /* [q][cols], 16-B aligned, or NULL */
+    float *xs;                        /* [q][cols / 32] */
+    int32_t *xsum;                    /* [q][cols / 32] */
+    float eps;                        /* >= 0 */
+    int32_t q, cols, reserved;
+} rfx_norm;
+int rfx_add_rms_norm(const rfx_norm *args, void *stream);
+
+/* What a head's logits z [q][n_vocab] say of each row: lse = log sum e^z,
+ * entropy = -sum p log p (natural logarithms, p = e^(z - lse)), the given
+ * token's logprob = z[token] - lse and rank (how many logits are larger), and
+ * the top_k largest logits in descending order, equal ones by the lower index.
+ * Logits may be -inf (excluded tokens): they have logprob -inf and are no
+ * alternatives; where fewer than top_k are left, the places behind have
+ * top_index -1 and top_logprob -inf. A row that is all -inf has lse and
+ * logprob -inf and entropy 0. A token outside 0..n_vocab - 1 is none: its
+ * logprob is 0 and its rank -1. A NaN or +inf among a row's logits makes its
+ * logprob, lse, entropy and top_logprob NaN. Sums over a chunk of logits are
+ * fp32, over chunks fp64. Results are deterministic.
+ * Any output may be NULL, but not all. ws: workspace of
+ * rfx_token_logprobs_workspace_bytes, 256-B aligned; it needs no
+ * initialisation and holds anything afterwards. Calls that can run
+ * concurrently must not share it. Two launches.
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
+#define RFX_LOGPROB_MAX_Q 65536
+typedef struct rfx_logprob {
+    int32_t type;       /* of the logits: RFX_F32, RFX_F16 or RFX_BF16 */
+    int32_t q;          /* rows, 0..RFX_LOGPROB_MAX_Q */
+    int32_t n_vocab;    /* 1..2^19 */
+    int32_t top_k;      /* 0..64 */
+    float *logprob;     /* [q] */
+    float *lse;         /* [q] */
+    float *entropy;     /* [q] */
+    int32_t *rank;      /* [q] */
+    int32_t *top_index; /* [q][top_k] */
+    float *top_logprob; /* [q][top_k] */
+} rfx_logprob;
+size_t rfx_token_logprobs_workspace_bytes(int q, int n_vocab, int top_k);
+/* logits: rows `stride` elements apart (>= n_vocab), aligned to their type.
+ * tokens int32 [q] on the device, or NULL with logprob and rank NULL. */
+int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens, const rfx_logprob *out, void *ws,
+                       size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
