@@ -97,6 +97,20 @@ class NormC(ctypes.Structure):
                 ("eps", ctypes.c_float), ("q", ctypes.c_int32), ("cols", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class LoraMatC(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("resid", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+LORA_MAX_MATS = 4
+
+
+class LoraC(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("n_mats", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("ids", ctypes.c_void_p), ("mats", LoraMatC * LORA_MAX_MATS)]
+
+
 class LogprobC(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int32), ("q", ctypes.c_int32), ("n_vocab", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("logprob", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
@@ -149,6 +163,8 @@ _SIGS = {
     "rfx_attn_workspace_bytes": ([_P, _P, _I], _SZ),
     "rfx_attn": ([_P, _P, _P, _I, _F, _I, _I, _P, _I, _P, _SZ, _P], _I),
     "rfx_add_rms_norm": ([_P, _P], _I),
+    "rfx_lora_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
+    "rfx_lora_apply": ([_P, _P, _SZ, _P], _I),
     "rfx_token_logprobs_workspace_bytes": ([_I, _I, _I], _SZ),
     "rfx_token_logprobs": ([_P, _I64, _P, _P, _P, _SZ, _P], _I),
 }
@@ -672,7 +688,7 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
              wp, wn)
 
 
-# ------------------------------------------- norm, log probabilities
+# --------------------------------- norm, adapters, log probabilities
 
 def _rows(t, name, shape, index):
     """Address and row stride of float32 [q][cols]; rows may be part of
@@ -718,6 +734,65 @@ def add_rms_norm(x, weight, eps, delta=None, out=None, y=None, xq=None, xs=None,
     if q: # an empty tensor has no address
         _call_on(dev, stream, lib().rfx_add_rms_norm,
                  _pack_norm(xp, dp, x_stride, d_stride, wp, op, yp, qp, sp, np_, eps, q, cols, 0))
+
+
+class DeviceLora:
+    """The low-rank adapters of one projection (kept alive here): a
+    [n_adapters][rank][cols] and b [n_adapters][rows][rank] in float16 or
+    bfloat16, scale float32 [n_adapters] (alpha / rank) or None for 1."""
+
+    def __init__(self, a, b, scale=None):
+        n, rank, cols = a.shape
+        if a.dtype != b.dtype or _elem(a.dtype) == F32:
+            raise ValueError(f"adapters in {a.dtype} and {b.dtype}: both float16 or both bfloat16")
+        if not 8 <= rank <= 128 or rank % 8 or cols % 32 or not cols:
+            raise ValueError(f"rank {rank} (a multiple of 8, at most 128), cols {cols} (a multiple of 32)")
+        if b.dim() != 3:
+            raise ValueError(f"b: {tuple(b.shape)}, {(n, 'rows', rank)} wanted")
+        self.a, self.b, self.scale = a, b, scale
+        self.n_adapters, self.rank, self.cols, self.rows = n, rank, cols, b.shape[1]
+        self.index = a.get_device()
+        self.pointers = (_want(a, "a", a.dtype, a.shape, self.index), _want(b, "b", a.dtype, (n, self.rows, rank), self.index),
+                         0 if scale is None else _want(scale, "scale", _torch().f32, (n,), self.index))
+        # what matrices of one call have in common
+        self.kind = (_elem(a.dtype), n, rank, cols)
+
+
+def lora_workspace_bytes(loras, n_tokens: int) -> int:
+    """For calls of these adapters (of one rank and columns) over n_tokens."""
+    first = loras[0]
+    _int32(n_tokens=n_tokens)
+    return int(lib().rfx_lora_workspace_bytes(n_tokens, first.rank, len(loras), first.cols, first.n_adapters))
+
+
+# rfx_lora up to its matrices, and one of those
+_pack_lora, _pack_lora_mat = struct.Struct("6iPqP").pack, struct.Struct("5P2i").pack
+
+
+def lora(x, ids, loras, ys, resids=None, ws=None, stream=None):
+    """y = resid + scale B (A x) with each token's adapter, for up to four
+    matrices over the same x (rfx_lora_apply). x: float32 [n_tokens][cols],
+    rows may be strided; ids int32 [n_tokens] on the device, a token whose id
+    is outside 0..n_adapters - 1 having none; loras: DeviceLora of one type,
+    rank, number and columns; ys float32 [n_tokens][rows]; resids the same
+    shapes, an entry None for 0; resids None: ys are added to in place."""
+    first = loras[0]
+    dev, (T, _) = first.index, x.shape
+    f32 = _torch().f32
+    if len(loras) > LORA_MAX_MATS or len(ys) != len(loras) or (resids is not None and len(resids) != len(loras)):
+        raise ValueError(f"{len(loras)} matrices (at most {LORA_MAX_MATS}), {len(ys)} results")
+    xp, x_stride = _rows(x, "x", (T, first.cols), dev)
+    args = [_pack_lora(*first.kind, T, len(loras), xp, x_stride, _want(ids, "ids", _Torch.i32, (T,), dev))]
+    for i, (m, y) in enumerate(zip(loras, ys)):
+        if m.kind != first.kind or m.index != dev:
+            raise ValueError(f"matrix {i}: (type, adapters, rank, cols) {m.kind} on GPU {m.index}, {first.kind} on GPU {dev} wanted")
+        shape = (T, m.rows)
+        yp = _want(y, "y", f32, shape, dev)
+        r = y if resids is None else resids[i]
+        args.append(_pack_lora_mat(*m.pointers, 0 if r is None else yp if r is y else _want(r, "resid", f32, shape, dev), yp, m.rows, 0))
+    if T: # an empty tensor has no address
+        wp, wn = _workspace(ws, dev)
+        _call_on(dev, stream, lib().rfx_lora_apply, b"".join(args).ljust(ctypes.sizeof(LoraC), b"\0"), wp, wn)
 
 
 def token_logprobs_workspace_bytes(q: int, n_vocab: int, top_k: int) -> int:

@@ -1,0 +1,455 @@
+// Low-rank adapters of many requests beside a shared projection:
+//
+//   y[t] = resid[t] + c[a] B[a] (A[a] x[t]),   a = ids[t],
+//
+// A[a] of rank x cols, B[a] of rows x rank, for up to four matrices (query,
+// key and value projections) over the same x. Two launches: v = A x into the
+// workspace, then y.
+//
+// Few tokens are bound by the adapters' bytes (each token may have its own),
+// prompts by x, resid and y. Both launches take 16 tokens as the columns of
+// v_mfma_16x16x32 products whose rows are one adapter's, for each adapter
+// among the 16 tokens in turn; the columns of other adapters' tokens are zero,
+// so one accumulator collects all. Tokens may have any order of adapters;
+// runs of one adapter (a prompt) cost one pass.
+//
+// Adapters are 16-bit, x and v fp32: these enter as 16-bit terms, bf16 as
+// three that sum to the fp32 value, fp16 as two (the second 2^11 larger, with
+// sums of its own, so that it stays clear of fp16's subnormals), 2^-22 of the
+// value. Sums are fp32.
+#include "rfx_kv.h"
+
+using namespace rfx;
+using namespace rfx::dev;
+
+namespace {
+
+constexpr int kMaxRank = 128;
+constexpr int kMats = RFX_LORA_MAX_MATS;
+constexpr int kMaxLoraTokens = 1 << 19; // 16 a workgroup along the grid's y
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kMaxSplits = 16;
+
+struct LoraArgs {
+    rfx_lora l;
+    int R16;          // rank in whole tiles of 16
+    int tiles;        // of all matrices
+    int groups;       // of up to eight tiles
+    int splits, slots;
+    int T16;          // tokens in whole tiles
+    float *v;         // [splits][T16][n_mats * R16]
+    int row_blocks[kMats]; // of the second launch
+    int vec;          // bit m: rows of matrix m are 16-byte aligned
+};
+
+// Terms of an fp32 operand and the sums that collect their products.
+template <class T>
+struct Terms;
+
+template <>
+struct Terms<BF16> {
+    static constexpr int N = 3, SUMS = 1;
+    static constexpr float IN = 1.0f;
+    static __device__ __forceinline__ void split(const float (&x)[8], u4 (&t)[3]) { split_terms<BF16, 3>(x, t); }
+    static __device__ __forceinline__ void mma(u4 a, const u4 (&t)[3], f32x4 (&c)[1])
+    {
+        c[0] = BF16::mma16(a, t[2], c[0]); // the smallest first
+        c[0] = BF16::mma16(a, t[1], c[0]);
+        c[0] = BF16::mma16(a, t[0], c[0]);
+    }
+    static __device__ __forceinline__ f32x4 total(const f32x4 (&c)[1]) { return c[0]; }
+};
+
+template <>
+struct Terms<F16> {
+    static constexpr int N = 2, SUMS = 2;
+    static constexpr float IN = 0x1p-4f; // x below 2^20 stays finite
+    static __device__ __forceinline__ void split(const float (&x)[8], u4 (&t)[2])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t u = F16::pack(x[2 * i], x[2 * i + 1]);
+            const f2 back = F16::unpack(u);
+            t[0][i] = u;
+            t[1][i] = F16::pack((x[2 * i] - back.x) * 0x1p11f, (x[2 * i + 1] - back.y) * 0x1p11f);
+        }
+    }
+    static __device__ __forceinline__ void mma(u4 a, const u4 (&t)[2], f32x4 (&c)[2])
+    {
+        c[0] = F16::mma16(a, t[0], c[0]);
+        c[1] = F16::mma16(a, t[1], c[1]);
+    }
+    static __device__ __forceinline__ f32x4 total(const f32x4 (&c)[2]) { return c[0] + c[1] * 0x1p-11f; }
+};
+
+// The adapter of token t, -1 for none.
+__device__ __forceinline__ int adapter_of(const rfx_lora &l, int t)
+{
+    if (t >= l.n_tokens)
+        return -1;
+    const int a = l.ids[t];
+    return (unsigned)a < (unsigned)l.n_adapters ? a : -1;
+}
+
+// v = A x: a workgroup takes 16 tokens, one of `splits` parts of the columns
+// (a quarter of it per wave, added through LDS) and every slots-th adapter of
+// its tokens, against TILES of the 16-row tiles of all matrices, which stand
+// one after the other.
+template <class T, int TILES>
+__global__ __launch_bounds__(kThreads, 2) void lora_down_kernel(LoraArgs a)
+{
+    using X = Terms<T>;
+    __shared__ __align__(16) f32x4 sums[kWaves][TILES][64];
+    const rfx_lora &l = a.l;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int b = blockIdx.x;
+    const int split = b % a.splits;
+    b /= a.splits;
+    const int tile0 = b % a.groups * TILES;
+    b /= a.groups;
+    const int slot = b % a.slots, t0 = b / a.slots * 16;
+    const int steps = l.cols / 32, part = a.splits * kWaves, p = split * kWaves + wave;
+    const int k0 = (int)((int64_t)steps * p / part), k1 = (int)((int64_t)steps * (p + 1) / part);
+    const int id = adapter_of(l, t0 + r16);
+
+    f32x4 acc[TILES][X::SUMS];
+#pragma unroll
+    for (int i = 0; i < TILES; i++)
+#pragma unroll
+        for (int s = 0; s < X::SUMS; s++)
+            acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+
+    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
+    bool mine = false; // this workgroup has the lane's token
+    for (int n = 0; todo; n++) {
+        const int first = __builtin_ctz(todo), ad = __builtin_amdgcn_readlane(id, first);
+        const bool match = id == ad;
+        todo &= ~(uint32_t)__ballot(match);
+        if (n % a.slots != slot)
+            continue;
+        mine |= match;
+        const uint32_t keep = match ? ~0u : 0u;
+        // lanes of other adapters' tokens read along with the first one's
+        const float *x = l.x + (int64_t)(t0 + (match ? r16 : first)) * l.x_stride + 8 * g4;
+        const uint16_t *w[TILES];
+#pragma unroll
+        for (int i = 0; i < TILES; i++) {
+            const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + r16, l.rank - 1);
+            w[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * g4;
+        }
+        f32x4 xn[2];
+        u4 wn[TILES];
+        const auto load = [&](int k) {
+            xn[0] = *reinterpret_cast<const f32x4 *>(x + 32 * (size_t)k);
+            xn[1] = *reinterpret_cast<const f32x4 *>(x + 32 * (size_t)k + 4);
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+                wn[i] = *reinterpret_cast<const u4 *>(w[i] + 32 * (size_t)k);
+        };
+        if (k0 < k1)
+            load(k0);
+        for (int k = k0; k < k1; k++) {
+            float xc[8];
+            u4 wc[TILES], t[X::N];
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                xc[e] = xn[e >> 2][e & 3] * X::IN;
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+                wc[i] = wn[i];
+            load(min(k + 1, k1 - 1));
+            X::split(xc, t);
+#pragma unroll
+            for (int s = 0; s < X::N; s++)
+                t[s] &= keep;
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+                X::mma(wc[i], t, acc[i]);
+        }
+    }
+    if (!__ballot(mine)) // the same in every wave
+        return;
+#pragma unroll
+    for (int i = 0; i < TILES; i++)
+        sums[wave][i][lane] = X::total(acc[i]) * (1.0f / X::IN);
+    __syncthreads();
+    // lane: token r16, rows 4 g4 .. + 3 of tile i
+    const int RS = l.n_mats * a.R16;
+    for (int i = wave; i < min(TILES, a.tiles - tile0); i += kWaves) {
+        f32x4 s = sums[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; w++)
+            s += sums[w][i][lane];
+        if (mine)
+            *reinterpret_cast<f32x4 *>(a.v + ((size_t)split * a.T16 + t0 + r16) * RS + 16 * (tile0 + i) + 4 * g4) = s;
+    }
+}
+
+// y = resid + c B v: a wave takes 16 tokens and RT tiles of 16 rows. KS: steps
+// of 32 over the rank. Where rows are few per wave, ADS adapters' tiles are
+// read at a time.
+template <class T, int KS, int RT, int ADS>
+__global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
+{
+    using X = Terms<T>;
+    const rfx_lora &l = a.l;
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t0 = blockIdx.y * 16, t = t0 + r16;
+    int m = 0, rb = blockIdx.x;
+    while (m + 1 < l.n_mats && rb >= a.row_blocks[m])
+        rb -= a.row_blocks[m++];
+    const rfx_lora_mat &M = l.mats[m];
+    const int n0 = (rb * kWaves + wave) * 16 * RT;
+    if (n0 >= M.rows)
+        return;
+    const int id = adapter_of(l, t);
+    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
+    if (!todo && M.resid == M.y)
+        return;
+
+    f32x4 acc[RT][X::SUMS];
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+        for (int s = 0; s < X::SUMS; s++)
+            acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    float out = 1.0f;
+    if (todo) {
+        // the lane's part of its token's v: the splits in order, times the
+        // adapter's factor
+        const int RS = l.n_mats * a.R16;
+        float v[KS][8];
+        const float c = id >= 0 && M.scale ? M.scale[id] : 1.0f;
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            const int r = 32 * k + 8 * g4;
+            const bool on = id >= 0 && r < l.rank;
+            const float *p = a.v + (size_t)(on ? t : t0) * RS + m * a.R16 + (on ? r : 0);
+            f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; s++) {
+                s0 += *reinterpret_cast<const f32x4 *>(p + (size_t)s * a.T16 * RS);
+                s1 += *reinterpret_cast<const f32x4 *>(p + (size_t)s * a.T16 * RS + 4);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                v[k][e] = on ? s0[e] * c : 0.f;
+                v[k][e + 4] = on ? s1[e] * c : 0.f;
+            }
+        }
+        if (X::SUMS > 1) { // a token's v below 2 in magnitude: a power of two off, and on again below
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    top = fmaxf(top, fabsf(v[k][e]));
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const int ex = top > 0.f && top < INFINITY ? max(-100, min(100, (int)(__float_as_uint(top) >> 23) - 127)) : 0;
+            const float in = __uint_as_float((uint32_t)(127 - ex) << 23);
+            out = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    v[k][e] *= in;
+        }
+        u4 vt[KS][X::N];
+#pragma unroll
+        for (int k = 0; k < KS; k++)
+            X::split(v[k], vt[k]);
+
+        int ad = 0;
+        while (todo) {
+            uint32_t keep[ADS];
+            u4 w[ADS][RT][KS];
+#pragma unroll
+            for (int j = 0; j < ADS; j++) {
+                const bool more = todo != 0;
+                if (more)
+                    ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+                const bool match = more & (id == ad); // none left: the last one's again, for nobody
+                todo &= ~(uint32_t)__ballot(match);
+                keep[j] = match ? ~0u : 0u;
+                const uint16_t *p = static_cast<const uint16_t *>(M.b) + (size_t)ad * M.rows * l.rank;
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+#pragma unroll
+                    for (int k = 0; k < KS; k++) {
+                        const int n = min(n0 + 16 * i + r16, M.rows - 1), r = 32 * k + 8 * g4;
+                        const u4 x = *reinterpret_cast<const u4 *>(p + (size_t)n * l.rank + (r < l.rank ? r : 0));
+                        w[j][i][k] = r < l.rank ? x : (u4){0, 0, 0, 0};
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < ADS; j++)
+#pragma unroll
+                for (int k = 0; k < KS; k++) {
+                    u4 tm[X::N];
+#pragma unroll
+                    for (int s = 0; s < X::N; s++)
+                        tm[s] = vt[k][s] & keep[j];
+#pragma unroll
+                    for (int i = 0; i < RT; i++)
+                        X::mma(w[j][i][k], tm, acc[i]);
+                }
+        }
+    }
+    // lane: token r16, rows 4 g4 .. + 3 of tile i
+    if (t >= l.n_tokens)
+        return;
+#pragma unroll
+    for (int i = 0; i < RT; i++) {
+        const int n = n0 + 16 * i + 4 * g4, left = M.rows - n;
+        if (left <= 0)
+            continue;
+        const size_t at = (size_t)t * M.rows + n;
+        f32x4 y = X::total(acc[i]) * out;
+        if (a.vec >> m & 1) {
+            if (M.resid)
+                y += *reinterpret_cast<const f32x4 *>(M.resid + at);
+            *reinterpret_cast<f32x4 *>(M.y + at) = y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (e < left)
+                    M.y[at + e] = M.resid ? y[e] + M.resid[at + e] : y[e];
+        }
+    }
+}
+
+struct Plan {
+    int R16, tiles, groups, splits, slots, T16;
+    size_t bytes;
+};
+
+Plan plan(int T, int rank, int n_mats, int cols, int n_adapters)
+{
+    Plan p{};
+    p.R16 = (rank + 15) / 16 * 16;
+    p.tiles = n_mats * p.R16 / 16;
+    p.groups = (p.tiles + 7) / 8;
+    p.T16 = (T + 15) / 16 * 16;
+    const int blocks = p.T16 / 16 > 0 ? p.T16 / 16 : 1;
+    // Adapters of a block of tokens: side by side where tokens are few and
+    // may each have their own, one after the other where they are many.
+    p.slots = T <= 128 ? 16 : T <= 512 ? 4 : 1;
+    p.slots = p.slots < T ? p.slots : T;
+    p.slots = p.slots < n_adapters ? p.slots : n_adapters;
+    // Columns split until there are two workgroups per compute unit, down to
+    // a step of 32 columns per wave.
+    const int want = 512 / (blocks * p.groups), most = (cols + 127) / 128;
+    p.splits = want < most ? want : most;
+    p.splits = p.splits < 1 ? 1 : p.splits > kMaxSplits ? kMaxSplits : p.splits;
+    p.bytes = (size_t)p.splits * p.T16 * n_mats * p.R16 * sizeof(float);
+    return p;
+}
+
+bool shape_ok(int T, int rank, int n_mats, int cols, int n_adapters)
+{
+    return T >= 0 && T <= kMaxLoraTokens && rank >= 8 && rank <= kMaxRank && rank % 8 == 0 && n_mats >= 1 && n_mats <= kMats &&
+           cols >= 32 && cols % 32 == 0 && cols <= 1 << 20 && n_adapters >= 1 && n_adapters <= 1 << 20;
+}
+
+template <class T>
+int launch_down(const LoraArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)(a.T16 / 16) * a.slots * a.groups * a.splits), block(kThreads);
+    if (a.tiles <= 1)
+        hipLaunchKernelGGL((lora_down_kernel<T, 1>), grid, block, 0, st, a);
+    else if (a.tiles <= 2)
+        hipLaunchKernelGGL((lora_down_kernel<T, 2>), grid, block, 0, st, a);
+    else if (a.tiles <= 4)
+        hipLaunchKernelGGL((lora_down_kernel<T, 4>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((lora_down_kernel<T, 8>), grid, block, 0, st, a);
+    return hip_status("lora down launch");
+}
+
+template <class T, int KS>
+void launch_up_rank(LoraArgs &a, bool many, hipStream_t st)
+{
+    int blocks = 0;
+    for (int m = 0; m < a.l.n_mats; m++)
+        blocks += a.row_blocks[m] = (int)ceil_div(a.l.mats[m].rows, (many ? 64 : 16) * kWaves);
+    const dim3 grid(blocks, a.T16 / 16), block(kThreads);
+    if (many)
+        hipLaunchKernelGGL((lora_up_kernel<T, KS, 4, 1>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((lora_up_kernel<T, KS, 1, 16 / KS>), grid, block, 0, st, a);
+}
+
+template <class T>
+int launch_up(LoraArgs &a, hipStream_t st)
+{
+    const bool many = a.l.n_tokens > 256;
+    if (a.l.rank <= 32)
+        launch_up_rank<T, 1>(a, many, st);
+    else if (a.l.rank <= 64)
+        launch_up_rank<T, 2>(a, many, st);
+    else
+        launch_up_rank<T, 4>(a, many, st);
+    return hip_status("lora up launch");
+}
+
+} // namespace
+
+extern "C" {
+
+size_t rfx_lora_workspace_bytes(int n_tokens, int rank, int n_mats, int cols, int n_adapters)
+{
+    return shape_ok(n_tokens, rank, n_mats, cols, n_adapters) ? plan(n_tokens, rank, n_mats, cols, n_adapters).bytes : 0;
+}
+
+int rfx_lora_apply(const rfx_lora *L, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!L)
+        return fail(RFX_E_INVAL, "rfx_lora_apply: arguments are NULL");
+    if (L->type != RFX_F16 && L->type != RFX_BF16)
+        return fail(RFX_E_INVAL, "rfx_lora_apply: type %d (RFX_F16 or RFX_BF16)", L->type);
+    if (!shape_ok(L->n_tokens, L->rank, L->n_mats, L->cols, L->n_adapters))
+        return fail(RFX_E_INVAL, "rfx_lora_apply: n_tokens=%d rank=%d n_mats=%d cols=%d n_adapters=%d (at most 2^19 tokens; rank a "
+                    "multiple of 8, at most %d; 1 to %d matrices; cols a multiple of 32, at most 2^20; 1 to 2^20 adapters)",
+                    L->n_tokens, L->rank, L->n_mats, L->cols, L->n_adapters, kMaxRank, kMats);
+    if (L->x_stride < L->cols || L->x_stride % 4 || L->x_stride > (int64_t)1 << 40)
+        return fail(RFX_E_INVAL, "rfx_lora_apply: x_stride=%lld (a multiple of 4, at least cols)", (long long)L->x_stride);
+    int st = check_ptr(L->x, 16, "x");
+    if (st || (st = check_ptr(L->ids, 4, "ids")))
+        return st;
+    LoraArgs a{};
+    for (int m = 0; m < L->n_mats; m++) {
+        const rfx_lora_mat &M = L->mats[m];
+        if (M.rows < 1 || M.rows > 1 << 24)
+            return fail(RFX_E_INVAL, "rfx_lora_apply: matrix %d of %d rows (1 to 2^24)", m, M.rows);
+        if ((st = check_ptr(M.a, 16, "a")) || (st = check_ptr(M.b, 16, "b")) || (st = check_ptr(M.y, 4, "y")) ||
+            (M.resid && (st = check_ptr(M.resid, 4, "resid"))) || (M.scale && (st = check_ptr(M.scale, 4, "scale"))))
+            return st;
+        if (M.rows % 4 == 0 && !((reinterpret_cast<uintptr_t>(M.y) | reinterpret_cast<uintptr_t>(M.resid)) & 15))
+            a.vec |= 1 << m;
+    }
+    if (L->n_tokens == 0)
+        return RFX_OK;
+    const Plan p = plan(L->n_tokens, L->rank, L->n_mats, L->cols, L->n_adapters);
+    if (!ws || ws_bytes < p.bytes)
+        return fail(RFX_E_WORKSPACE, "rfx_lora_apply: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.bytes);
+    if ((st = check_ptr(ws, 256, "ws")))
+        return st;
+    a.l = *L;
+    a.R16 = p.R16;
+    a.tiles = p.tiles;
+    a.groups = p.groups;
+    a.splits = p.splits;
+    a.slots = p.slots;
+    a.T16 = p.T16;
+    a.v = static_cast<float *>(ws);
+    const hipStream_t hs = (hipStream_t)stream;
+    st = L->type == RFX_BF16 ? launch_down<BF16>(a, hs) : launch_down<F16>(a, hs);
+    if (st)
+        return st;
+    return L->type == RFX_BF16 ? launch_up<BF16>(a, hs) : launch_up<F16>(a, hs);
+}
+
+} // extern "C"

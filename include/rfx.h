@@ -567,6 +567,47 @@ typedef struct rfx_norm {
 } rfx_norm;
 int rfx_add_rms_norm(const rfx_norm *args, void *stream);
 
+/* Low-rank adapters of many requests beside a shared projection: for each
+ * matrix m and token t with a = ids[t],
+ *   y_m[t] = resid_m[t] + c_m[a] B_m[a] (A_m[a] x[t]),
+ * A [n_adapters][rank][cols] and B [n_adapters][rows][rank] in 16 bits, x,
+ * resid and y fp32. The shared projection's result is resid, and may be y
+ * itself (what an activation would be applied to, so it is run before any).
+ * A token whose id is outside 0..n_adapters - 1 has no adapter: y = resid. Up
+ * to RFX_LORA_MAX_MATS matrices over the same x (query, key, value) share the
+ * launches. Adapters of smaller rank are padded with zeros. Sums are fp32; x
+ * and A x enter the matrix core as three bf16 terms (together the fp32 value)
+ * or two fp16 terms (2^-22 of it; with fp16 adapters |x| < 2^19.9). One token's
+ * infinities and NaN stay its own. Results are deterministic, and a token's
+ * do not depend on the other tokens' values.
+ * ws: workspace of rfx_lora_workspace_bytes, 256-B aligned; it needs no
+ * initialisation and holds anything afterwards. Calls that can run
+ * concurrently must not share it. Two launches.
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
+#define RFX_LORA_MAX_MATS 4
+typedef struct rfx_lora_mat {
+    const void *a, *b;  /* 16-B aligned */
+    const float *scale; /* fp32 [n_adapters] (alpha / rank), or NULL: 1 */
+    const float *resid; /* fp32 [n_tokens][rows], or NULL: 0 */
+    float *y;           /* fp32 [n_tokens][rows]; overlaps nothing but resid */
+    int32_t rows;       /* 1..2^24 */
+    int32_t reserved;
+} rfx_lora_mat;
+typedef struct rfx_lora {
+    int32_t type;       /* of A and B: RFX_F16 or RFX_BF16 */
+    int32_t n_adapters; /* 1..2^20 */
+    int32_t rank;       /* multiple of 8, 8..128 */
+    int32_t cols;       /* multiple of 32, at most 2^20 */
+    int32_t n_tokens;   /* 0..2^19 */
+    int32_t n_mats;     /* 1..RFX_LORA_MAX_MATS */
+    const float *x;     /* fp32 [n_tokens][cols], 16-B aligned */
+    int64_t x_stride;   /* elements between rows: a multiple of 4, at least cols */
+    const int32_t *ids; /* [n_tokens], on the device */
+    rfx_lora_mat mats[RFX_LORA_MAX_MATS];
+} rfx_lora;
+size_t rfx_lora_workspace_bytes(int n_tokens, int rank, int n_mats, int cols, int n_adapters);
+int rfx_lora_apply(const rfx_lora *args, void *ws, size_t ws_bytes, void *stream);
+
 /* What a head's logits z [q][n_vocab] say of each row: lse = log sum e^z,
  * entropy = -sum p log p (natural logarithms, p = e^(z - lse)), the given
  * token's logprob = z[token] - lse and rank (how many logits are larger), and
