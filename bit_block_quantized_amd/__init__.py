@@ -90,6 +90,11 @@ class QkRopeC(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class KVPrefixC(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("seq_off", ctypes.c_void_p), ("len", ctypes.c_void_p)]
+
+
 class NormC(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("delta", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
                 ("delta_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("sum", ctypes.c_void_p),
@@ -162,6 +167,8 @@ _SIGS = {
     "rfx_qk_norm_rope": ([_P, _P, _P, _P, _P], _I),
     "rfx_attn_workspace_bytes": ([_P, _P, _I], _SZ),
     "rfx_attn": ([_P, _P, _P, _I, _F, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "rfx_attn_shared_workspace_bytes": ([_P, _P, _P, _I], _SZ),
+    "rfx_attn_shared": ([_P, _P, _P, _P, _I, _F, _P, _I, _P, _SZ, _P], _I),
     "rfx_add_rms_norm": ([_P, _P], _I),
     "rfx_lora_workspace_bytes": ([_I, _I, _I, _I, _I], _SZ),
     "rfx_lora_apply": ([_P, _P, _SZ, _P], _I),
@@ -685,6 +692,43 @@ def attn(q, cache: DeviceKVCache, batch: KVBatch, out, scale, window=0, sinks=0,
     _int32(window=window, sinks=sinks)
     wp, wn = _workspace(ws, dev)
     _call_on(dev, stream, lib().rfx_attn, qp, cache.c_ref, batch.c_ref, Hq, scale, window, sinks, op, _elem(out.dtype),
+             wp, wn)
+
+
+class KVPrefix:
+    """Groups of a batch's sequences that share a prefix (rfx_kv_prefix): int32
+    device tensors seq_off [n_groups + 1] and length [n_groups]; max_tokens: the
+    most new tokens of a group's sequences in all, max_len: the longest prefix."""
+
+    def __init__(self, seq_off, length, max_tokens, max_len):
+        _int32(max_tokens=max_tokens, max_len=max_len)
+        n, i32 = length.numel(), _torch().i32
+        self.seq_off, self.length, self.max_tokens, self.max_len = seq_off, length, max_tokens, max_len
+        self.n_groups, self.index = n, length.get_device()
+        self.c = KVPrefixC(n, max_tokens, max_len, 0, _want(seq_off, "seq_off", i32, (n + 1,), self.index),
+                           _want(length, "length", i32, (n,), self.index))
+        self.c_ref = ctypes.byref(self.c)
+
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def attn_shared_workspace_bytes(cache: DeviceKVCache, batch: KVBatch, prefix: KVPrefix, n_heads: int) -> int:
+    return int(lib().rfx_attn_shared_workspace_bytes(cache.ref(), batch.ref(), prefix.ref(), n_heads))
+
+
+def attn_shared(q, cache: DeviceKVCache, batch: KVBatch, prefix: KVPrefix, out, scale, ws=None, stream=None):
+    """attn for a batch whose sequences share prefixes, without a window: a
+    prefix is read once for its group (rfx_attn_shared)."""
+    dev = cache.index
+    Hq = q.shape[1]
+    shape = (batch.n_tokens, Hq, cache.head_dim)
+    qp = _want(q, "q", cache.dtype, shape, dev)
+    op = _want(out, "out", out.dtype, shape, dev)
+    if batch.index != dev or prefix.index != dev:
+        raise ValueError(f"batch and prefix on GPU {batch.index} and {prefix.index}, the cache is on GPU {dev}")
+    wp, wn = _workspace(ws, dev)
+    _call_on(dev, stream, lib().rfx_attn_shared, qp, cache.c_ref, batch.c_ref, prefix.c_ref, Hq, scale, op, _elem(out.dtype),
              wp, wn)
 
 

@@ -18,7 +18,7 @@ OUT = os.path.join(HERE, "librfx.so")
 
 SOURCES = ["rfx_host.cpp", "rfx_gemv.hip", "rfx_moe.hip", "rfx_moe_layer.hip", "rfx_prefill.hip", "rfx_probe.hip",
            "rfx_gemm.hip", "rfx_gemm_mx.hip", "rfx_rope.hip", "rfx_attn.hip", "rfx_attn_decode.hip", "rfx_attn_prefill.hip",
-           "rfx_norm.hip", "rfx_logprob.hip", "rfx_lora.hip"]
+           "rfx_attn_shared.hip", "rfx_norm.hip", "rfx_logprob.hip", "rfx_lora.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

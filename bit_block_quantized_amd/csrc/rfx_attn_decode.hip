@@ -20,6 +20,13 @@
 // Each wave keeps a running maximum and sum per row (fp32); waves are joined
 // through LDS, and where few rows have long sequences the keys are split
 // over S workgroups whose partials a second launch joins in split order.
+//
+// The same kernel serves rfx_attn_shared, with SharedArgs: some workgroups
+// take the rows of a whole group of sequences against the prefix that they
+// share, the others a sequence's rows against its own keys behind the prefix;
+// both leave partials for the join.
+#include <type_traits>
+
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -63,9 +70,14 @@ __device__ __forceinline__ float max_groups(float x)
 // fill DP.
 enum Pages { kOne, kTwo, kAny };
 
-template <class T, int DP, int NR, Pages PG>
-__global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
+// The launch that a workgroup belongs to.
+__device__ __forceinline__ const AttnArgs &launch_of(const AttnArgs &a, bool) { return a; }
+__device__ __forceinline__ const AttnArgs &launch_of(const SharedArgs &a, bool group) { return group ? a.group : a.own; }
+
+template <class T, int DP, int NR, Pages PG, class Args>
+__global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(Args args)
 {
+    constexpr bool SHARED = std::is_same_v<Args, SharedArgs>;
     constexpr int NC = DP / 32;         // K steps of the score product
     constexpr int NV = DP / 16;         // 16-byte loads per lane and V tile; also 16-row tiles of O^T
     constexpr int CH = DP / 8;          // 16-byte chunks per key
@@ -77,21 +89,54 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
 
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    bool group = false; // the rows of a group of sequences
+    int block = blockIdx.x;
+    if constexpr (SHARED) {
+        group = block < args.group_blocks;
+        block -= group ? 0 : args.group_blocks;
+    }
+    const AttnArgs &a = launch_of(args, group);
     const KvArgs &kv = a.kv;
     // splits vary slowest: those that a short sequence leaves empty are the
     // last of the launch, and the others spread over all compute units (18 to
     // 14 us at 8192 keys with the splits of one unit side by side)
-    const int split = a.div_units(blockIdx.x), unit = a.div_units.rem(blockIdx.x, split);
-    const int seq = kv.div_hk(unit), hk = kv.div_hk.rem(unit, seq);
+    const int split = a.div_units(block), unit = a.div_units.rem(block, split);
+    int seq = kv.div_hk(unit);
+    const int hk = kv.div_hk.rem(unit, seq);
     const int D = PG == kAny ? kv.D : DP;
-    const int window = a.window ? a.window : 1 << 30; // positions are below 2^30
+    const int window = !SHARED && a.window ? a.window : 1 << 30; // positions are below 2^30
 
-    const Seq sq = load_seq(kv, seq);
-    const int nrows = min(sq.nq * kv.G, NR * 16);
+    Seq sq;
+    int row0 = 0;        // of the block
+    bool alone = true;   // no prefix beside these keys
+    KeyTiles kt;
+    if constexpr (SHARED) {
+        Group gr;
+        if (group) { // all of its keys are before all of its rows
+            const int g = a.div_rb(seq);
+            row0 = a.div_rb.rem(seq, g) * NR * 16;
+            gr = load_group(kv, args.pre, g);
+            seq = gr.s0;
+            sq = {gr.t0, gr.nt, gr.len - 1, gr.len}; // as if at the last key
+            kt = range_tiles(BN, 0, gr.len);
+        } else {
+            sq = load_seq(kv, seq);
+            if (sq.nq > 0)
+                prefix_of(kv, args.pre, seq, sq, gr);
+            else
+                gr.len = 0;
+            kt = range_tiles(BN, gr.len, min(sq.kv, sq.p0 + sq.nq));
+        }
+        alone = !group && gr.len == 0;
+    } else {
+        sq = load_seq(kv, seq);
+    }
+    const int nrows = min(sq.nq * kv.G - row0, NR * 16);
     if (nrows <= 0)
         return;
-    const int p_lo = sq.p0, p_hi = sq.p0 + kv.div_g(nrows - 1);
-    const KeyTiles kt = key_tiles(BN, p_lo, p_hi, sq.kv, a.window, a.sinks);
+    const int p_lo = sq.p0, p_hi = group ? sq.p0 : sq.p0 + kv.div_g(nrows - 1);
+    if constexpr (!SHARED)
+        kt = key_tiles(BN, p_lo, p_hi, sq.kv, a.window, a.sinks);
     int per, active;
     split_tiles(a, kt.n, per, active);
     if (split >= active)
@@ -104,8 +149,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     int pos[NR];
 #pragma unroll
     for (int n = 0; n < NR; n++) {
-        const int row = 16 * n + r16, rr = min(row, nrows - 1), tok = kv.div_g(rr), head = hk * kv.G + kv.div_g.rem(rr, tok);
-        pos[n] = sq.p0 + tok;
+        const int row = 16 * n + r16, rr = row0 + min(row, nrows - 1), tok = kv.div_g(rr), head = hk * kv.G + kv.div_g.rem(rr, tok);
+        pos[n] = group ? sq.p0 : sq.p0 + tok;
         const uint16_t *qp = a.q + ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
 #pragma unroll
         for (int c = 0; c < NC; c++) {
@@ -267,17 +312,19 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
             else
                 return usable(__shfl(cur.id[0], kk, 64));
         };
-        const bool edge = (key0 + BN - 1 > p_lo) | (key0 + BN > kt.hi) | ((key0 <= p_hi - window) & (key0 + BN > a.sinks)) | page_bad;
+        const int sinks = SHARED ? 0 : a.sinks;
+        const bool edge = (key0 + BN - 1 > p_lo) | (key0 + BN > kt.hi) | ((key0 <= p_hi - window) & (key0 + BN > sinks)) |
+                          (SHARED & (key0 < kt.lo)) | page_bad;
         if (edge) { // no branches inside: the compiler's waits for the loads in flight would cover all of them
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int v = 0; v < 4; v++) {
                     const int kk = 8 * g4 + 4 * j + v, key = key0 + kk;
-                    const bool good = page_good(kk) & (key < kt.hi);
+                    const bool good = page_good(kk) & (key < kt.hi) & (!SHARED | (key >= kt.lo));
 #pragma unroll
                     for (int n = 0; n < NR; n++) {
-                        const bool seen = good & (key <= pos[n]) & ((key > pos[n] - window) | (key < a.sinks));
+                        const bool seen = good & (key <= pos[n]) & ((key > pos[n] - window) | (key < sinks));
                         s[n][j][v] = seen ? s[n][j][v] : -INFINITY;
                     }
                 }
@@ -365,7 +412,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
         }
     }
     const size_t slot = ((size_t)unit * a.S + split) * (NR * 16);
-    const bool joined = active == 1;
+    const bool joined = active == 1 && alone;
     float *o_lds = reinterpret_cast<float *>(smem);
     constexpr int OP = DP + 4;
 #pragma unroll
@@ -414,24 +461,29 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(AttnArgs a)
     }
 }
 
-template <class T, int DP, int NR>
-int launch(const AttnArgs &a, hipStream_t st)
+unsigned blocks(const AttnArgs &a) { return (unsigned)a.kv.n_seq * a.kv.Hk * a.S; }
+unsigned blocks(const SharedArgs &a) { return a.group_blocks + blocks(a.own); }
+const KvArgs &cache_of(const AttnArgs &a) { return a.kv; }
+const KvArgs &cache_of(const SharedArgs &a) { return a.own.kv; }
+
+template <class T, int DP, int NR, class Args>
+int launch(const Args &a, hipStream_t st)
 {
-    const unsigned grid = (unsigned)a.kv.n_seq * a.kv.Hk * a.S;
-    const dim3 block(64 * kWaves);
-    if (a.kv.D != DP || a.kv.page_shift < 4)
-        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kAny>), dim3(grid), block, 0, st, a);
-    else if (a.kv.page_shift == 4)
-        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kTwo>), dim3(grid), block, 0, st, a);
+    const KvArgs &kv = cache_of(a);
+    const dim3 grid(blocks(a)), block(64 * kWaves);
+    if (kv.D != DP || kv.page_shift < 4)
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kAny, Args>), grid, block, 0, st, a);
+    else if (kv.page_shift == 4)
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kTwo, Args>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kOne>), dim3(grid), block, 0, st, a);
+        hipLaunchKernelGGL((attn_decode_kernel<T, DP, NR, kOne, Args>), grid, block, 0, st, a);
     return hip_status("attn decode launch");
 }
 
-template <class T>
-int launch_dim(const AttnArgs &a, int row_tiles, hipStream_t st)
+template <class T, class Args>
+int launch_dim(const Args &a, int row_tiles, hipStream_t st)
 {
-    const int D = a.kv.D;
+    const int D = cache_of(a).D;
     if (row_tiles == 1)
         return D <= 64 ? launch<T, 64, 1>(a, st) : D <= 128 ? launch<T, 128, 1>(a, st) : launch<T, 256, 1>(a, st);
     return D <= 64 ? launch<T, 64, 2>(a, st) : launch<T, 128, 2>(a, st);
@@ -442,6 +494,11 @@ int launch_dim(const AttnArgs &a, int row_tiles, hipStream_t st)
 namespace rfx {
 
 int attn_decode_launch(const AttnArgs &a, int type, int row_tiles, hipStream_t st)
+{
+    return type == RFX_BF16 ? launch_dim<BF16>(a, row_tiles, st) : launch_dim<F16>(a, row_tiles, st);
+}
+
+int attn_decode_launch(const SharedArgs &a, int type, int row_tiles, hipStream_t st)
 {
     return type == RFX_BF16 ? launch_dim<BF16>(a, row_tiles, st) : launch_dim<F16>(a, row_tiles, st);
 }

@@ -15,6 +15,8 @@
 //   of V^T are read in that order (transposed LDS reads), so the weights stay
 //   in their lane.
 // Tiles outside a wave's rows' window or after their positions are skipped.
+// With SharedArgs the rows are those of a whole group of sequences and the
+// keys the prefix that they share, which all rows see (rfx_attn_shared).
 // Few row blocks over long sequences: the keys are split over S workgroups
 // and a second launch joins the partials in split order.
 //
@@ -22,6 +24,8 @@
 // that type (its own rounding is as large), and the row sums are of the
 // rounded ones; for an fp32 result they are carried as the sum of TERMS
 // values, and the sums are of the fp32 weights.
+#include <type_traits>
+
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -74,9 +78,14 @@ __device__ __forceinline__ void subtract_max(f32x16 (&s)[NK], float m)
 // beside the wave that waits.
 constexpr int waves_per_simd(int dp, int terms) { return dp <= 64 && terms < 3 ? 3 : dp <= 128 ? 2 : 1; }
 
-template <class T, int DP, int TERMS>
-__global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_prefill_kernel(AttnArgs a)
+__device__ __forceinline__ const AttnArgs &launch_of(const AttnArgs &a) { return a; }
+__device__ __forceinline__ const AttnArgs &launch_of(const SharedArgs &a) { return a.group; }
+
+template <class T, int DP, int TERMS, class Args>
+__global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_prefill_kernel(Args args)
 {
+    constexpr bool SHARED = std::is_same_v<Args, SharedArgs>;
+    const AttnArgs &a = launch_of(args);
     using L = Tile<DP>;
     constexpr int BN = L::BN, NC = DP / 16, ND = DP / 32, NK = BN / 32;
     __shared__ __align__(16) char smem[2 * L::buf];
@@ -91,17 +100,27 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
     // XCD's L2 holds one head's keys and values.
     const int split = a.div_units(blockIdx.x), b = a.div_units.rem(blockIdx.x, split);
     const int us = kv.div_hk(b), hk = kv.div_hk.rem(b, us);
-    const int seq = a.div_rb(us), rb = a.row_blocks - 1 - a.div_rb.rem(us, seq); // the longest first
+    int seq = a.div_rb(us);
+    const int rb = a.row_blocks - 1 - a.div_rb.rem(us, seq); // the longest first
     const int unit = (seq * a.row_blocks + rb) * kv.Hk + hk;
     const int D = kv.D;
-    const int window = a.window ? a.window : 1 << 30; // positions are below 2^30
+    const int window = !SHARED && a.window ? a.window : 1 << 30; // positions are below 2^30
+    const int sinks = SHARED ? 0 : a.sinks;
 
-    const Seq sq = load_seq(kv, seq);
+    Seq sq;
+    if constexpr (SHARED) {
+        const Group gr = load_group(kv, args.pre, seq);
+        seq = gr.s0;
+        sq = {gr.t0, gr.nt, gr.len - 1, gr.len}; // as if at the last key
+    } else {
+        sq = load_seq(kv, seq);
+    }
     const int nrows = sq.nq * kv.G, row0 = rb * kRows;
     if (row0 >= nrows)
         return;
     const int row_end = min(nrows, row0 + kRows);
-    const KeyTiles kt = key_tiles(BN, sq.p0 + kv.div_g(row0), sq.p0 + kv.div_g(row_end - 1), sq.kv, a.window, a.sinks);
+    const KeyTiles kt = SHARED ? range_tiles(BN, 0, sq.kv)
+                               : key_tiles(BN, sq.p0 + kv.div_g(row0), sq.p0 + kv.div_g(row_end - 1), sq.kv, a.window, a.sinks);
     int per, active;
     split_tiles(a, kt.n, per, active);
     if (split >= active)
@@ -113,8 +132,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
     const bool wave_on = wrow < nrows;
     const int row = min(wrow + r32, nrows - 1), tok = kv.div_g(row), head = hk * kv.G + kv.div_g.rem(row, tok);
     const bool row_ok = wrow + r32 < nrows;
-    const int pos = sq.p0 + tok;
-    const int w_lo = sq.p0 + kv.div_g(min(wrow, nrows - 1)), w_hi = sq.p0 + kv.div_g(min(wrow + 31, nrows - 1));
+    // every key of a shared prefix is before every row
+    const int pos = SHARED ? sq.p0 : sq.p0 + tok;
+    const int w_lo = SHARED ? pos : sq.p0 + kv.div_g(min(wrow, nrows - 1)), w_hi = SHARED ? pos : sq.p0 + kv.div_g(min(wrow + 31, nrows - 1));
     const size_t at = ((size_t)(sq.t0 + tok) * kv.Hq + head) * D;
     u4 qf[NC];
 #pragma unroll
@@ -216,7 +236,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
             s_bad[(t + 2) % 3][tid] = 0; // last read for tile t - 1
         const int key0 = tile_key<BN>(kt, t);
         const char *kb = smem + (t & 1) * L::buf, *vb = kb + BN * L::KP;
-        const bool seen = wave_on && key0 <= w_hi && (key0 + BN - 1 > w_lo - window || key0 < a.sinks);
+        const bool seen = wave_on && key0 <= w_hi && (key0 + BN - 1 > w_lo - window || key0 < sinks);
         if (seen) {
             f32x16 s[NK];
 #pragma unroll
@@ -232,14 +252,14 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
                     s[k] = T::mma32(kf, qf[c], s[k]);
                 }
             const unsigned bad0 = s_bad[t % 3][0], bad1 = s_bad[t % 3][1];
-            const bool edge = key0 + BN - 1 > w_lo || (key0 <= w_hi - window && key0 + BN > a.sinks) || (bad0 | bad1);
+            const bool edge = key0 + BN - 1 > w_lo || (key0 <= w_hi - window && key0 + BN > sinks) || (bad0 | bad1);
             if (edge) {
 #pragma unroll
                 for (int k = 0; k < NK; k++)
 #pragma unroll
                     for (int v = 0; v < 16; v++) {
                         const int kk = 8 * (v >> 2) + 4 * hl + (v & 3), key = key0 + 32 * k + kk;
-                        const bool ok = (key <= pos) & ((key > pos - window) | (key < a.sinks)) & !(((k ? bad1 : bad0) >> kk) & 1);
+                        const bool ok = (key <= pos) & ((key > pos - window) | (key < sinks)) & !(((k ? bad1 : bad0) >> kk) & 1);
                         s[k][v] = ok ? s[k][v] : -INFINITY;
                     }
             }
@@ -303,7 +323,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(DP, TERMS)) void attn_pref
 
     l += __shfl_xor(l, 32, 64);
     // lane (row r32), register 4 j + v of acc[i]: element 32 i + 8 j + 4 hl + v
-    if (active == 1) {
+    if (!SHARED && active == 1) {
         if (!row_ok)
             return;
         const float inv = l > 0.f ? 1.0f / l : 0.f; // a row that sees nothing is zero
@@ -737,10 +757,28 @@ int launch(const AttnArgs &a, hipStream_t st)
             return hip_status("attn prefill launch");
         }
     if (a.out_f32)
-        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, T::TERMS>), dim3(grid), dim3(kThreads), 0, st, a);
+        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, T::TERMS, AttnArgs>), dim3(grid), dim3(kThreads), 0, st, a);
     else
-        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, 1>), dim3(grid), dim3(kThreads), 0, st, a);
+        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, 1, AttnArgs>), dim3(grid), dim3(kThreads), 0, st, a);
     return hip_status("attn prefill launch");
+}
+
+template <class T, int DP>
+int launch(const SharedArgs &a, hipStream_t st)
+{
+    const dim3 grid(a.group_blocks);
+    if (a.group.out_f32)
+        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, T::TERMS, SharedArgs>), grid, dim3(kThreads), 0, st, a);
+    else
+        hipLaunchKernelGGL((attn_prefill_kernel<T, DP, 1, SharedArgs>), grid, dim3(kThreads), 0, st, a);
+    return hip_status("attn prefix launch");
+}
+
+template <class T>
+int launch_dim(const SharedArgs &a, hipStream_t st)
+{
+    const int D = a.group.kv.D;
+    return D <= 64 ? launch<T, 64>(a, st) : D <= 128 ? launch<T, 128>(a, st) : launch<T, 256>(a, st);
 }
 
 template <class T>
@@ -754,6 +792,11 @@ int launch_dim(const AttnArgs &a, hipStream_t st)
 namespace rfx {
 
 int attn_prefill_launch(const AttnArgs &a, int type, hipStream_t st)
+{
+    return type == RFX_BF16 ? launch_dim<BF16>(a, st) : launch_dim<F16>(a, st);
+}
+
+int attn_prefill_launch(const SharedArgs &a, int type, hipStream_t st)
 {
     return type == RFX_BF16 ? launch_dim<BF16>(a, st) : launch_dim<F16>(a, st);
 }

@@ -91,11 +91,29 @@ struct AttnArgs {
     float *stat;       // [unit][split][rows][2] their maxima and sums
 };
 
+// Sequences that share a prefix (rfx_attn_shared).
+struct PrefixArgs {
+    const int32_t *seq_off, *len;
+    int n_groups, max_tokens;
+};
+
+// Its kernels' arguments: `group` is a launch whose sequences are the groups,
+// each with all its sequences' new tokens as rows and the prefix as keys; `own`
+// one over the sequences, whose keys begin behind the prefix. Both leave
+// partials; what has no prefix and no split is done by `own`.
+struct SharedArgs {
+    PrefixArgs pre;
+    AttnArgs group, own;
+    int group_blocks; // workgroups of `group` ahead of `own`'s
+};
+
 // The two-group prefill kernel: rows of a block, and the page ids that its
 // LDS holds (for 64 keys one of each page they touch).
 constexpr int kPairRows = 256, kPairIds = 4096;
 
 int attn_decode_launch(const AttnArgs &a, int type, int row_tiles, hipStream_t st);
+int attn_decode_launch(const SharedArgs &a, int type, int row_tiles, hipStream_t st);
+int attn_prefill_launch(const SharedArgs &a, int type, hipStream_t st); // its `group` alone
 int attn_prefill_launch(const AttnArgs &a, int type, hipStream_t st);
 int attn_join_launch(const AttnArgs &a, int type, int64_t units, hipStream_t st);
 
@@ -233,6 +251,62 @@ __device__ __forceinline__ Seq load_seq(const KvArgs &a, int s)
     return q;
 }
 
+// The run that t is in, of n one after the other (run s is off[s] .. off[s +
+// 1] - 1): the last s with off[s] <= t, or -1 before the first and behind the
+// last. 64 lanes probe at a time.
+__device__ __forceinline__ int find_run(const int32_t *off, int n, int t)
+{
+    const int lane = threadIdx.x & 63;
+    const int first = off[0], last = off[n];
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 64) / 65;
+        const int i = lo + (lane + 1) * step;
+        const bool le = i < hi && off[min(i, n)] <= t;
+        const int c = __popcll(__ballot(le));
+        hi = min(hi, lo + (c + 1) * step);
+        lo += c * step;
+    }
+    return t >= first && t < last ? lo : -1;
+}
+
+// What a group of sequences has in common, as the batch's kernels see it: its
+// new tokens are rows t0 .. t0 + nt - 1, its prefix the first len tokens of
+// sequence s0's pages. len = 0: no prefix (more new tokens than max_tokens,
+// rows or sequences that leave the arrays, a prefix that leaves the table).
+struct Group {
+    int s0, t0, nt, len;
+};
+
+__device__ __forceinline__ Group load_group(const KvArgs &a, const PrefixArgs &pre, int g)
+{
+    const int s0 = __builtin_amdgcn_readfirstlane(pre.seq_off[g]), s1 = __builtin_amdgcn_readfirstlane(pre.seq_off[g + 1]);
+    const int len = __builtin_amdgcn_readfirstlane(pre.len[g]);
+    Group r = {0, 0, 0, 0};
+    if (s0 < 0 || s1 <= s0 || s1 > a.n_seq || len <= 0 || len > a.stride << a.page_shift)
+        return r;
+    const int t0 = __builtin_amdgcn_readfirstlane(a.q_off[s0]), t1 = __builtin_amdgcn_readfirstlane(a.q_off[s1]);
+    if (t0 < 0 || t1 <= t0 || t1 > a.n_tokens || t1 - t0 > pre.max_tokens)
+        return r;
+    return {s0, t0, t1 - t0, len};
+}
+
+// The group whose prefix sequence s takes part in, -1 and len 0 where there
+// is none, where its new tokens begin inside the prefix, or where its rows are
+// not among the group's.
+__device__ __forceinline__ int prefix_of(const KvArgs &a, const PrefixArgs &pre, int s, const Seq &sq, Group &gr)
+{
+    const int g = __builtin_amdgcn_readfirstlane(find_run(pre.seq_off, pre.n_groups, s));
+    gr = {0, 0, 0, 0};
+    if (g < 0)
+        return -1;
+    gr = load_group(a, pre, g);
+    if (gr.len && sq.p0 >= gr.len && sq.t0 >= gr.t0 && sq.t0 + sq.nq <= gr.t0 + gr.nt)
+        return g;
+    gr.len = 0;
+    return -1;
+}
+
 // The key tiles of bn keys that rows with first position p_lo and last
 // position p_hi can see: the sinks' tiles, then those of the window.
 struct KeyTiles {
@@ -269,6 +343,18 @@ __device__ __forceinline__ void split_tiles(const AttnArgs &a, int n, int &per, 
     }
     per = max(a.div_s(n + a.S - 1), max(a.min_tiles, min((n + (1 << a.cap_shift) - 1) >> a.cap_shift, 16)));
     active = (n + per - 1) / per;
+}
+
+// The tiles of keys lo .. hi - 1, with no window.
+__device__ __forceinline__ KeyTiles range_tiles(int bn, int lo, int hi)
+{
+    KeyTiles t;
+    t.hi = max(0, hi);
+    t.lo = min(lo, t.hi);
+    t.sk = t.nst = 0;
+    t.wt = t.lo / bn;
+    t.n = max(0, (t.hi + bn - 1) / bn - t.wt);
+    return t;
 }
 
 // First key of the i-th tile.

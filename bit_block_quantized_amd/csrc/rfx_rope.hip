@@ -33,24 +33,6 @@ struct RopeArgs {
     uint16_t *qo;
 };
 
-// Sequence of row t: the last s with q_off[s] <= t, or -1 for rows before
-// the first and behind the last sequence. 64 lanes probe at a time.
-__device__ __forceinline__ int find_seq(const int32_t *q_off, int n, int t)
-{
-    const int lane = threadIdx.x & 63;
-    const int first = q_off[0], last = q_off[n];
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 64) / 65;
-        const int i = lo + (lane + 1) * step;
-        const bool le = i < hi && q_off[min(i, n)] <= t;
-        const int c = __popcll(__ballot(le));
-        hi = min(hi, lo + (c + 1) * step);
-        lo += c * step;
-    }
-    return t >= first && t < last ? lo : -1;
-}
-
 // Sum over the LPH (8, 16 or 32) lanes of a head: neighbours, pairs and
 // halves by the vector pipe's own lane exchanges.
 template <int LPH>
@@ -106,7 +88,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a)
     };
     f32x4 x0 = load(e0), x1 = load(e1);
 
-    const int s = find_seq(a.kv.q_off, a.kv.n_seq, t);
+    const int s = find_run(a.kv.q_off, a.kv.n_seq, t);
     if (s < 0)
         return; // rows of no sequence stay as they are
     const Seq sq = load_seq(a.kv, s);

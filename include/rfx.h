@@ -537,6 +537,41 @@ size_t rfx_attn_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *b
 int rfx_attn(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch, int n_heads, float scale,
              int window, int sinks, void *out, int out_type, void *ws, size_t ws_bytes, void *stream);
 
+/* Groups of sequences of a batch whose first tokens are the same: group g has
+ * the sequences seq_off[g] .. seq_off[g+1] - 1 and the prefix of the first
+ * len[g] cached tokens. Every sequence's table holds its whole sequence, the
+ * prefix in the same pages or in copies of them; a group says that one's may be
+ * read for all. A group may have no sequence, and a sequence no group. Where
+ * len is not positive, the prefix leaves the table, a group's sequences or rows
+ * leave the batch's or it has more than max_tokens new tokens, its sequences
+ * are attended one by one, and so is a sequence whose new tokens begin inside
+ * the prefix. max_len sets how a prefix is split and no more. The arrays are on
+ * the device and may change between replays. */
+typedef struct rfx_kv_prefix {
+    int32_t n_groups;         /* 1..2^23 */
+    int32_t max_tokens;       /* most new tokens of a group's sequences in all, 1..2^23 */
+    int32_t max_len;          /* longest prefix, >= 1 */
+    int32_t reserved;
+    const int32_t *seq_off;   /* [n_groups + 1], ascending */
+    const int32_t *len;       /* [n_groups] */
+} rfx_kv_prefix;
+
+/* rfx_attn (without a window) for a batch in which sequences share prefixes: a
+ * prefix's keys and values are read once for all new tokens of its group, what
+ * a sequence has behind it once for the sequence. Arguments as rfx_attn's. For
+ * a 16-bit result the softmax weights of a prefix enter the matrix core as one
+ * term where its group has more than 64 rows (new tokens x query heads per kv
+ * head). Sequences of more than 32 rows, 16 with heads over 128, go to
+ * rfx_attn, which reads a key once per 128 rows of one sequence. A prefix is
+ * read from the pages of its group's first sequence.
+ * ws: workspace of rfx_attn_shared_workspace_bytes, as rfx_attn's. Two
+ * launches, and a third with more than 64 rows to a prefix.
+ * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
+size_t rfx_attn_shared_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *batch, const rfx_kv_prefix *prefix,
+                                       int n_heads);
+int rfx_attn_shared(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch, const rfx_kv_prefix *prefix,
+                    int n_heads, float scale, void *out, int out_type, void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------ */
 /* Residual norm, adapters, log probabilities.                         */
 /* ------------------------------------------------------------------ */
