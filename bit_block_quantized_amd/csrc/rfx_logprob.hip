@@ -9,9 +9,10 @@
 // and leaves the chunk's maximum, sums, count and k best keys. A second
 // launch, one workgroup per row, joins the chunks in 64 bits.
 //
-// The elements equal to the maximum are counted and the others' sum is kept
-// apart from that count, so that a row with one likely token keeps the small
-// rest (1 + 1e-9 is 1 in fp32), which its log probability and entropy are.
+// Where little is beside the maximum, the elements equal to it are counted
+// and the others' sum is kept apart from that count, so that a row with one
+// likely token keeps the small rest (1 + 1e-9 is 1 in fp32), which its log
+// probability and entropy are.
 //
 // The k best: an element is a key of 64 bits, the value's order above the
 // complement of its index, so that no two are equal and ties are decided. In
@@ -23,9 +24,11 @@
 // ones), the k are taken out one after the other.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include "rfx.h"
 #include "rfx_internal.h"
@@ -40,12 +43,14 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMaxTop = 64;
 constexpr int kMaxVocab = 1 << 19;
-constexpr int kLong = 32, kShort = 8;   // elements per thread of a chunk
+constexpr int kShort = 8;               // elements per thread of a short chunk
+constexpr int kLoads = 4;               // 16-byte loads per thread of a long one
 constexpr int kJoinKeys = 32;           // keys per thread of the join
 constexpr float kLog2e = 1.4426950408889634f;
 
-// What a chunk leaves: its maximum, how many elements equal it, and over the
-// others sum e^(z - m); sum e^(z - m) (z - m) over all; elements above the token's.
+// What a wave's part of a chunk leaves: its maximum m; sum e^(z - m), as the number of elements
+// that equal the maximum and the rest's sum where that is little, else all in
+// `rest`; sum e^(z - m) (z - m); elements above the token's.
 struct Stat {
     float m, n, rest, dot, above, pad[3];
 };
@@ -55,7 +60,7 @@ struct LogpArgs {
     int64_t stride;
     int q, V, k, S, chunk;
     const int32_t *tokens;
-    Stat *stat;      // [q][S]
+    Stat *stat;      // [q][S][wave]
     uint64_t *keys;  // [q][S][k]
     rfx_logprob out;
 };
@@ -75,9 +80,56 @@ __device__ __forceinline__ float value_of(uint64_t key)
 __device__ __forceinline__ uint64_t make_key(float v, int index) { return (uint64_t)ordered(v) << 32 | (uint32_t)~index; }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)~(uint32_t)key; }
 
-__device__ __forceinline__ uint64_t shfl64(uint64_t v, int o)
+// Wave reductions by the vector pipe's lane exchanges: pairs, fours, eights,
+// sixteens inside a row of 16, then rows and halves.
+template <class V, class Op>
+__device__ __forceinline__ V wave_reduce(V x, Op op)
 {
-    return (uint64_t)__shfl_xor((uint32_t)(v >> 32), o, 64) << 32 | (uint32_t)__shfl_xor((uint32_t)v, o, 64);
+    const auto dpp = [&](auto ctrl) {
+        constexpr int N = sizeof(V) / 4;
+        uint32_t u[N];
+        __builtin_memcpy(u, &x, sizeof(V));
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            u[i] = __builtin_amdgcn_update_dpp(0, (int)u[i], decltype(ctrl)::value, 0xf, 0xf, true);
+        V y;
+        __builtin_memcpy(&y, u, sizeof(V));
+        x = op(x, y);
+    };
+    dpp(std::integral_constant<int, 0xB1>{});  // lanes 1 0 3 2
+    dpp(std::integral_constant<int, 0x4E>{});  // lanes 2 3 0 1
+    dpp(std::integral_constant<int, 0x141>{}); // 7 - i of 8
+    dpp(std::integral_constant<int, 0x140>{}); // 15 - i of 16
+    constexpr int N = sizeof(V) / 4;
+    uint32_t u[N], v[N];
+    V y;
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+        __builtin_memcpy(u, &x, sizeof(V));
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const auto r = half ? __builtin_amdgcn_permlane32_swap(u[i], u[i], false, false)
+                                : __builtin_amdgcn_permlane16_swap(u[i], u[i], false, false);
+            u[i] = r[0];
+            v[i] = r[1];
+        }
+        __builtin_memcpy(&x, u, sizeof(V));
+        __builtin_memcpy(&y, v, sizeof(V));
+        x = op(x, y);
+    }
+    return x;
+}
+// A value that all lanes have, for branches that a wave takes as one.
+__device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
+
+template <class V>
+__device__ __forceinline__ V wave_sum(V x)
+{
+    return wave_reduce(x, [](V p, V q) { return p + q; });
+}
+__device__ __forceinline__ float wave_max(float x)
+{
+    return wave_reduce(x, [](float p, float q) { return fmaxf(p, q); });
 }
 
 struct Shared {
@@ -86,35 +138,31 @@ struct Shared {
     int count;
 };
 
-// The n-th largest (n >= 1) of a wave's 64 values, uniform: its bits one
-// after the other, from the highest, by counting who reaches them.
+// The upper 16 bits of the n-th largest (n >= 1) of a wave's 64 values, the
+// lower ones zero, uniform: its bits one after the other, from the highest, by
+// counting who reaches them.
 __device__ __forceinline__ uint32_t nth_largest(uint32_t v, int n)
 {
     uint32_t t = 0;
-#pragma unroll 4
-    for (int b = 31; b >= 0; b--) {
+#pragma unroll
+    for (int b = 31; b >= 16; b--) {
         const uint32_t u = t | 1u << b;
         if (__popcll(__ballot(v >= u)) >= n)
             t = u;
     }
     return t;
 }
-__device__ __forceinline__ uint64_t nth_largest(uint64_t v, int n)
-{
-    const uint32_t hi = (uint32_t)(v >> 32), h = nth_largest(hi, n);
-    const int above = __popcll(__ballot(hi > h));
-    const uint32_t lo = nth_largest(hi == h ? (uint32_t)v : 0u, n - above);
-    return (uint64_t)h << 32 | lo;
-}
 
 // The k largest keys of the workgroup's to out[0..k), in descending order,
-// 0 where there are fewer; key(j) is this thread's j-th of N, 0 for none;
-// best: the largest of them. All threads call it.
-template <int N, class Key>
-__device__ __forceinline__ void top_keys(Shared &sh, int k, uint64_t best, Key &&key, uint64_t *out)
+// 0 where there are fewer. This thread's N elements are value(j), -inf for
+// none, and key(j); best: the largest value. All threads call it.
+template <int N, class Value, class Key>
+__device__ __forceinline__ void top_keys(Shared &sh, int k, float best, Value &&value, Key &&key, uint64_t *out)
 {
     const int tid = threadIdx.x, wave = tid >> 6;
-    const uint64_t bound = nth_largest(best, (k + kWaves - 1) / kWaves);
+    // values that at least k elements reach: one for the largest, else in
+    // every wave ceil(k / 4)
+    const uint32_t bound = k == 1 ? ordered(wave_max(best)) : nth_largest(best > -INFINITY ? ordered(best) : 0u, (k + kWaves - 1) / kWaves);
     if ((tid & 63) == 0)
         sh.wave[wave] = bound;
     if (tid == 0)
@@ -123,23 +171,22 @@ __device__ __forceinline__ void top_keys(Shared &sh, int k, uint64_t best, Key &
     uint64_t t = sh.wave[0];
 #pragma unroll
     for (int w = 1; w < kWaves; w++)
-        t = sh.wave[w] < t ? sh.wave[w] : t;
-    t = t ? t : 1; // 0 is no key
-    if (best >= t)
+        t = (k == 1) == (sh.wave[w] > t) ? sh.wave[w] : t;
+    const float from = fmaxf(value_of(t << 32), -3.4028234663852886e38f); // not -inf, which is no element
+    if (best >= from)
 #pragma unroll
-        for (int j = 0; j < N; j++) {
-            const uint64_t v = key(j);
-            if (v >= t) {
+        for (int j = 0; j < N; j++)
+            if (value(j) >= from) {
                 const int at = atomicAdd(&sh.count, 1);
                 if (at < kThreads)
-                    sh.list[at] = v;
+                    sh.list[at] = key(j);
             }
-        }
     __syncthreads();
     const int n = sh.count;
     if (n <= kThreads) {
         const uint64_t mine = tid < n ? sh.list[tid] : 0;
         int rank = 0;
+#pragma unroll 4
         for (int i = 0; i < n; i++)
             rank += sh.list[i] > mine;
         if (tid < n && rank < k)
@@ -154,14 +201,10 @@ __device__ __forceinline__ void top_keys(Shared &sh, int k, uint64_t best, Key &
         uint64_t m = 0;
 #pragma unroll
         for (int j = 0; j < N; j++) {
-            const uint64_t v = key(j);
+            const uint64_t v = value(j) > -INFINITY ? key(j) : 0;
             m = v < last && v > m ? v : m;
         }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const uint64_t v = shfl64(m, o);
-            m = v > m ? v : m;
-        }
+        m = wave_reduce(m, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
         __syncthreads();
         if ((tid & 63) == 0)
             sh.wave[wave] = m;
@@ -176,21 +219,6 @@ __device__ __forceinline__ void top_keys(Shared &sh, int k, uint64_t best, Key &
     }
 }
 
-__device__ __forceinline__ float wave_sum(float x)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        x += __shfl_xor(x, o, 64);
-    return x;
-}
-__device__ __forceinline__ float wave_max(float x)
-{
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        x = fmaxf(x, __shfl_xor(x, o, 64));
-    return x;
-}
-
 template <int TYPE>
 __device__ __forceinline__ float logit(const void *row, int i)
 {
@@ -202,14 +230,13 @@ __device__ __forceinline__ float logit(const void *row, int i)
 }
 
 // One workgroup per (row, chunk of E elements per thread). A thread's 16-byte
-// loads are aligned, so that the row's elements start `lead` elements into
-// the first; a load that the row fills only in part goes element by element.
+// loads are aligned, so that the row's elements start `lead` elements into the
+// first; a load that the row fills only in part goes element by element.
 template <int TYPE, int E>
 __global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(LogpArgs a)
 {
     constexpr int PER = TYPE == RFX_F32 ? 4 : 8, LOADS = E / PER, SIZE = 16 / PER;
     __shared__ Shared sh;
-    __shared__ Stat ws[kWaves];
     const int tid = threadIdx.x, wave = tid >> 6;
     const int row = blockIdx.x / a.S, c = blockIdx.x - row * a.S;
     const char *zr = static_cast<const char *>(a.z) + (int64_t)row * a.stride * SIZE;
@@ -217,87 +244,97 @@ __global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(LogpArgs a)
     const int token = a.tokens ? a.tokens[row] : -1;
     const bool known = (unsigned)token < (unsigned)a.V;
 
-    float z[E];
     const auto index = [&](int l) { return c * a.chunk + (l * kThreads + tid) * PER - lead; }; // of a load's first element
+    const bool whole = c * a.chunk >= lead && (c + 1) * a.chunk - lead <= a.V;                 // uniform
+    u32x4 raw[LOADS];
+    if (whole) {
+        const char *p = zr + ((int64_t)c * a.chunk - lead) * SIZE;
 #pragma unroll
-    for (int l = 0; l < LOADS; l++) {
-        const int i = index(l);
-        if (i >= 0 && i + PER <= a.V) {
-            const u32x4 u = *reinterpret_cast<const u32x4 *>(zr + (int64_t)i * SIZE);
+        for (int l = 0; l < LOADS; l++)
+            raw[l] = *reinterpret_cast<const u32x4 *>(p + 16 * (unsigned)(l * kThreads + tid));
+    } else { // what the row does not fill reads the workspace instead
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const uint32_t w = u[e]; // a bit cast of the vector's element itself reads another one
-                if (TYPE == RFX_F32) {
-                    z[l * PER + e] = __uint_as_float(w);
-                } else if (TYPE == RFX_BF16) {
-                    z[l * PER + 2 * e] = __uint_as_float(w << 16);
-                    z[l * PER + 2 * e + 1] = __uint_as_float(w & 0xffff0000u);
-                } else {
-                    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-                    const h2 h = __builtin_bit_cast(h2, w);
-                    z[l * PER + 2 * e] = (float)h[0];
-                    z[l * PER + 2 * e + 1] = (float)h[1];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < PER; e++)
-                z[l * PER + e] = i + e >= 0 && i + e < a.V ? logit<TYPE>(zr, i + e) : -INFINITY;
+        for (int l = 0; l < LOADS; l++) {
+            const int i = index(l);
+            const bool full = i >= 0 && i + PER <= a.V;
+            raw[l] = *reinterpret_cast<const u32x4 *>(full ? zr + (int64_t)i * SIZE : reinterpret_cast<const char *>(a.stat));
         }
     }
-    const float zt = known ? logit<TYPE>(zr, token) : INFINITY;
+    const float zt = uniform(known ? logit<TYPE>(zr, token) : INFINITY);
 
-    // the thread's largest, the first of equal ones
-    float top = -INFINITY, mx = -INFINITY;
-    int at = 0;
+    float z[E];
 #pragma unroll
-    for (int j = 0; j < E; j++) {
-        if (z[j] > top) {
-            top = z[j];
-            at = j;
+    for (int l = 0; l < LOADS; l++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint32_t w = raw[l][e]; // a bit cast of the vector's element itself reads another one
+            if (TYPE == RFX_F32) {
+                z[l * PER + e] = __uint_as_float(w);
+            } else if (TYPE == RFX_BF16) {
+                z[l * PER + 2 * e] = __uint_as_float(w << 16);
+                z[l * PER + 2 * e + 1] = __uint_as_float(w & 0xffff0000u);
+            } else {
+                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                const h2 h = __builtin_bit_cast(h2, w);
+                z[l * PER + 2 * e] = (float)h[0];
+                z[l * PER + 2 * e + 1] = (float)h[1];
+            }
         }
-        mx = fmaxf(mx, z[j]);
-    }
-    const float m = wave_max(mx), base = m == -INFINITY ? 0.f : m;
+    if (!whole)
+#pragma unroll
+        for (int l = 0; l < LOADS; l++) {
+            const int i = index(l);
+            if (i < 0 || i + PER > a.V) {
+#pragma unroll
+                for (int e = 0; e < PER; e++)
+                    z[l * PER + e] = i + e >= 0 && i + e < a.V ? logit<TYPE>(zr, i + e) : -INFINITY;
+            }
+        }
+
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < E; j++)
+        top = fmaxf(top, z[j]);
+    // e^(z - m) = 2^(c z - c m), one fused operation: c m is rounded, by
+    // the same for all, and what it lacks is made up for below
+    const float m = uniform(wave_max(top)), base = m == -INFINITY ? 0.f : m;
+    const float off = base * kLog2e, lack = fmaf(base, kLog2e, -off);
     float rest = 0.f, dot = 0.f;
-    int n = 0, above = 0;
 #pragma unroll
     for (int j = 0; j < E; j++) {
-        const float d = z[j] - base;
-        const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-        const bool is_one = e == 1.0f;
-        n += __popcll(__ballot(is_one));
-        rest += is_one ? 0.f : e;
-        dot = fmaf(e, fmaxf(d, -1e30f), dot); // 0 * -inf where nothing is left
-        above += __popcll(__ballot(z[j] > zt));
+        const float x = fmaxf(fmaf(z[j], kLog2e, -off), -1e30f); // 0 * -inf where nothing is left
+        const float e = __builtin_amdgcn_exp2f(x);
+        rest += e;
+        dot = fmaf(e, x, dot);
     }
-    rest = wave_sum(rest);
-    dot = wave_sum(dot);
-    if ((tid & 63) == 0)
-        ws[wave] = Stat{m, (float)n, rest, dot, (float)above};
-    __syncthreads();
-    if (tid == 0) {
-        Stat s = ws[0];
+    const float fix = __builtin_amdgcn_exp2f(-lack), s = uniform(wave_sum(rest));
+    rest = s * fix;
+    dot = (wave_sum(dot) - lack * s) * fix;
+    int n = 0, above = 0;
+    // little beside the largest, or c m past fp32's range: the others alone
+    if (rest < 1.25f || fabsf(base) > 2e38f) {
+        rest = dot = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWaves; w++)
-            s.m = fmaxf(s.m, ws[w].m);
-        s.n = s.rest = s.dot = s.above = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; w++) {
-            const Stat &p = ws[w];
-            const float d = p.m == -INFINITY ? 0.f : fmaxf(p.m - s.m, -1e30f); // times the mass stays finite
-            const float f = p.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(d * kLog2e);
-            const bool first = p.m == s.m;
-            s.n += first ? p.n : 0.f;
-            s.rest += first ? p.rest : f * (p.n + p.rest);
-            s.dot += f * (p.dot + d * (p.n + p.rest));
-            s.above += p.above;
+        for (int j = 0; j < E; j++) {
+            const float x = fmaxf((z[j] - m) * kLog2e, -1e30f), e = z[j] == m ? 0.f : __builtin_amdgcn_exp2f((z[j] - m) * kLog2e);
+            rest += e;
+            dot = fmaf(e, x, dot);
+            n += z[j] == m;
         }
-        a.stat[(size_t)row * a.S + c] = s;
+        rest = m == INFINITY ? NAN : wave_sum(rest);
+        dot = wave_sum(dot);
+        n = m == -INFINITY ? 0 : wave_sum(n);
     }
+    if (m > zt) {
+#pragma unroll
+        for (int j = 0; j < E; j++)
+            above += z[j] > zt;
+        above = wave_sum(above);
+    }
+    if ((tid & 63) == 0) // from powers of two
+        a.stat[((size_t)row * a.S + c) * kWaves + wave] = Stat{m, (float)n, rest, dot * 0.69314718055994531f, (float)above};
     if (a.k)
-        top_keys<E>(sh, a.k, top > -INFINITY ? make_key(top, index(at / PER) + at % PER) : 0,
-                    [&](int j) { return z[j] > -INFINITY ? make_key(z[j], index(j / PER) + j % PER) : 0; },
+        top_keys<E>(sh, a.k, top, [&](int j) { return z[j]; }, [&](int j) { return make_key(z[j], index(j / PER) + j % PER); },
                     a.keys + ((size_t)row * a.S + c) * a.k);
 }
 
@@ -310,34 +347,56 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     __shared__ float tops[kWaves];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const size_t row = blockIdx.x;
-    const Stat *st = a.stat + row * a.S;
+    const rfx_logprob &o = a.out;
+    const Stat *st = a.stat + row * a.S * kWaves;
+    const int parts = a.S * kWaves;
 
-    float m = -INFINITY;
-    for (int i = tid; i < a.S; i += kThreads)
+    // Everything is read before it is waited for: the first statistics, the
+    // keys (S lists of k; the threads of a wave take every fourth), the token.
+    const Stat none = {-INFINITY, 0.f, 0.f, 0.f, 0.f}, own = tid < parts ? st[tid] : none;
+    const uint64_t *keys = a.keys + row * a.S * a.k;
+    const int n = a.S * a.k, first = lane * kWaves + wave;
+    uint64_t mine[kJoinKeys];
+#pragma unroll
+    for (int j = 0; j < kJoinKeys; j++) {
+        mine[j] = 0;
+        if (j * kThreads < n) // uniform
+            mine[j] = j * kThreads + first < n ? keys[j * kThreads + first] : 0;
+    }
+    const int token = a.tokens ? a.tokens[row] : -1;
+    const bool known = (unsigned)token < (unsigned)a.V;
+    float zt = 0.f;
+    if (known) {
+        const char *zr = static_cast<const char *>(a.z) + (int64_t)row * a.stride * (o.type == RFX_F32 ? 4 : 2);
+        zt = o.type == RFX_F32 ? logit<RFX_F32>(zr, token) : o.type == RFX_F16 ? logit<RFX_F16>(zr, token) : logit<RFX_BF16>(zr, token);
+    }
+
+    float m = own.m;
+    for (int i = tid + kThreads; i < parts; i += kThreads)
         m = fmaxf(m, st[i].m);
     m = wave_max(m);
     if (lane == 0)
         tops[wave] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    m = uniform(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
     double ones = 0.0, rest = 0.0, dot = 0.0, above = 0.0;
-    for (int i = tid; i < a.S; i += kThreads) {
-        const Stat p = st[i];
+    const auto add = [&](const Stat &p) {
         above += p.above;
         if (p.m == -INFINITY && p.n + p.rest == 0.f)
-            continue;
-        const double d = (double)p.m - (double)m, f = p.m == m ? 1.0 : exp(d), mass = (double)p.n + (double)p.rest;
+            return;
+        const float d = fmaxf(p.m - m, -1e30f);
+        const double f = p.m == m ? 1.f : __builtin_amdgcn_exp2f(d * kLog2e), mass = (double)p.n + (double)p.rest;
         ones += p.m == m ? (double)p.n : 0.0;
         rest += p.m == m ? (double)p.rest : f * mass;
-        dot += f * ((double)p.dot + (p.m == m ? 0.0 : d * mass));
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        ones += __shfl_xor(ones, o, 64);
-        rest += __shfl_xor(rest, o, 64);
-        dot += __shfl_xor(dot, o, 64);
-        above += __shfl_xor(above, o, 64);
-    }
+        dot += f * ((double)p.dot + (p.m == m ? 0.0 : (double)d * mass));
+    };
+    add(own);
+    for (int i = tid + kThreads; i < parts; i += kThreads)
+        add(st[i]);
+    ones = wave_sum(ones);
+    rest = wave_sum(rest);
+    dot = wave_sum(dot);
+    above = wave_sum(above);
     if (lane == 0) {
         part[wave][0] = ones;
         part[wave][1] = rest;
@@ -355,47 +414,33 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     }
     const double s = ones + rest;
     const bool any = !(s == 0.0); // a row that nothing is left of: -inf, entropy 0
-    const double ls = any ? log1p(ones - 1.0 + rest) : 0.0, lse = any ? (double)m + ls : -INFINITY;
+    const double ls = any ? log1p(ones - 1.0 + rest) : 0.0;
     const auto logp = [&](float z) { return z == -INFINITY && ls == ls ? -INFINITY : (float)((double)z - (double)m - ls); };
     if (tid == 0) {
-        const rfx_logprob &o = a.out;
         if (o.lse)
-            o.lse[row] = (float)lse;
+            o.lse[row] = any ? (float)((double)m + ls) : -INFINITY;
         if (o.entropy)
             o.entropy[row] = any ? (float)(ls - dot / s) : 0.f;
-        const int token = a.tokens ? a.tokens[row] : -1;
-        const bool known = (unsigned)token < (unsigned)a.V;
         if (o.rank)
             o.rank[row] = known ? (int)above : -1;
-        if (o.logprob) {
-            const int size = o.type == RFX_F32 ? 4 : 2;
-            const char *zr = static_cast<const char *>(a.z) + (int64_t)row * a.stride * size;
-            float z = 0.f;
-            if (known)
-                z = o.type == RFX_F32 ? logit<RFX_F32>(zr, token) : o.type == RFX_F16 ? logit<RFX_F16>(zr, token) : logit<RFX_BF16>(zr, token);
-            o.logprob[row] = known ? logp(z) : 0.f;
-        }
+        if (o.logprob)
+            o.logprob[row] = known ? logp(zt) : 0.f;
     }
     if (!a.k)
         return;
-    // S lists of k: neighbouring threads of a wave take every fourth key
-    const uint64_t *keys = a.keys + row * a.S * a.k;
-    const int n = a.S * a.k, first = lane * kWaves + wave;
-    uint64_t mine[kJoinKeys], best = 0;
+    uint64_t best = 0;
 #pragma unroll
-    for (int j = 0; j < kJoinKeys; j++) {
-        const int i = j * kThreads + first;
-        mine[j] = i < n ? keys[i] : 0;
+    for (int j = 0; j < kJoinKeys; j++)
         best = mine[j] > best ? mine[j] : best;
-    }
-    top_keys<kJoinKeys>(sh, a.k, best, [&](int j) { return mine[j]; }, best_keys);
+    const auto value = [](uint64_t key) { return key ? value_of(key) : -INFINITY; };
+    top_keys<kJoinKeys>(sh, a.k, value(best), [&](int j) { return value(mine[j]); }, [&](int j) { return mine[j]; }, best_keys);
     __syncthreads();
     if (tid < a.k) {
         const uint64_t key = best_keys[tid];
-        if (a.out.top_index)
-            a.out.top_index[row * a.k + tid] = key ? index_of(key) : -1;
-        if (a.out.top_logprob)
-            a.out.top_logprob[row * a.k + tid] = key ? logp(value_of(key)) : -INFINITY;
+        if (o.top_index)
+            o.top_index[row * a.k + tid] = key ? index_of(key) : -1;
+        if (o.top_logprob)
+            o.top_logprob[row * a.k + tid] = key ? logp(value_of(key)) : -INFINITY;
     }
 }
 
@@ -406,23 +451,26 @@ struct Plan {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Chunks of 8192 logits, or of 2048 where the long ones would leave compute
-// units idle and the join still holds the short ones' keys.
-Plan plan(int q, int V, int k)
+// Chunks of four loads per thread (4096 fp32 or 8192 16-bit logits; twice the
+// fp32 ones where the join could not hold all keys), or of 2048 logits where
+// the long ones would leave compute units idle.
+Plan plan(int type, int q, int V, int k)
 {
     Plan p{};
     // a row may start up to seven elements into its first 16 bytes
     const auto chunks = [&](int E) { return (int)ceil_div((int64_t)V + 7, (int64_t)E * kThreads); };
-    const int fine = chunks(kShort);
-    p.E = (int64_t)q * chunks(kLong) < 512 && (int64_t)fine * (k ? k : 1) <= kJoinKeys * kThreads ? kShort : kLong;
+    const auto fits = [&](int E) { return chunks(E) * k <= kJoinKeys * kThreads; };
+    p.E = kLoads * (type == RFX_F32 && fits(kLoads * 4) ? 4 : 8);
+    if ((int64_t)q * chunks(p.E) < 512 && fits(kShort))
+        p.E = kShort;
     p.chunk = p.E * kThreads;
     p.S = chunks(p.E);
-    p.stat = align256((size_t)q * p.S * sizeof(Stat));
+    p.stat = align256((size_t)q * p.S * kWaves * sizeof(Stat));
     p.keys = align256((size_t)q * p.S * k * sizeof(uint64_t));
     return p;
 }
 
-static_assert((kMaxVocab + 7 + kLong * kThreads - 1) / (kLong * kThreads) * kMaxTop <= kJoinKeys * kThreads, "the join holds all keys");
+static_assert((kMaxVocab + 7 + 8 * kLoads * kThreads - 1) / (8 * kLoads * kThreads) * kMaxTop <= kJoinKeys * kThreads, "the join holds all keys");
 
 bool shape_ok(int q, int V, int k) { return q >= 0 && q <= RFX_LOGPROB_MAX_Q && V >= 1 && V <= kMaxVocab && k >= 0 && k <= kMaxTop; }
 
@@ -446,8 +494,9 @@ size_t rfx_token_logprobs_workspace_bytes(int q, int n_vocab, int top_k)
 {
     if (!shape_ok(q, n_vocab, top_k))
         return 0;
-    const Plan p = plan(q, n_vocab, top_k);
-    return p.stat + p.keys;
+    // for logits of any type: fp32's chunks are the most
+    const Plan a = plan(RFX_F32, q, n_vocab, top_k), b = plan(RFX_BF16, q, n_vocab, top_k);
+    return std::max(a.stat, b.stat) + std::max(a.keys, b.keys);
 }
 
 int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens, const rfx_logprob *O, void *ws, size_t ws_bytes,
@@ -479,10 +528,11 @@ int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens
         return fail(RFX_E_INVAL, "rfx_token_logprobs: top_index and top_logprob want top_k");
     if (!O->logprob && !O->lse && !O->entropy && !O->rank && !O->top_index && !O->top_logprob)
         return fail(RFX_E_INVAL, "rfx_token_logprobs: no output");
-    const Plan p = plan(O->q, O->n_vocab, O->top_k);
-    if (!ws || ws_bytes < p.stat + p.keys) {
+    const Plan p = plan(O->type, O->q, O->n_vocab, O->top_k);
+    const size_t need = rfx_token_logprobs_workspace_bytes(O->q, O->n_vocab, O->top_k);
+    if (!ws || ws_bytes < need) {
         if (O->q)
-            return fail(RFX_E_WORKSPACE, "rfx_token_logprobs: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.stat + p.keys);
+            return fail(RFX_E_WORKSPACE, "rfx_token_logprobs: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, need);
     } else if ((st = check_ptr(ws, 256, "ws"))) {
         return st;
     }
@@ -503,8 +553,10 @@ int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens
     const hipStream_t hs = (hipStream_t)stream;
     if (p.E == kShort)
         launch<kShort>(a, O->type, hs);
+    else if (p.E == kLoads * 4) // fp32 alone
+        hipLaunchKernelGGL((logprob_chunk_kernel<RFX_F32, kLoads * 4>), dim3((unsigned)a.q * a.S), dim3(kThreads), 0, hs, a);
     else
-        launch<kLong>(a, O->type, hs);
+        launch<kLoads * 8>(a, O->type, hs);
     if ((st = hip_status("token_logprobs chunk launch")))
         return st;
     hipLaunchKernelGGL(logprob_join_kernel, dim3(a.q), dim3(kThreads), 0, hs, a);
