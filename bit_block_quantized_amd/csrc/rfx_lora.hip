@@ -36,6 +36,7 @@ struct LoraArgs {
     int tiles;        // of all matrices
     int groups;       // of up to eight tiles
     int splits, slots;
+    int down;         // workgroups of the first launch
     int T16;          // tokens in whole tiles
     float *v;         // [splits][T16][n_mats * R16]
     int row_blocks[kMats]; // of the second launch
@@ -51,12 +52,8 @@ struct Terms<BF16> {
     static constexpr int N = 3, SUMS = 1;
     static constexpr float IN = 1.0f;
     static __device__ __forceinline__ void split(const float (&x)[8], u4 (&t)[3]) { split_terms<BF16, 3>(x, t); }
-    static __device__ __forceinline__ void mma(u4 a, const u4 (&t)[3], f32x4 (&c)[1])
-    {
-        c[0] = BF16::mma16(a, t[2], c[0]); // the smallest first
-        c[0] = BF16::mma16(a, t[1], c[0]);
-        c[0] = BF16::mma16(a, t[0], c[0]);
-    }
+    // One term's product, the smallest first (s = 0).
+    static __device__ __forceinline__ void mma(int s, u4 a, const u4 (&t)[3], f32x4 (&c)[1]) { c[0] = BF16::mma16(a, t[2 - s], c[0]); }
     static __device__ __forceinline__ f32x4 total(const f32x4 (&c)[1]) { return c[0]; }
 };
 
@@ -74,11 +71,7 @@ struct Terms<F16> {
             t[1][i] = F16::pack((x[2 * i] - back.x) * 0x1p11f, (x[2 * i + 1] - back.y) * 0x1p11f);
         }
     }
-    static __device__ __forceinline__ void mma(u4 a, const u4 (&t)[2], f32x4 (&c)[2])
-    {
-        c[0] = F16::mma16(a, t[0], c[0]);
-        c[1] = F16::mma16(a, t[1], c[1]);
-    }
+    static __device__ __forceinline__ void mma(int s, u4 a, const u4 (&t)[2], f32x4 (&c)[2]) { c[s] = F16::mma16(a, t[s], c[s]); }
     static __device__ __forceinline__ f32x4 total(const f32x4 (&c)[2]) { return c[0] + c[1] * 0x1p-11f; }
 };
 
@@ -91,98 +84,155 @@ __device__ __forceinline__ int adapter_of(const rfx_lora &l, int t)
     return (unsigned)a < (unsigned)l.n_adapters ? a : -1;
 }
 
-// v = A x: a workgroup takes 16 tokens, one of `splits` parts of the columns
-// (a quarter of it per wave, added through LDS) and every slots-th adapter of
-// its tokens, against TILES of the 16-row tiles of all matrices, which stand
-// one after the other.
-template <class T, int TILES>
-__global__ __launch_bounds__(kThreads, 2) void lora_down_kernel(LoraArgs a)
+// v = A x: a workgroup takes NB times 16 tokens, one of `splits` parts of the
+// columns (a quarter of it per wave, added through LDS) and every slots-th
+// adapter of its tokens, against TILES of the 16-row tiles of all matrices,
+// which stand one after the other. 64 columns at a time, so that a row's 128
+// bytes are read together, with the next ones' loads in flight.
+// The registers of six tiles and more of 32 tokens leave one wave per SIMD.
+constexpr int down_waves(int tiles, int nb) { return tiles * nb > 8 ? 1 : 2; }
+
+template <class T, int TILES, int NB>
+__global__ __launch_bounds__(kThreads, down_waves(TILES, NB)) void lora_down_kernel(LoraArgs a)
 {
     using X = Terms<T>;
-    __shared__ __align__(16) f32x4 sums[kWaves][TILES][64];
+    constexpr int SUMS = TILES * NB > 4 ? 4 : TILES * NB; // tiles in LDS at a time
+    __shared__ __align__(16) f32x4 sums[kWaves][SUMS][64];
     const rfx_lora &l = a.l;
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int b = blockIdx.x;
+    // Workgroups go round the eight XCDs in order: a contiguous run of them to
+    // each, so that its L2 keeps the few adapters of its tokens.
+    int b = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
+    if (b >= a.down)
+        return;
     const int split = b % a.splits;
     b /= a.splits;
     const int tile0 = b % a.groups * TILES;
     b /= a.groups;
-    const int slot = b % a.slots, t0 = b / a.slots * 16;
-    const int steps = l.cols / 32, part = a.splits * kWaves, p = split * kWaves + wave;
+    const int slot = b % a.slots, t0 = b / a.slots * 16 * NB;
+    const int steps = (l.cols + 63) / 64, part = a.splits * kWaves, p = split * kWaves + wave;
     const int k0 = (int)((int64_t)steps * p / part), k1 = (int)((int64_t)steps * (p + 1) / part);
-    const int id = adapter_of(l, t0 + r16);
 
-    f32x4 acc[TILES][X::SUMS];
+    f32x4 acc[NB][TILES][X::SUMS];
+    int id[NB];
+    bool mine[NB]; // this workgroup has the lane's token
+    uint32_t todo = 0;
 #pragma unroll
-    for (int i = 0; i < TILES; i++)
+    for (int n = 0; n < NB; n++) {
+        id[n] = adapter_of(l, t0 + 16 * n + r16);
+        mine[n] = false;
+        todo |= ((uint32_t)__ballot(id[n] >= 0) & 0xffffu) << 16 * n;
 #pragma unroll
-        for (int s = 0; s < X::SUMS; s++)
-            acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < TILES; i++)
+#pragma unroll
+            for (int s = 0; s < X::SUMS; s++)
+                acc[n][i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    }
 
-    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
-    bool mine = false; // this workgroup has the lane's token
-    for (int n = 0; todo; n++) {
-        const int first = __builtin_ctz(todo), ad = __builtin_amdgcn_readlane(id, first);
-        const bool match = id == ad;
-        todo &= ~(uint32_t)__ballot(match);
-        if (n % a.slots != slot)
+    bool any = false;
+    for (int turn = 0; todo; turn++) {
+        const int first = __builtin_ctz(todo);
+        int ad = __builtin_amdgcn_readlane(id[0], first & 15);
+        if (NB > 1 && first >= 16)
+            ad = __builtin_amdgcn_readlane(id[NB - 1], first & 15);
+        const bool own = turn % a.slots == slot;
+        any |= own;
+        uint32_t keep[NB];
+        const float *x[NB];
+#pragma unroll
+        for (int n = 0; n < NB; n++) {
+            const bool match = id[n] == ad;
+            todo &= ~(((uint32_t)__ballot(match) & 0xffffu) << 16 * n);
+            mine[n] |= match & own;
+            keep[n] = match ? ~0u : 0u;
+            // lanes of other adapters' tokens read along with the first one's
+            x[n] = l.x + (int64_t)(t0 + (match ? 16 * n + r16 : first)) * l.x_stride + 8 * g4;
+        }
+        if (!own || k0 >= k1)
             continue;
-        mine |= match;
-        const uint32_t keep = match ? ~0u : 0u;
-        // lanes of other adapters' tokens read along with the first one's
-        const float *x = l.x + (int64_t)(t0 + (match ? r16 : first)) * l.x_stride + 8 * g4;
         const uint16_t *w[TILES];
 #pragma unroll
         for (int i = 0; i < TILES; i++) {
             const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + r16, l.rank - 1);
             w[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * g4;
         }
-        f32x4 xn[2];
-        u4 wn[TILES];
-        const auto load = [&](int k) {
-            xn[0] = *reinterpret_cast<const f32x4 *>(x + 32 * (size_t)k);
-            xn[1] = *reinterpret_cast<const f32x4 *>(x + 32 * (size_t)k + 4);
+        struct Step {
+            f32x4 x[2][NB][2];
+            u4 w[TILES][2];
+        } s0, s1;
+        const auto load = [&](Step &s, int k) { // columns past the last: the step's first half again
+            const size_t at = 64 * (size_t)min(k, k1 - 1), up = at + 32 < (size_t)l.cols ? 32 : 0;
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int n = 0; n < NB; n++)
+#pragma unroll
+                    for (int q = 0; q < 2; q++)
+                        s.x[h][n][q] = *reinterpret_cast<const f32x4 *>(x[n] + at + h * up + 4 * q);
 #pragma unroll
             for (int i = 0; i < TILES; i++)
-                wn[i] = *reinterpret_cast<const u4 *>(w[i] + 32 * (size_t)k);
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    s.w[i][h] = *reinterpret_cast<const u4 *>(w[i] + at + h * up);
+            __builtin_amdgcn_sched_barrier(0);
         };
-        if (k0 < k1)
-            load(k0);
-        for (int k = k0; k < k1; k++) {
-            float xc[8];
-            u4 wc[TILES], t[X::N];
+        const auto compute = [&](const Step &s, int k) {
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                xc[e] = xn[e >> 2][e & 3] * X::IN;
+            for (int h = 0; h < 2; h++) {
+                const uint32_t in = 64 * k + 32 * h < l.cols ? ~0u : 0u;
 #pragma unroll
-            for (int i = 0; i < TILES; i++)
-                wc[i] = wn[i];
-            load(min(k + 1, k1 - 1));
-            X::split(xc, t);
+                for (int n = 0; n < NB; n++) {
+                    float xc[8];
+                    u4 t[X::N];
 #pragma unroll
-            for (int s = 0; s < X::N; s++)
-                t[s] &= keep;
+                    for (int e = 0; e < 8; e++)
+                        xc[e] = s.x[h][n][e >> 2][e & 3] * X::IN;
+                    X::split(xc, t);
 #pragma unroll
-            for (int i = 0; i < TILES; i++)
-                X::mma(wc[i], t, acc[i]);
+                    for (int q = 0; q < X::N; q++)
+                        t[q] &= keep[n] & in;
+#pragma unroll
+                    for (int q = 0; q < X::N; q++) // neighbours do not depend on one another
+#pragma unroll
+                        for (int j = 0; j < TILES; j++)
+                            X::mma(q, s.w[j][h], t, acc[n][j]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        load(s0, k0);
+        for (int k = k0; k < k1; k += 2) {
+            load(s1, k + 1);
+            compute(s0, k);
+            if (k + 1 == k1)
+                break;
+            load(s0, k + 2);
+            compute(s1, k + 1);
         }
     }
-    if (!__ballot(mine)) // the same in every wave
+    if (!any) // the same in every wave
         return;
-#pragma unroll
-    for (int i = 0; i < TILES; i++)
-        sums[wave][i][lane] = X::total(acc[i]) * (1.0f / X::IN);
-    __syncthreads();
-    // lane: token r16, rows 4 g4 .. + 3 of tile i
+    // lane: token r16 of its sixteen, rows 4 g4 .. + 3 of tile i
     const int RS = l.n_mats * a.R16;
-    for (int i = wave; i < min(TILES, a.tiles - tile0); i += kWaves) {
-        f32x4 s = sums[0][i][lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; w++)
-            s += sums[w][i][lane];
-        if (mine)
-            *reinterpret_cast<f32x4 *>(a.v + ((size_t)split * a.T16 + t0 + r16) * RS + 16 * (tile0 + i) + 4 * g4) = s;
+    for (int j = 0; j < TILES * NB; j += SUMS) {
+        if (j)
+            __syncthreads();
+#pragma unroll
+        for (int i = j; i < j + SUMS; i++)
+            if (i < TILES * NB)
+                sums[wave][i - j][lane] = X::total(acc[i / TILES][i % TILES]) * (1.0f / X::IN);
+        __syncthreads();
+        const int i = j + wave, n = i / TILES, tile = tile0 + i % TILES; // SUMS is at most the waves' number
+        if (wave < SUMS && i < TILES * NB && tile < a.tiles) {
+            f32x4 s = sums[0][wave][lane];
+#pragma unroll
+            for (int w = 1; w < kWaves; w++)
+                s += sums[w][wave][lane];
+            if (NB > 1 && n ? mine[NB - 1] : mine[0])
+                *reinterpret_cast<f32x4 *>(a.v + ((size_t)split * a.T16 + t0 + 16 * n + r16) * RS + 16 * tile + 4 * g4) = s;
+        }
     }
 }
 
@@ -293,8 +343,10 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
                     for (int s = 0; s < X::N; s++)
                         tm[s] = vt[k][s] & keep[j];
 #pragma unroll
-                    for (int i = 0; i < RT; i++)
-                        X::mma(w[j][i][k], tm, acc[i]);
+                    for (int s = 0; s < X::N; s++)
+#pragma unroll
+                        for (int i = 0; i < RT; i++)
+                            X::mma(s, w[j][i][k], tm, acc[i]);
                 }
         }
     }
@@ -323,6 +375,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
 
 struct Plan {
     int R16, tiles, groups, splits, slots, T16;
+    bool wide; // 32 tokens per workgroup of the first launch
     size_t bytes;
 };
 
@@ -332,16 +385,17 @@ Plan plan(int T, int rank, int n_mats, int cols, int n_adapters)
     p.R16 = (rank + 15) / 16 * 16;
     p.tiles = n_mats * p.R16 / 16;
     p.groups = (p.tiles + 7) / 8;
-    p.T16 = (T + 15) / 16 * 16;
-    const int blocks = p.T16 / 16 > 0 ? p.T16 / 16 : 1;
+    p.wide = T > 512;
+    const int per = p.wide ? 32 : 16, blocks = T > per ? (T + per - 1) / per : 1;
+    p.T16 = blocks * per;
     // Adapters of a block of tokens: side by side where tokens are few and
     // may each have their own, one after the other where they are many.
     p.slots = T <= 128 ? 16 : T <= 512 ? 4 : 1;
     p.slots = p.slots < T ? p.slots : T;
     p.slots = p.slots < n_adapters ? p.slots : n_adapters;
-    // Columns split until there are two workgroups per compute unit, down to
-    // a step of 32 columns per wave.
-    const int want = 512 / (blocks * p.groups), most = (cols + 127) / 128;
+    // Columns split until there is a workgroup for every place, down to a step
+    // of 64 columns per wave.
+    const int waves = down_waves(p.tiles < 8 ? p.tiles : 8, p.wide ? 2 : 1), want = 256 * waves / (blocks * p.groups), most = (cols + 255) / 256;
     p.splits = want < most ? want : most;
     p.splits = p.splits < 1 ? 1 : p.splits > kMaxSplits ? kMaxSplits : p.splits;
     p.bytes = (size_t)p.splits * p.T16 * n_mats * p.R16 * sizeof(float);
@@ -354,18 +408,34 @@ bool shape_ok(int T, int rank, int n_mats, int cols, int n_adapters)
            cols >= 32 && cols % 32 == 0 && cols <= 1 << 20 && n_adapters >= 1 && n_adapters <= 1 << 20;
 }
 
-template <class T>
-int launch_down(const LoraArgs &a, hipStream_t st)
+template <class T, int NB>
+void launch_down_tiles(LoraArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)(a.T16 / 16) * a.slots * a.groups * a.splits), block(kThreads);
+    a.down = a.T16 / (16 * NB) * a.slots * a.groups * a.splits;
+    const dim3 grid((a.down + 7) / 8 * 8), block(kThreads);
+#define RFX_LORA(TILES) hipLaunchKernelGGL((lora_down_kernel<T, TILES, NB>), grid, block, 0, st, a)
     if (a.tiles <= 1)
-        hipLaunchKernelGGL((lora_down_kernel<T, 1>), grid, block, 0, st, a);
+        RFX_LORA(1);
     else if (a.tiles <= 2)
-        hipLaunchKernelGGL((lora_down_kernel<T, 2>), grid, block, 0, st, a);
+        RFX_LORA(2);
+    else if (a.tiles <= 3)
+        RFX_LORA(3);
     else if (a.tiles <= 4)
-        hipLaunchKernelGGL((lora_down_kernel<T, 4>), grid, block, 0, st, a);
+        RFX_LORA(4);
+    else if (a.tiles <= 6)
+        RFX_LORA(6);
     else
-        hipLaunchKernelGGL((lora_down_kernel<T, 8>), grid, block, 0, st, a);
+        RFX_LORA(8);
+#undef RFX_LORA
+}
+
+template <class T>
+int launch_down(LoraArgs &a, bool wide, hipStream_t st)
+{
+    if (wide)
+        launch_down_tiles<T, 2>(a, st);
+    else
+        launch_down_tiles<T, 1>(a, st);
     return hip_status("lora down launch");
 }
 
@@ -446,7 +516,7 @@ int rfx_lora_apply(const rfx_lora *L, void *ws, size_t ws_bytes, void *stream)
     a.T16 = p.T16;
     a.v = static_cast<float *>(ws);
     const hipStream_t hs = (hipStream_t)stream;
-    st = L->type == RFX_BF16 ? launch_down<BF16>(a, hs) : launch_down<F16>(a, hs);
+    st = L->type == RFX_BF16 ? launch_down<BF16>(a, p.wide, hs) : launch_down<F16>(a, p.wide, hs);
     if (st)
         return st;
     return L->type == RFX_BF16 ? launch_up<BF16>(a, hs) : launch_up<F16>(a, hs);
