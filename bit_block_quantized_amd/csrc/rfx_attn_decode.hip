@@ -120,12 +120,16 @@ __global__ __launch_bounds__(64 * kWaves) void attn_decode_kernel(Args args)
             sq = {gr.t0, gr.nt, gr.len - 1, gr.len}; // as if at the last key
             kt = range_tiles(BN, 0, gr.len);
         } else {
-            sq = load_seq(kv, seq);
-            if (sq.nq > 0)
-                prefix_of(kv, args.pre, seq, sq, gr);
-            else
-                gr.len = 0;
+            int g;
+            sq = load_seq_prefix(kv, args.pre, seq, g, gr);
             kt = range_tiles(BN, gr.len, min(sq.kv, sq.p0 + sq.nq));
+            if (split == 0 && threadIdx.x == 0) {
+                int per, n_own, n_group = 0;
+                split_tiles(a, kt.n, per, n_own);
+                if (gr.len)
+                    split_tiles(args.group, range_tiles(args.group.bn, 0, gr.len).n, per, n_group);
+                args.units[unit] = {sq.t0, sq.nq, n_own, n_group, g, (sq.t0 - gr.t0) * kv.G};
+            }
         }
         alone = !group && gr.len == 0;
     } else {

@@ -20,26 +20,41 @@ namespace {
 
 constexpr int kMaxSplits = 64; // one lane of the join each
 
-// Adds the n partials of one row, `stride` elements apart, by their factors
-// (lane i: the i-th's), eight loads at a time.
+// The first eight partials of a row, `stride` elements apart, past the last
+// (of most) the last again.
 template <class V>
-__device__ __forceinline__ void add_partials(V &sum, const float *p, size_t stride, int n, float factor)
+__device__ __forceinline__ void first_partials(V (&x)[8], const float *p, size_t stride, int most)
+{
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        x[i] = *reinterpret_cast<const V *>(p + (size_t)min(i, most - 1) * stride);
+}
+
+// Adds the n partials of a row by their factors (lane i: the i-th's); x: the
+// first of them.
+template <class V>
+__device__ __forceinline__ void add_partials(V &sum, V (&x)[8], const float *p, size_t stride, int n, float factor)
 {
     for (int s = 0; s < n; s += 8) {
-        V x[8];
+        V y[8];
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            x[i] = *reinterpret_cast<const V *>(p + (size_t)min(s + i, n - 1) * stride);
+            y[i] = x[i];
+        if (s + 8 < n) // the next ones' loads
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x[i] = *reinterpret_cast<const V *>(p + (size_t)min(s + 8 + i, n - 1) * stride);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(factor), min(s + i, 63)));
             if (s + i < n)
-                sum += x[i] * w;
+                sum += y[i] * w;
         }
     }
 }
 
-// One wave per row of a sequence's new tokens.
+// One wave per row of a sequence's new tokens. The sequence's own partials are
+// read beside the unit's record, which says where the prefix's are.
 template <class T, int DP>
 __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs args)
 {
@@ -50,33 +65,31 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs args)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int quads = o.rows / 4, unit = blockIdx.x >> __builtin_ctz(quads), row = (blockIdx.x & (quads - 1)) * 4 + wave;
     const int seq = kv.div_hk(unit), hk = kv.div_hk.rem(unit, seq);
-    const Seq sq = load_seq(kv, seq);
-    if (row >= sq.nq * kv.G)
+    const size_t own = (size_t)unit * o.S * o.rows + row, so = (size_t)o.rows * DP, sg = (size_t)g.rows * DP;
+    const float *po = o.part + own * DP + PER * lane;
+    const f2 any = *reinterpret_cast<const f2 *>(o.stat + (own + (size_t)min(lane, o.S - 1) * o.rows) * 2);
+    fp xo[8], xg[8];
+    xo[0] = *reinterpret_cast<const fp *>(po);
+    const SharedArgs::Unit u = args.units[unit];
+    if (row >= u.nq * kv.G || (!u.n_group && u.n_own == 1)) // none, or done already
         return;
-    Group gr;
-    const int gi = prefix_of(kv, args.pre, seq, sq, gr);
-    int per, n_own, n_group = 0;
-    split_tiles(o, range_tiles(o.bn, gr.len, min(sq.kv, sq.p0 + sq.nq)).n, per, n_own);
-    if (!gr.len && n_own == 1)
-        return; // done already
-    const int tok = kv.div_g(row), head = kv.div_g.rem(row, tok);
-    const size_t own = (size_t)unit * o.S * o.rows + row;
-    size_t pre = 0;
-    if (gr.len) {
-        split_tiles(g, range_tiles(g.bn, 0, gr.len).n, per, n_group);
-        const int r = (sq.t0 + tok - gr.t0) * kv.G + head, shift = __builtin_ctz(g.rows); // rows: a power of two
-        pre = ((size_t)(gi * g.row_blocks + (r >> shift)) * kv.Hk + hk) * g.S * g.rows + (r & (g.rows - 1));
-    }
+    const int r = u.row0 + row, shift = __builtin_ctz(g.rows); // rows: a power of two
+    const size_t pre = u.n_group ? ((size_t)(u.g * g.row_blocks + (r >> shift)) * kv.Hk + hk) * g.S * g.rows + (r & (g.rows - 1)) : 0;
+    const float *pg = g.part + pre * DP + PER * lane;
     // what no split wrote may be anything and is selected away
     const f2 none = {-INFINITY, 0.f};
-    const f2 so = lane < n_own ? *reinterpret_cast<const f2 *>(o.stat + (own + (size_t)lane * o.rows) * 2) : none;
-    const f2 sg = lane < n_group ? *reinterpret_cast<const f2 *>(g.stat + (pre + (size_t)lane * g.rows) * 2) : none;
-    float m = fmaxf(so.x, sg.x);
+    const f2 stg = lane < u.n_group ? *reinterpret_cast<const f2 *>(g.stat + (pre + (size_t)lane * g.rows) * 2) : none;
+    if (u.n_group)
+        first_partials(xg, pg, sg, u.n_group);
+    if (u.n_own > 1)
+        first_partials(xo, po, so, u.n_own);
+    const f2 sto = lane < u.n_own ? any : none;
+    float m = fmaxf(sto.x, stg.x);
 #pragma unroll
     for (int i = 32; i > 0; i >>= 1)
         m = fmaxf(m, __shfl_xor(m, i, 64));
-    const float fo = so.x == -INFINITY ? 0.f : fast_exp2(o.c * (so.x - m)), fg = sg.x == -INFINITY ? 0.f : fast_exp2(o.c * (sg.x - m));
-    float l = so.y * fo + sg.y * fg;
+    const float fo = sto.x == -INFINITY ? 0.f : fast_exp2(o.c * (sto.x - m)), fg = stg.x == -INFINITY ? 0.f : fast_exp2(o.c * (stg.x - m));
+    float l = sto.y * fo + stg.y * fg;
 #pragma unroll
     for (int i = 32; i > 0; i >>= 1)
         l += __shfl_xor(l, i, 64);
@@ -84,13 +97,18 @@ __global__ __launch_bounds__(256) void shared_join_kernel(SharedArgs args)
 #pragma unroll
     for (int i = 0; i < PER; i++)
         sum[i] = 0.f;
-    add_partials(sum, g.part + pre * DP + PER * lane, (size_t)g.rows * DP, n_group, fg);
-    add_partials(sum, o.part + own * DP + PER * lane, (size_t)o.rows * DP, n_own, fo);
+    if (u.n_group)
+        add_partials(sum, xg, pg, sg, u.n_group, fg);
+    if (u.n_own > 1)
+        add_partials(sum, xo, po, so, u.n_own, fo);
+    else
+        sum += xo[0] * __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(fo)));
     const int d = PER * lane;
     if (d >= kv.D)
         return;
     const float inv = l > 0.f ? 1.0f / l : 0.f; // a row that sees nothing is zero
-    const size_t at = ((size_t)(sq.t0 + tok) * kv.Hq + hk * kv.G + head) * kv.D + d;
+    const int tok = kv.div_g(row);
+    const size_t at = ((size_t)(u.t0 + tok) * kv.Hq + hk * kv.G + kv.div_g.rem(row, tok)) * kv.D + d;
     if (o.out_f32) {
         *reinterpret_cast<fp *>(static_cast<float *>(o.out) + at) = sum * inv;
     } else {
@@ -129,6 +147,7 @@ struct Plan {
     bool shared;     // else rfx_attn
     bool tall;       // the prefix on the prefill kernel
     Part group, own;
+    size_t units, bytes;
 };
 
 void sizes(Part &p, int dp)
@@ -137,18 +156,18 @@ void sizes(Part &p, int dp)
     p.stat = align256((size_t)p.units * p.S * p.rows * 2 * sizeof(float));
 }
 
-int splits(int64_t units, int64_t tiles, const Part &p)
+int splits(int64_t units, int64_t tiles, const Part &p, int places = 512)
 {
-    const int64_t want = 512 / (units < 512 ? units : 512), most = tiles <= p.one_tiles ? 1 : ceil_div(tiles, p.min_tiles);
+    const int64_t want = places / (units < places ? units : places), most = tiles <= p.one_tiles ? 1 : ceil_div(tiles, p.min_tiles);
     const int64_t s = want < most ? want : most;
     return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
 }
 
 // Sequences of more rows than the decode kernel takes are left to rfx_attn,
-// whose prefill tiles already have 128 rows of one sequence per key. A group
-// of up to kTallRows rows stays on the decode kernel, in the launch of the
-// sequences' own keys; more go to the prefill kernel.
-constexpr int kTallRows = 64;
+// whose prefill tiles already have 128 rows of one sequence per key. A prefix
+// of few rows and keys stays on the decode kernel, in the launch of the
+// sequences' own keys; larger ones go to the prefill kernel.
+constexpr int64_t kTall = 2 << 20;
 
 Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, int n_heads)
 {
@@ -159,7 +178,7 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, 
     p.shared = rows <= most;
     if (!p.shared)
         return p;
-    p.tall = all > kTallRows;
+    p.tall = all > 64 && all * P->max_len > kTall;
     p.own.rows = rows > 16 || (!p.tall && all > 16 && most > 16) ? 32 : 16;
     p.own.row_blocks = 1;
     p.own.bn = 32;
@@ -176,9 +195,13 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, 
     p.group.one_tiles = p.tall ? 4 : 8;
     p.group.cap_shift = 5;
     p.group.units = (int64_t)P->n_groups * C->n_kv_heads * p.group.row_blocks;
-    p.group.S = splits(p.group.units, ceil_div(P->max_len < room ? P->max_len : room, p.group.bn), p.group);
+    p.group.S = splits(p.group.units, ceil_div(P->max_len < room ? P->max_len : room, p.group.bn), p.group, p.tall ? 512 : 256);
+    const int cap = p.tall ? 16 : 32; // partials of more splits cost the join more than they save
+    p.group.S = p.group.S < cap ? p.group.S : cap;
     sizes(p.group, dp);
     sizes(p.own, dp);
+    p.units = align256((size_t)p.own.units * sizeof(SharedArgs::Unit));
+    p.bytes = p.group.part + p.group.stat + p.own.part + p.own.stat + p.units;
     return p;
 }
 
@@ -215,7 +238,7 @@ size_t rfx_attn_shared_workspace_bytes(const rfx_kv_cache *C, const rfx_kv_batch
         B->table_stride < 1 || !prefix_ok(P))
         return 0;
     const Plan p = plan(C, B, P, n_heads);
-    return p.shared ? p.group.part + p.group.stat + p.own.part + p.own.stat : rfx_attn_workspace_bytes(C, B, n_heads);
+    return p.shared ? p.bytes : rfx_attn_workspace_bytes(C, B, n_heads);
 }
 
 int rfx_attn_shared(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, int n_heads,
@@ -243,9 +266,8 @@ int rfx_attn_shared(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B,
     if (p.group.units * p.group.S + p.own.units * p.own.S >= (int64_t)kMaxTokens || p.own.units * (p.own.rows / 4) >= (int64_t)kMaxTokens)
         return fail(RFX_E_INVAL, "rfx_attn_shared: %d sequences in %d groups of up to %d new tokens need more than %d workgroups",
                     B->n_seq, P->n_groups, P->max_tokens, kMaxTokens);
-    const size_t need = p.group.part + p.group.stat + p.own.part + p.own.stat;
-    if (!ws || ws_bytes < need)
-        return fail(RFX_E_WORKSPACE, "rfx_attn_shared: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, need);
+    if (!ws || ws_bytes < p.bytes)
+        return fail(RFX_E_WORKSPACE, "rfx_attn_shared: workspace %zu < %zu bytes", ws ? ws_bytes : (size_t)0, p.bytes);
     if ((st = check_ptr(ws, 256, "ws")))
         return st;
     if (B->n_tokens == 0)
@@ -261,6 +283,7 @@ int rfx_attn_shared(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B,
     char *w = static_cast<char *>(ws);
     fill(a.group, p.group, w);
     fill(a.own, p.own, w);
+    a.units = reinterpret_cast<SharedArgs::Unit *>(w);
     a.group_blocks = (int)(p.group.units * p.group.S);
     const hipStream_t hs = (hipStream_t)stream;
     if (p.tall) {

@@ -105,6 +105,12 @@ struct SharedArgs {
     PrefixArgs pre;
     AttnArgs group, own;
     int group_blocks; // workgroups of `group` ahead of `own`'s
+    // What `own` leaves for the join, per unit: the sequence's first row and
+    // new tokens, splits of its own keys and of the prefix, the group and where
+    // the sequence's rows begin among the group's.
+    struct Unit {
+        int t0, nq, n_own, n_group, g, row0, pad[2];
+    } *units;
 };
 
 // The two-group prefill kernel: rows of a block, and the page ids that its
@@ -278,33 +284,57 @@ struct Group {
     int s0, t0, nt, len;
 };
 
-__device__ __forceinline__ Group load_group(const KvArgs &a, const PrefixArgs &pre, int g)
+// Group of the sequences s0 .. s1 - 1.
+__device__ __forceinline__ Group make_group(const KvArgs &a, const PrefixArgs &pre, int s0, int s1, int len)
 {
-    const int s0 = __builtin_amdgcn_readfirstlane(pre.seq_off[g]), s1 = __builtin_amdgcn_readfirstlane(pre.seq_off[g + 1]);
-    const int len = __builtin_amdgcn_readfirstlane(pre.len[g]);
-    Group r = {0, 0, 0, 0};
     if (s0 < 0 || s1 <= s0 || s1 > a.n_seq || len <= 0 || len > a.stride << a.page_shift)
-        return r;
+        return {0, 0, 0, 0};
     const int t0 = __builtin_amdgcn_readfirstlane(a.q_off[s0]), t1 = __builtin_amdgcn_readfirstlane(a.q_off[s1]);
     if (t0 < 0 || t1 <= t0 || t1 > a.n_tokens || t1 - t0 > pre.max_tokens)
-        return r;
+        return {0, 0, 0, 0};
     return {s0, t0, t1 - t0, len};
 }
 
-// The group whose prefix sequence s takes part in, -1 and len 0 where there
-// is none, where its new tokens begin inside the prefix, or where its rows are
-// not among the group's.
-__device__ __forceinline__ int prefix_of(const KvArgs &a, const PrefixArgs &pre, int s, const Seq &sq, Group &gr)
+__device__ __forceinline__ Group load_group(const KvArgs &a, const PrefixArgs &pre, int g)
 {
-    const int g = __builtin_amdgcn_readfirstlane(find_run(pre.seq_off, pre.n_groups, s));
+    const int s0 = __builtin_amdgcn_readfirstlane(pre.seq_off[g]), s1 = __builtin_amdgcn_readfirstlane(pre.seq_off[g + 1]);
+    return make_group(a, pre, s0, s1, __builtin_amdgcn_readfirstlane(pre.len[g]));
+}
+
+// Sequence s, and the group whose prefix it takes part in: -1 and len 0 where
+// there is none, where its new tokens begin inside the prefix, or where its
+// rows are not among the group's. Up to 64 groups are looked at beside the
+// sequence's own loads, one per lane.
+__device__ __forceinline__ Seq load_seq_prefix(const KvArgs &a, const PrefixArgs &pre, int s, int &g, Group &gr)
+{
+    const int lane = threadIdx.x & 63;
+    const bool few = pre.n_groups <= 64;
+    const int i = min(lane, pre.n_groups - 1);
+    int lo = 0, hi = 0, len = 0;
+    if (few) {
+        lo = pre.seq_off[i];
+        hi = pre.seq_off[i + 1];
+        len = pre.len[i];
+    }
+    const Seq sq = load_seq(a, s);
     gr = {0, 0, 0, 0};
-    if (g < 0)
-        return -1;
-    gr = load_group(a, pre, g);
+    if (few) {
+        const uint64_t in = __ballot(lane < pre.n_groups && lo <= s && s < hi);
+        g = in ? __builtin_ctzll(in) : -1;
+    } else {
+        g = __builtin_amdgcn_readfirstlane(find_run(pre.seq_off, pre.n_groups, s));
+    }
+    if (g < 0 || sq.nq <= 0) {
+        g = -1;
+        return sq;
+    }
+    gr = few ? make_group(a, pre, __builtin_amdgcn_readlane(lo, g), __builtin_amdgcn_readlane(hi, g), __builtin_amdgcn_readlane(len, g))
+             : load_group(a, pre, g);
     if (gr.len && sq.p0 >= gr.len && sq.t0 >= gr.t0 && sq.t0 + sq.nq <= gr.t0 + gr.nt)
-        return g;
+        return sq;
     gr.len = 0;
-    return -1;
+    g = -1;
+    return sq;
 }
 
 // The key tiles of bn keys that rows with first position p_lo and last

@@ -86,9 +86,10 @@ def check(groups, heads, kv_heads, dim, page, kind, out="f32", seed=0, scale=Non
     q = torch.randn((b.n_tokens, heads, dim), generator=g).to(TYPES[kind])
     scale = dim ** -0.5 if scale is None else scale
     o = run(b, q, scale, out, **(share or {}))
-    # one term a weight: a prefix of many rows, or rfx_attn's prompts
+    # one term a weight: a large prefix of many rows, or rfx_attn's prompts
     G = heads // kv_heads
-    compare(b, q, o, scale, out, out != "f32" and (b.most * G > 64 or b.max_q * G > 16))
+    rows, longest = (share or {}).get("max_tokens", b.most) * G, (share or {}).get("max_len", max(b.len))
+    compare(b, q, o, scale, out, out != "f32" and ((rows > 64 and rows * longest > 1 << 21) or b.max_q * G > 16))
     return b, q, o
 
 
@@ -119,6 +120,14 @@ CASES = [
 def test_groups(case, kind):
     check(*CASES[case], kind, seed=case, lead=case % 2, tail=case % 3, copies=case % 2 == 0)
     check(*CASES[case], kind, out="same", seed=100 + case)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("case", [c for c in range(len(CASES)) if c > 3])
+def test_groups_as_if_their_prefixes_were_long(case, kind):
+    """max_len says how long: with more than 64 rows the prefill kernel."""
+    for i, out in enumerate(("f32", "same")):
+        check(*CASES[case], kind, out=out, seed=200 + case, lead=i, share=dict(max_len=1 << 20))
 
 
 @pytest.mark.parametrize("heads,kv_heads", [(4, 1), (32, 2)])
