@@ -17,6 +17,8 @@
 // three that sum to the fp32 value, fp16 as two (the second 2^11 larger, with
 // sums of its own, so that it stays clear of fp16's subnormals), 2^-22 of the
 // value. Sums are fp32.
+#include <algorithm>
+
 #include "rfx_kv.h"
 
 using namespace rfx;
@@ -236,29 +238,57 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB)) void lora_down_ker
     }
 }
 
-// y = resid + c B v: a wave takes 16 tokens and RT tiles of 16 rows. KS: steps
-// of 32 over the rank. Where rows are few per wave, ADS adapters' tiles are
-// read at a time.
+// y = resid + c B v: a workgroup takes 16 tokens, whose v it adds up once in
+// LDS, a wave RT tiles of 16 rows. KS: steps of 32 over the rank. Where rows
+// are few per wave, ADS adapters' tiles are read at a time.
 template <class T, int KS, int RT, int ADS>
 __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
 {
     using X = Terms<T>;
+    constexpr int CH = 4 * KS;                       // chunks of eight ranks
+    constexpr int PARTS = kThreads / (16 * CH);      // threads that share the splits of a chunk
+    constexpr int VP = 32 * KS + 4;                  // pitch of a token's v
+    __shared__ __align__(16) float sv[PARTS][16][VP];
     const rfx_lora &l = a.l;
-    const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g4 = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t0 = blockIdx.y * 16, t = t0 + r16;
     int m = 0, rb = blockIdx.x;
     while (m + 1 < l.n_mats && rb >= a.row_blocks[m])
         rb -= a.row_blocks[m++];
     const rfx_lora_mat &M = l.mats[m];
     const int n0 = (rb * kWaves + wave) * 16 * RT;
-    if (n0 >= M.rows)
-        return;
     const int id = adapter_of(l, t);
     uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
-    if (!todo && M.resid == M.y)
+    const bool any = todo != 0; // the same in every wave
+    if (!any && M.resid == M.y)
         return;
 
+    // ADS adapters of those left: their rows of B, and who has them
+    bool live[ADS];
+    uint32_t keep[ADS];
+    u4 w[ADS][RT][KS];
+    const auto fetch = [&] {
+#pragma unroll
+        for (int j = 0; j < ADS; j++) {
+            live[j] = todo != 0;
+            if (!live[j])
+                continue;
+            const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
+            const bool match = id == ad;
+            todo &= ~(uint32_t)__ballot(match);
+            keep[j] = match ? ~0u : 0u;
+            const uint16_t *p = static_cast<const uint16_t *>(M.b) + (size_t)ad * M.rows * l.rank;
+#pragma unroll
+            for (int i = 0; i < RT; i++)
+#pragma unroll
+                for (int k = 0; k < KS; k++) {
+                    const int n = min(n0 + 16 * i + r16, M.rows - 1), r = 32 * k + 8 * g4;
+                    const u4 x = *reinterpret_cast<const u4 *>(p + (size_t)n * l.rank + (r < l.rank ? r : 0));
+                    w[j][i][k] = r < l.rank ? x : (u4){0, 0, 0, 0};
+                }
+        }
+    };
     f32x4 acc[RT][X::SUMS];
 #pragma unroll
     for (int i = 0; i < RT; i++)
@@ -266,22 +296,36 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
         for (int s = 0; s < X::SUMS; s++)
             acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float out = 1.0f;
-    if (todo) {
-        // the lane's part of its token's v: the splits in order, times the
-        // adapter's factor
-        const int RS = l.n_mats * a.R16;
-        float v[KS][8];
+    if (any) {
+        fetch();
         const float c = id >= 0 && M.scale ? M.scale[id] : 1.0f;
+        // the splits of v in order: every PARTS-th by one thread
+        {
+            const int RS = l.n_mats * a.R16, ch = tid % CH, tok = tid / CH % 16, part = tid / (16 * CH);
+            const bool on = 8 * ch < l.rank;
+            const float *p = a.v + (size_t)(t0 + tok) * RS + m * a.R16 + (on ? 8 * ch : 0);
+            const size_t stride = (size_t)a.T16 * RS;
+            f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+#pragma unroll 4
+            for (int s = part; s < a.splits; s += PARTS) {
+                s0 += *reinterpret_cast<const f32x4 *>(p + s * stride);
+                s1 += *reinterpret_cast<const f32x4 *>(p + s * stride + 4);
+            }
+            *reinterpret_cast<f32x4 *>(&sv[part][tok][8 * ch]) = s0;
+            *reinterpret_cast<f32x4 *>(&sv[part][tok][8 * ch + 4]) = s1;
+        }
+        __syncthreads();
+        // the lane's part of its token's v, times the adapter's factor
+        float v[KS][8];
 #pragma unroll
         for (int k = 0; k < KS; k++) {
             const int r = 32 * k + 8 * g4;
-            const bool on = id >= 0 && r < l.rank;
-            const float *p = a.v + (size_t)(on ? t : t0) * RS + m * a.R16 + (on ? r : 0);
-            f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
-#pragma unroll 4
-            for (int s = 0; s < a.splits; s++) {
-                s0 += *reinterpret_cast<const f32x4 *>(p + (size_t)s * a.T16 * RS);
-                s1 += *reinterpret_cast<const f32x4 *>(p + (size_t)s * a.T16 * RS + 4);
+            const bool on = id >= 0 && r < l.rank; // what no one wrote may be anything
+            f32x4 s0 = *reinterpret_cast<const f32x4 *>(&sv[0][r16][r]), s1 = *reinterpret_cast<const f32x4 *>(&sv[0][r16][r + 4]);
+#pragma unroll
+            for (int q = 1; q < PARTS; q++) {
+                s0 += *reinterpret_cast<const f32x4 *>(&sv[q][r16][r]);
+                s1 += *reinterpret_cast<const f32x4 *>(&sv[q][r16][r + 4]);
             }
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -311,31 +355,11 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
 #pragma unroll
         for (int k = 0; k < KS; k++)
             X::split(v[k], vt[k]);
-
-        int ad = 0;
-        while (todo) {
-            uint32_t keep[ADS];
-            u4 w[ADS][RT][KS];
+        for (;;) {
 #pragma unroll
             for (int j = 0; j < ADS; j++) {
-                const bool more = todo != 0;
-                if (more)
-                    ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-                const bool match = more & (id == ad); // none left: the last one's again, for nobody
-                todo &= ~(uint32_t)__ballot(match);
-                keep[j] = match ? ~0u : 0u;
-                const uint16_t *p = static_cast<const uint16_t *>(M.b) + (size_t)ad * M.rows * l.rank;
-#pragma unroll
-                for (int i = 0; i < RT; i++)
-#pragma unroll
-                    for (int k = 0; k < KS; k++) {
-                        const int n = min(n0 + 16 * i + r16, M.rows - 1), r = 32 * k + 8 * g4;
-                        const u4 x = *reinterpret_cast<const u4 *>(p + (size_t)n * l.rank + (r < l.rank ? r : 0));
-                        w[j][i][k] = r < l.rank ? x : (u4){0, 0, 0, 0};
-                    }
-            }
-#pragma unroll
-            for (int j = 0; j < ADS; j++)
+                if (!live[j])
+                    continue;
 #pragma unroll
                 for (int k = 0; k < KS; k++) {
                     u4 tm[X::N];
@@ -348,6 +372,10 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
                         for (int i = 0; i < RT; i++)
                             X::mma(s, w[j][i][k], tm, acc[i]);
                 }
+            }
+            if (!todo)
+                break;
+            fetch();
         }
     }
     // lane: token r16, rows 4 g4 .. + 3 of tile i
@@ -394,10 +422,13 @@ Plan plan(int T, int rank, int n_mats, int cols, int n_adapters)
     p.slots = p.slots < T ? p.slots : T;
     p.slots = p.slots < n_adapters ? p.slots : n_adapters;
     // Columns split until there is a workgroup for every place, down to a step
-    // of 64 columns per wave.
-    const int waves = down_waves(p.tiles < 8 ? p.tiles : 8, p.wide ? 2 : 1), want = 256 * waves / (blocks * p.groups), most = (cols + 255) / 256;
-    p.splits = want < most ? want : most;
-    p.splits = p.splits < 1 ? 1 : p.splits > kMaxSplits ? kMaxSplits : p.splits;
+    // of 64 columns per wave. Few tokens: for every adapter's place, since the
+    // second launch reads v once per split: 64 tokens, 48 adapters of rank 64, 18
+    // us with four splits and 24 with sixteen; one token 8.5 with sixteen and 10.0
+    // with four.
+    const int waves = down_waves(p.tiles < 8 ? p.tiles : 8, p.wide ? 2 : 1), most = (cols + 255) / 256;
+    const int want = T <= 128 ? std::max(4, 256 / (blocks * p.slots * p.groups)) : 256 * waves / (blocks * p.groups);
+    p.splits = std::max(1, std::min({want, most, kMaxSplits}));
     p.bytes = (size_t)p.splits * p.T16 * n_mats * p.R16 * sizeof(float);
     return p;
 }

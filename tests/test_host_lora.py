@@ -50,8 +50,8 @@ def test_workspace_sizes():
     assert need(1, 16, 1, 64, 4) > 0 and need(100, 16, 3, 64, 4) > need(100, 16, 1, 64, 4)
     for bad in ((-1, 16, 1, 64, 4), (1, 12, 1, 64, 4), (1, 16, 5, 64, 4), (1, 16, 1, 40, 4), (1, 16, 1, 64, 0)):
         assert need(*bad) == 0
-    # every split of up to 16 parts has the padded tokens' sums
-    assert need(17, 40, 2, 4096, 4) == 16 * 32 * 2 * 48 * 4
+    # a split has the padded tokens' sums: 17 tokens in 32, ranks of 40 in 48
+    assert need(17, 40, 2, 256, 4) == 32 * 2 * 48 * 4 and need(17, 40, 2, 4096, 4) % need(17, 40, 2, 256, 4) == 0
 
 
 def test_binding_checks_tensors():
