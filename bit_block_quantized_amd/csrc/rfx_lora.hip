@@ -91,20 +91,24 @@ __device__ __forceinline__ int adapter_of(const rfx_lora &l, int t)
 // adapter of its tokens, against TILES of the 16-row tiles of all matrices,
 // which stand one after the other. 64 columns at a time, so that a row's 128
 // bytes are read together, with the next ones' loads in flight.
-// The registers of six tiles and more of 32 tokens leave one wave per SIMD.
-constexpr int down_waves(int tiles, int nb) { return tiles * nb > 8 ? 1 : 2; }
+// Waves per SIMD that the registers leave room for.
+constexpr int down_waves(int tiles, int nb, int sums) { return tiles * nb * (2 + sums) > 36 || (sums > 1 && tiles > 6) ? 1 : 2; }
 
 template <class T, int TILES, int NB>
-__global__ __launch_bounds__(kThreads, down_waves(TILES, NB)) void lora_down_kernel(LoraArgs a)
+__global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) void lora_down_kernel(LoraArgs a)
 {
     using X = Terms<T>;
     constexpr int SUMS = TILES * NB > 4 ? 4 : TILES * NB; // tiles in LDS at a time
-    __shared__ __align__(16) f32x4 sums[kWaves][SUMS][64];
+    constexpr int XP = 128 + 16, WP = 64 + 16;            // pitches of 32 columns of x and of A
+    constexpr int PIECE = NB > 1 ? 16 * NB * XP + 16 * TILES * WP : 0, LDS = PIECE > SUMS * 1024 ? PIECE : SUMS * 1024;
+    __shared__ __align__(16) char smem[kWaves * LDS];
+    auto &sums = *reinterpret_cast<f32x4 (*)[kWaves][SUMS][64]>(smem);
     const rfx_lora &l = a.l;
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Workgroups go round the eight XCDs in order: a contiguous run of them to
     // each, so that its L2 keeps the few adapters of its tokens.
+    [[maybe_unused]] char *piece = smem + wave * LDS;
     int b = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;
     if (b >= a.down)
         return;
@@ -112,7 +116,7 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB)) void lora_down_ker
     b /= a.splits;
     const int tile0 = b % a.groups * TILES;
     b /= a.groups;
-    const int slot = b % a.slots, t0 = b / a.slots * 16 * NB;
+    const int blocks = a.T16 / (16 * NB), slot = b / blocks, t0 = (b - slot * blocks) * 16 * NB;
     const int steps = (l.cols + 63) / 64, part = a.splits * kWaves, p = split * kWaves + wave;
     const int k0 = (int)((int64_t)steps * p / part), k1 = (int)((int64_t)steps * (p + 1) / part);
 
@@ -148,71 +152,149 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB)) void lora_down_ker
             todo &= ~(((uint32_t)__ballot(match) & 0xffffu) << 16 * n);
             mine[n] |= match & own;
             keep[n] = match ? ~0u : 0u;
-            // lanes of other adapters' tokens read along with the first one's
+            // (few tokens) lanes of other adapters' tokens read along with the first one's
             x[n] = l.x + (int64_t)(t0 + (match ? 16 * n + r16 : first)) * l.x_stride + 8 * g4;
         }
         if (!own || k0 >= k1)
             continue;
-        const uint16_t *w[TILES];
+        if constexpr (NB == 1) {
+            const uint16_t *w[TILES];
 #pragma unroll
-        for (int i = 0; i < TILES; i++) {
-            const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + r16, l.rank - 1);
-            w[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * g4;
-        }
-        struct Step {
-            f32x4 x[2][NB][2];
-            u4 w[TILES][2];
-        } s0, s1;
-        const auto load = [&](Step &s, int k) { // columns past the last: the step's first half again
-            const size_t at = 64 * (size_t)min(k, k1 - 1), up = at + 32 < (size_t)l.cols ? 32 : 0;
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int n = 0; n < NB; n++)
-#pragma unroll
-                    for (int q = 0; q < 2; q++)
-                        s.x[h][n][q] = *reinterpret_cast<const f32x4 *>(x[n] + at + h * up + 4 * q);
-#pragma unroll
-            for (int i = 0; i < TILES; i++)
+            for (int i = 0; i < TILES; i++) {
+                const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + r16, l.rank - 1);
+                w[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * g4;
+            }
+            struct Step {
+                f32x4 x[2][NB][2];
+                u4 w[TILES][2];
+            } s0, s1;
+            const auto load = [&](Step &s, int k) { // columns past the last: the step's first half again
+                const size_t at = 64 * (size_t)min(k, k1 - 1), up = at + 32 < (size_t)l.cols ? 32 : 0;
 #pragma unroll
                 for (int h = 0; h < 2; h++)
-                    s.w[i][h] = *reinterpret_cast<const u4 *>(w[i] + at + h * up);
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        const auto compute = [&](const Step &s, int k) {
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t in = 64 * k + 32 * h < l.cols ? ~0u : 0u;
+                    for (int n = 0; n < NB; n++)
+#pragma unroll
+                        for (int q = 0; q < 2; q++)
+                            s.x[h][n][q] = *reinterpret_cast<const f32x4 *>(x[n] + at + h * up + 4 * q);
+#pragma unroll
+                for (int i = 0; i < TILES; i++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+                        s.w[i][h] = *reinterpret_cast<const u4 *>(w[i] + at + h * up);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            const auto compute = [&](const Step &s, int k) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const uint32_t in = 64 * k + 32 * h < l.cols ? ~0u : 0u;
+#pragma unroll
+                    for (int n = 0; n < NB; n++) {
+                        float xc[8];
+                        u4 t[X::N];
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            xc[e] = s.x[h][n][e >> 2][e & 3] * X::IN;
+                        X::split(xc, t);
+#pragma unroll
+                        for (int q = 0; q < X::N; q++)
+                            t[q] &= keep[n] & in;
+#pragma unroll
+                        for (int q = 0; q < X::N; q++) // neighbours do not depend on one another
+#pragma unroll
+                            for (int j = 0; j < TILES; j++)
+                                X::mma(q, s.w[j][h], t, acc[n][j]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            load(s0, k0);
+            for (int k = k0; k < k1; k += 2) {
+                load(s1, k + 1);
+                compute(s0, k);
+                if (k + 1 == k1)
+                    break;
+                load(s0, k + 2);
+                compute(s1, k + 1);
+            }
+        } else {
+            // 32 columns at a time through the wave's own piece of LDS: a load
+            // whose 16 lanes of a quarter read 16 rows takes the cycles of
+            // sixteen, one that reads whole lines of two (x) or four (A) rows
+            // those of as many.
+            const int first_k = 2 * k0, last_k = min(2 * k1, l.cols / 32);
+            const float *px[2 * NB];
+#pragma unroll
+            for (int j = 0; j < 2 * NB; j++)
+                px[j] = l.x + (int64_t)min(t0 + 8 * j + (lane >> 3), l.n_tokens - 1) * l.x_stride + 4 * (lane & 7);
+            const uint16_t *pw[TILES];
+#pragma unroll
+            for (int i = 0; i < TILES; i++) {
+                const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + (lane >> 2), l.rank - 1);
+                pw[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * (lane & 3);
+            }
+            constexpr int AHEAD = 2; // steps in flight
+            f32x4 xn[AHEAD][2 * NB];
+            u4 wn[AHEAD][TILES];
+            const auto load = [&](int u, int k) {
+                const int at = 32 * min(k, last_k - 1);
+#pragma unroll
+                for (int j = 0; j < 2 * NB; j++)
+                    xn[u][j] = *reinterpret_cast<const f32x4 *>(px[j] + at);
+#pragma unroll
+                for (int i = 0; i < TILES; i++)
+                    wn[u][i] = *reinterpret_cast<const u4 *>(pw[i] + at);
+            };
+            const auto step = [&](int u, int k) {
+#pragma unroll
+                for (int j = 0; j < 2 * NB; j++)
+                    *reinterpret_cast<f32x4 *>(piece + (8 * j + (lane >> 3)) * XP + 16 * (lane & 7)) = xn[u][j];
+#pragma unroll
+                for (int i = 0; i < TILES; i++)
+                    *reinterpret_cast<u4 *>(piece + 16 * NB * XP + (16 * i + (lane >> 2)) * WP + 16 * (lane & 3)) = wn[u][i];
+                load(u, k + AHEAD);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                u4 w[TILES];
+#pragma unroll
+                for (int i = 0; i < TILES; i++)
+                    w[i] = *reinterpret_cast<const u4 *>(piece + 16 * NB * XP + (16 * i + r16) * WP + 16 * g4);
 #pragma unroll
                 for (int n = 0; n < NB; n++) {
+                    const char *p = piece + (16 * n + r16) * XP + 32 * g4;
+                    const f32x4 x0 = *reinterpret_cast<const f32x4 *>(p), x1 = *reinterpret_cast<const f32x4 *>(p + 16);
                     float xc[8];
                     u4 t[X::N];
 #pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        xc[e] = s.x[h][n][e >> 2][e & 3] * X::IN;
+                    for (int e = 0; e < 4; e++) {
+                        xc[e] = x0[e] * X::IN;
+                        xc[e + 4] = x1[e] * X::IN;
+                    }
                     X::split(xc, t);
 #pragma unroll
                     for (int q = 0; q < X::N; q++)
-                        t[q] &= keep[n] & in;
+                        t[q] &= keep[n];
 #pragma unroll
-                    for (int q = 0; q < X::N; q++) // neighbours do not depend on one another
+                    for (int q = 0; q < X::N; q++)
 #pragma unroll
-                        for (int j = 0; j < TILES; j++)
-                            X::mma(q, s.w[j][h], t, acc[n][j]);
+                        for (int i = 0; i < TILES; i++)
+                            X::mma(q, w[i], t, acc[n][i]);
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        load(s0, k0);
-        for (int k = k0; k < k1; k += 2) {
-            load(s1, k + 1);
-            compute(s0, k);
-            if (k + 1 == k1)
-                break;
-            load(s0, k + 2);
-            compute(s1, k + 1);
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            };
+#pragma unroll
+            for (int u = 0; u < AHEAD; u++)
+                load(u, first_k + u);
+            for (int k = first_k; k < last_k; k += AHEAD)
+#pragma unroll
+                for (int u = 0; u < AHEAD; u++)
+                    if (k + u < last_k)
+                        step(u, k + u);
         }
     }
+    if (NB > 1 && any)
+        __syncthreads(); // the pieces become the sums
     if (!any) // the same in every wave
         return;
     // lane: token r16 of its sixteen, rows 4 g4 .. + 3 of tile i
@@ -408,17 +490,19 @@ struct Plan {
 };
 
 Plan plan(int T, int rank, int n_mats, int cols, int n_adapters)
-{
+{ // the same for both types: a workspace may serve either
     Plan p{};
     p.R16 = (rank + 15) / 16 * 16;
     p.tiles = n_mats * p.R16 / 16;
     p.groups = (p.tiles + 7) / 8;
-    p.wide = T > 512;
+    // 300 tokens of two prompts 18.0 us with 32 a workgroup and 22.0 with 16, 400
+    // 20.6 and 27.0; 200 tokens of 64 requests 16.9 and 15.2.
+    p.wide = T > 256;
     const int per = p.wide ? 32 : 16, blocks = T > per ? (T + per - 1) / per : 1;
     p.T16 = blocks * per;
     // Adapters of a block of tokens: side by side where tokens are few and
     // may each have their own, one after the other where they are many.
-    p.slots = T <= 128 ? 16 : T <= 512 ? 4 : 1;
+    p.slots = T <= 128 ? 16 : T <= 256 ? 4 : 1;
     p.slots = p.slots < T ? p.slots : T;
     p.slots = p.slots < n_adapters ? p.slots : n_adapters;
     // Columns split until there is a workgroup for every place, down to a step
@@ -426,7 +510,7 @@ Plan plan(int T, int rank, int n_mats, int cols, int n_adapters)
     // second launch reads v once per split: 64 tokens, 48 adapters of rank 64, 18
     // us with four splits and 24 with sixteen; one token 8.5 with sixteen and 10.0
     // with four.
-    const int waves = down_waves(p.tiles < 8 ? p.tiles : 8, p.wide ? 2 : 1), most = (cols + 255) / 256;
+    const int waves = down_waves(p.tiles < 8 ? p.tiles : 8, p.wide ? 2 : 1, 1), most = (cols + 255) / 256;
     const int want = T <= 128 ? std::max(4, 256 / (blocks * p.slots * p.groups)) : 256 * waves / (blocks * p.groups);
     p.splits = std::max(1, std::min({want, most, kMaxSplits}));
     p.bytes = (size_t)p.splits * p.T16 * n_mats * p.R16 * sizeof(float);
@@ -475,10 +559,10 @@ void launch_up_rank(LoraArgs &a, bool many, hipStream_t st)
 {
     int blocks = 0;
     for (int m = 0; m < a.l.n_mats; m++)
-        blocks += a.row_blocks[m] = (int)ceil_div(a.l.mats[m].rows, (many ? 64 : 16) * kWaves);
+        blocks += a.row_blocks[m] = (int)ceil_div(a.l.mats[m].rows, (many ? 32 : 16) * kWaves);
     const dim3 grid(blocks, a.T16 / 16), block(kThreads);
     if (many)
-        hipLaunchKernelGGL((lora_up_kernel<T, KS, 4, 1>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((lora_up_kernel<T, KS, 2, 1>), grid, block, 0, st, a);
     else
         hipLaunchKernelGGL((lora_up_kernel<T, KS, 1, 16 / KS>), grid, block, 0, st, a);
 }
