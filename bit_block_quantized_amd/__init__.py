@@ -892,6 +892,6 @@ class LogprobBuffers:
         return self
 
 
-from .layer import (AttentionBuffers, DeviceAttention, DeviceMoeLayer, MoeBuffers, PlacedMoeLayer,  # noqa: E402,F401
-                    hot_experts_by_frequency)
+from .layer import (AttentionBuffers, DeviceAttention, DeviceHead, DeviceMoeLayer, HeadBuffers, MoeBuffers,  # noqa: E402,F401
+                    PlacedMoeLayer, hot_experts_by_frequency)
 from . import layer  # noqa: E402,F401

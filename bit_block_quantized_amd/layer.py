@@ -188,10 +188,11 @@ Q_PROJ, K_PROJ, V_PROJ, O_PROJ = 0, 1, 2, 3
 class DeviceAttention:
     """The attention half of a decoder layer on the GPU: packed query, key,
     value and output projections, optional per-head norm weights of queries
-    and keys, rotary frequencies, and the mask's window and sinks."""
+    and keys, rotary frequencies, and the mask's window and sinks; in_norm:
+    the weight (float32 [hidden]) of an RMS norm of the layer's input."""
 
     def __init__(self, wq, wk, wv, wo, n_heads, n_kv_heads, head_dim, inv_freq, q_norm=None, k_norm=None, eps=1e-6,
-                 interleaved=False, window=0, sinks=0, scale=None):
+                 interleaved=False, window=0, sinks=0, scale=None, in_norm=None):
         if n_kv_heads < 1 or n_heads < 1 or n_heads % n_kv_heads:
             raise ValueError(f"{n_heads} heads over {n_kv_heads} kv heads")
         if window < 0 or sinks < 0 or not eps >= 0 or not (scale is None or scale > 0):
@@ -204,15 +205,16 @@ class DeviceAttention:
         if wo.rows != wq.cols or wo.cols != n_heads * head_dim:
             raise ValueError(f"wo: {wo.rows} x {wo.cols}, {wq.cols} x {n_heads * head_dim} wanted")
         self.hidden = wq.cols
-        self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
+        self.inv_freq, self.q_norm, self.k_norm, self.in_norm = inv_freq, q_norm, k_norm, in_norm
         self.eps, self.interleaved, self.window, self.sinks = eps, interleaved, window, sinks
         self.scale = head_dim ** -0.5 if scale is None else scale
 
     @classmethod
     def build(cls, hidden, n_heads, n_kv_heads, head_dim, weight_fn, fmt=FP4, rot_dim=None, base=10000.0, q_norm=None,
-              k_norm=None, device="cuda", **kw):
+              k_norm=None, device="cuda", in_norm=None, **kw):
         """weight_fn(mat, rows, cols) -> fp32 [rows][cols]; mat is 0 query, 1
-        key, 2 value, 3 output. q_norm, k_norm: fp32 [head_dim] or None."""
+        key, 2 value, 3 output. q_norm, k_norm: fp32 [head_dim] or None;
+        in_norm: fp32 [hidden] or None."""
         import torch
 
         from . import rope_inv_freq
@@ -226,18 +228,19 @@ class DeviceAttention:
         inv = torch.from_numpy(rope_inv_freq(head_dim if rot_dim is None else rot_dim, base)).to(device)
         return cls(proj(Q_PROJ, n_heads * head_dim, hidden), proj(K_PROJ, n_kv_heads * head_dim, hidden),
                    proj(V_PROJ, n_kv_heads * head_dim, hidden), proj(O_PROJ, hidden, n_heads * head_dim), n_heads,
-                   n_kv_heads, head_dim, inv, up(q_norm), up(k_norm), **kw)
+                   n_kv_heads, head_dim, inv, up(q_norm), up(k_norm), in_norm=up(in_norm), **kw)
 
 
 class AttentionBuffers:
     """Device buffers for attention calls over batches of this shape
     (n_tokens, max_q, sequences and page-table width as `batch` has them),
-    for any layer with this one's formats and sizes."""
+    for any layer with this one's formats and sizes. prefix, loras: also for
+    calls with such shared prefixes (KVPrefix) and such adapters."""
 
-    def __init__(self, attn: DeviceAttention, cache, batch, device="cuda"):
+    def __init__(self, attn: DeviceAttention, cache, batch, device="cuda", prefix=None, loras=None):
         import torch
 
-        from . import attn_workspace_bytes, gemm_workspace_bytes, gemv_grouped_workspace_bytes
+        from . import gemm_workspace_bytes, gemv_grouped_workspace_bytes
         T, D, H = batch.n_tokens, attn.head_dim, attn.hidden
         O = attn.n_heads * D
 
@@ -257,14 +260,35 @@ class AttentionBuffers:
         with torch.inference_mode(False): # run clears o, inside such a mode or not
             self.o = empty(T, attn.n_heads, D)
         self.y = empty(T, H)
+        self.xn = empty(T, H) if attn.in_norm is not None and loras else None # the adapters' input
         mats = (attn.wq, attn.wk, attn.wv, attn.wo)
         self.ws_gemm = zeros(max(gemm_workspace_bytes(W, T) for W in mats))
-        self.ws_attn = zeros(attn_workspace_bytes(cache, batch, attn.n_heads))
+        self.ws_attn = zeros(max(self._attention_bytes(attn, cache, batch, p) for p in (None, prefix)))
+        self.ws_lora = zeros(self._lora_bytes(loras, T))
         self.ws_jobs = zeros(gemv_grouped_workspace_bytes(self._jobs(attn))) if T <= 4 else None
 
     @staticmethod
     def _sizes(attn):
         return attn.hidden, attn.n_heads, attn.n_kv_heads, attn.head_dim
+
+    @staticmethod
+    def _attention_bytes(attn, cache, batch, prefix):
+        from . import attn_shared_workspace_bytes, attn_workspace_bytes
+        if prefix is None:
+            return attn_workspace_bytes(cache, batch, attn.n_heads)
+        return attn_shared_workspace_bytes(cache, batch, prefix, attn.n_heads)
+
+    @staticmethod
+    def _lora_calls(loras):
+        """Adapters that share a call: those of the input's projections, and
+        the output's."""
+        both = [m for m in loras[:O_PROJ] if m is not None], [m for m in loras[O_PROJ:] if m is not None]
+        return [c for c in both if c]
+
+    @classmethod
+    def _lora_bytes(cls, loras, T):
+        from . import lora_workspace_bytes
+        return max((lora_workspace_bytes(c, T) for c in cls._lora_calls(loras)), default=0) if loras else 0
 
     def _jobs(self, attn):
         """Decode's query, key and value projections, one launch."""
@@ -272,28 +296,49 @@ class AttentionBuffers:
         return gemv_jobs([(W, self.q.shape[0], *self.x_act, y)
                           for W, y in zip((attn.wq, attn.wk, attn.wv), (self.q, self.k, self.v))])
 
-    def run(self, attn: DeviceAttention, x, cache, batch, resid=None, out=None, stream=None):
+    def run(self, attn: DeviceAttention, x, cache, batch, resid=None, out=None, stream=None, prefix=None, loras=None,
+            ids=None):
         """Projections, norm, rotation and cache append, attention, output
         projection for x (device fp32 [n_tokens][hidden]); y = resid +
-        Attention(x) lands in `out` (default self.y). Rows that attention
-        leaves (of no sequence, of a skipped one, past max_q) have Attention(x)
-        = 0. What does not fit these buffers is refused before anything is
-        launched."""
+        Attention(x) lands in `out` (default self.y), Attention beginning with
+        the layer's in_norm where it has one. Rows that attention leaves (of no
+        sequence, of a skipped one, past max_q) have Attention(x) = 0. prefix:
+        a KVPrefix of the batch's sequences, read once per group. loras: the
+        low-rank adapters of the query, key, value and output projections (four
+        DeviceLora or None), ids int32 [n_tokens] the one of each token. What
+        does not fit these buffers is refused before anything is launched."""
         from . import _torch
         t, dev = _torch(), cache.index
         y = self.y if out is None else out
         jobs = self._jobs(attn) if batch.n_tokens <= 4 else None
-        self._check(attn, x, cache, batch, resid, y, jobs)
+        self._check(attn, x, cache, batch, resid, y, jobs, prefix, loras, ids)
+        more = prefix, loras, ids
         if dev >= 0 and t.current_device() != dev:
             with t.device_guard(dev):
-                return self._run(attn, x, cache, batch, resid, y, jobs, stream)
-        return self._run(attn, x, cache, batch, resid, y, jobs, stream)
+                return self._run(attn, x, cache, batch, resid, y, jobs, stream, *more)
+        return self._run(attn, x, cache, batch, resid, y, jobs, stream, *more)
 
-    def _check(self, attn, x, cache, batch, resid, y, jobs):
+    def _check_loras(self, attn, loras, ids, T, dev):
+        from . import _torch, _want
+        mats = attn.wq, attn.wk, attn.wv, attn.wo
+        if len(loras) != 4 or not any(m is not None for m in loras):
+            raise ValueError("loras: four adapters, of the query, key, value and output projections, None for those without")
+        for m, W, name in zip(loras, mats, ("query", "key", "value", "output")):
+            if m is not None and ((m.cols, m.rows) != (W.cols, W.rows) or m.index != dev):
+                raise ValueError(f"{name} adapters: {m.rows} x {m.cols} on GPU {m.index}, {W.rows} x {W.cols} on GPU {dev} wanted")
+        for call in self._lora_calls(loras):
+            if any(m.kind != call[0].kind for m in call):
+                raise ValueError(f"adapters of one input: (type, number, rank, cols) {[m.kind for m in call]}, one for all wanted")
+        if ids is None:
+            raise ValueError("adapters without ids")
+        _want(ids, "ids", _torch().i32, (T,), dev)
+        if attn.in_norm is not None and self.xn is None and any(m is not None for m in loras[:O_PROJ]):
+            raise ValueError("buffers made without adapters have no room for their input")
+
+    def _check(self, attn, x, cache, batch, resid, y, jobs, prefix, loras, ids):
         """The projections do not know how large their results' buffers are,
         and the append changes the cache: everything is looked at first."""
-        from . import (_torch, _want, _want_vec, attn_workspace_bytes, gemm_workspace_bytes,
-                       gemv_grouped_workspace_bytes)
+        from . import _torch, _want, _want_vec, gemm_workspace_bytes, gemv_grouped_workspace_bytes
         t, T, dev = _torch(), batch.n_tokens, cache.index
         if self.q.shape[0] != T:
             raise ValueError(f"buffers for {self.q.shape[0]} tokens, the batch has {T}")
@@ -313,24 +358,39 @@ class AttentionBuffers:
         _want_vec(attn.inv_freq, "inv_freq", t.f64, attn.inv_freq.numel(), dev)
         _want_vec(attn.q_norm, "q_norm", t.f32, attn.head_dim, dev)
         _want_vec(attn.k_norm, "k_norm", t.f32, attn.head_dim, dev)
+        _want_vec(attn.in_norm, "in_norm", t.f32, attn.hidden, dev)
+        if prefix is not None and (attn.window or prefix.index != dev):
+            raise ValueError(f"a shared prefix on GPU {prefix.index} with window {attn.window}: GPU {dev}, no window wanted")
+        if loras:
+            self._check_loras(attn, loras, ids, T, dev)
         mats = (attn.wo,) if T <= 4 else (attn.wq, attn.wk, attn.wv, attn.wo)
-        for name, ws, need in (("attention", self.ws_attn, attn_workspace_bytes(cache, batch, attn.n_heads)),
+        for name, ws, need in (("attention", self.ws_attn, self._attention_bytes(attn, cache, batch, prefix)),
+                               ("adapters", self.ws_lora, self._lora_bytes(loras, T)),
                                ("projections", self.ws_gemm, max(gemm_workspace_bytes(W, T) for W in mats)),
                                ("projections", self.ws_jobs, 0 if jobs is None else gemv_grouped_workspace_bytes(jobs))):
             if need > (0 if ws is None else ws.nbytes):
                 raise ValueError(f"buffers have {0 if ws is None else ws.nbytes} bytes of workspace for the {name}, {need} wanted")
 
-    def _run(self, attn, x, cache, batch, resid, y, jobs, stream):
+    def _run(self, attn, x, cache, batch, resid, y, jobs, stream, prefix, loras, ids):
         from . import _torch
         from . import attn as attention
-        from . import gemm, gemv_grouped, qk_norm_rope, quantize_act
+        from . import add_rms_norm, attn_shared, gemm, gemv_grouped, lora, qk_norm_rope, quantize_act
         T = batch.n_tokens
-        quantize_act(x, *self.x_act, stream)
+        flat = [o.view(T, -1) for o in (self.q, self.k, self.v)]
+        some = [(m, o) for m, o in zip(loras[:O_PROJ], flat) if m is not None] if loras else []
+        xn = x
+        if attn.in_norm is None:
+            quantize_act(x, *self.x_act, stream)
+        else:
+            xn = self.xn if some else None
+            add_rms_norm(x, attn.in_norm, attn.eps, None, None, xn, *self.x_act, stream)
         if jobs is not None:
             gemv_grouped(jobs, self.ws_jobs, stream)
         else:
             for W, o in ((attn.wq, self.q), (attn.wk, self.k), (attn.wv, self.v)):
                 gemm(W, *self.x_act, T, o, ws=self.ws_gemm, stream=stream)
+        if some:
+            lora(xn, ids, [m for m, _ in some], [o for _, o in some], ws=self.ws_lora, stream=stream)
         qk_norm_rope(self.q, self.k, self.v, cache, batch, self.q16, attn.inv_freq, attn.q_norm, attn.k_norm, attn.eps,
                      attn.interleaved, stream)
         # the rows that attention leaves must not carry an earlier call's on
@@ -339,7 +399,80 @@ class AttentionBuffers:
         else:
             with _torch().on_stream(stream):
                 self.o.zero_()
-        attention(self.q16, cache, batch, self.o, attn.scale, attn.window, attn.sinks, self.ws_attn, stream)
-        quantize_act(self.o.view(T, -1), *self.o_act, stream)
+        if prefix is None:
+            attention(self.q16, cache, batch, self.o, attn.scale, attn.window, attn.sinks, self.ws_attn, stream)
+        else:
+            attn_shared(self.q16, cache, batch, prefix, self.o, attn.scale, self.ws_attn, stream)
+        o = self.o.view(T, -1)
+        quantize_act(o, *self.o_act, stream)
         gemm(attn.wo, *self.o_act, T, y, resid=resid, ws=self.ws_gemm, stream=stream)
+        if loras and loras[O_PROJ] is not None:
+            lora(o, ids, [loras[O_PROJ]], [y], ws=self.ws_lora, stream=stream)
         return y
+
+
+class DeviceHead:
+    """The head on the GPU: a packed projection to the vocabulary behind an
+    optional RMS norm (float32 [hidden])."""
+
+    def __init__(self, w, norm=None, eps=1e-6):
+        if not eps >= 0:
+            raise ValueError(f"eps {eps}")
+        self.w, self.norm, self.eps = w, norm, eps
+        self.hidden, self.n_vocab = w.cols, w.rows
+
+    @classmethod
+    def build(cls, n_vocab, hidden, weight, fmt=FP4, norm=None, eps=1e-6, device="cuda"):
+        """weight: fp32 [n_vocab][hidden]; norm: fp32 [hidden] or None."""
+        import torch
+        if norm is not None:
+            norm = torch.from_numpy(np.ascontiguousarray(norm, np.float32)).to(device)
+        return cls(DeviceQMat.from_host(fmt, n_vocab, hidden, quantize_matrix(fmt, weight), device=device), norm, eps)
+
+
+class HeadBuffers:
+    """Device buffers for q rows through a head: logits [q][n_vocab] and what
+    they say of the rows (probs: a LogprobBuffers with top_k alternatives)."""
+
+    def __init__(self, head: DeviceHead, q: int, top_k: int = 0, device="cuda"):
+        import torch
+
+        from . import LogprobBuffers, gemm_workspace_bytes
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.q, H = q, head.hidden
+        self.probs = LogprobBuffers(q, head.n_vocab, top_k, device)
+        self.x_act = empty(q, H, dtype=torch.int8), empty(q, H // 32), empty(q, H // 32, dtype=torch.int32)
+        self.logits = empty(q, head.n_vocab)
+        n = gemm_workspace_bytes(head.w, q)
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=device) if n else None
+
+    def run(self, head: DeviceHead, x, tokens=None, stream=None):
+        """Norm, projection and log probabilities for x (device fp32
+        [q][hidden]); tokens int32 [q] as LogprobBuffers.run takes them. Returns
+        probs. What does not fit these buffers is refused before anything is
+        launched."""
+        from . import _torch, _want, _want_vec, add_rms_norm, gemm, gemm_workspace_bytes, quantize_act
+        t, dev = _torch(), self.probs.index
+        H = self.x_act[0].shape[1]
+        if (head.hidden, head.n_vocab, head.w.index) != (H, self.probs.n_vocab, dev):
+            raise ValueError(f"buffers for a head of {self.probs.n_vocab} x {H} on GPU {dev}, this one is {head.n_vocab} x "
+                             f"{head.hidden} on GPU {head.w.index}")
+        need = gemm_workspace_bytes(head.w, self.q)
+        if need > (0 if self.ws is None else self.ws.nbytes):
+            raise ValueError(f"buffers have {0 if self.ws is None else self.ws.nbytes} bytes of workspace, {need} wanted")
+        _want(x, "x", t.f32, (self.q, H), dev)
+        _want_vec(head.norm, "norm", t.f32, H, dev)
+        if tokens is not None:
+            _want(tokens, "tokens", t.i32, (self.q,), dev)
+        if dev >= 0 and t.current_device() != dev:
+            with t.device_guard(dev):
+                return self.run(head, x, tokens, stream)
+        if head.norm is None:
+            quantize_act(x, *self.x_act, stream)
+        else:
+            add_rms_norm(x, head.norm, head.eps, None, None, None, *self.x_act, stream)
+        gemm(head.w, *self.x_act, self.q, self.logits, ws=self.ws, stream=stream)
+        return self.probs.run(self.logits, tokens, stream)
