@@ -232,7 +232,9 @@ class _Torch:
         import torch
         cls.f64, cls.i32, cls.i8 = torch.float64, torch.int32, torch.int8
         cls.elem = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-        cls.current_device, cls.device_guard = torch.cuda.current_device, torch.cuda.device
+        # the C function under torch.cuda.current_device, where torch has it (who has a GPU tensor has begun to use the GPU)
+        cls.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        cls.device_guard = torch.cuda.device
         # the handle itself, without a Stream object around it, where torch has that
         cls.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -762,22 +764,50 @@ def add_rms_norm(x, weight, eps, delta=None, out=None, y=None, xq=None, xs=None,
     t = _torch()
     f32, shape, dev = t.f32, x.shape, x.get_device()
     q, cols = shape
-    xp, x_stride = _rows(x, "x", shape, dev)
-    dp, d_stride = (0, 0) if delta is None else _rows(delta, "delta", shape, dev)
-    qp = sp = np_ = 0
+    # the checks of _rows and _want, which raise, for tensors that pass them, at half the cost
+    if x.dtype is f32 and x.is_contiguous():
+        xp, x_stride = x.data_ptr(), cols
+    else:
+        xp, x_stride = _rows(x, "x", shape, dev)
+    dp = d_stride = wp = op = yp = qp = sp = np_ = 0
+    if delta is not None:
+        if delta.dtype is f32 and delta.shape == shape and delta.is_contiguous() and delta.get_device() == dev:
+            dp, d_stride = delta.data_ptr(), cols
+        else:
+            dp, d_stride = _rows(delta, "delta", shape, dev)
+    if weight is not None:
+        if weight.dtype is f32 and weight.shape == (cols,) and weight.is_contiguous() and weight.get_device() == dev:
+            wp = weight.data_ptr()
+        else:
+            wp = _want(weight, "weight", f32, (cols,), dev)
+    if out is not None:
+        if out.dtype is f32 and out.shape == shape and out.is_contiguous() and out.get_device() == dev:
+            op = out.data_ptr()
+        else:
+            op = _want(out, "out", f32, shape, dev)
+    if y is not None:
+        if y.dtype is f32 and y.shape == shape and y.is_contiguous() and y.get_device() == dev:
+            yp = y.data_ptr()
+        else:
+            yp = _want(y, "y", f32, shape, dev)
     if xq is not None:
         blocks = (q, cols // 32)
-        qp = _want(xq, "xq", t.i8, shape, dev)
+        if xq.dtype is t.i8 and xq.shape == shape and xq.is_contiguous() and xq.get_device() == dev:
+            qp = xq.data_ptr()
+        else:
+            qp = _want(xq, "xq", t.i8, shape, dev)
+        if xs is None or xsum is None:
+            raise ValueError("xq without xs and xsum")
         sp = _want(xs, "xs", f32, blocks, dev)
         np_ = _want(xsum, "xsum", t.i32, blocks, dev)
     elif xs is not None or xsum is not None:
         raise ValueError("xs and xsum without xq")
-    wp = 0 if weight is None else _want(weight, "weight", f32, (cols,), dev)
-    op = 0 if out is None else _want(out, "out", f32, shape, dev)
-    yp = 0 if y is None else _want(y, "y", f32, shape, dev)
     if q: # an empty tensor has no address
-        _call_on(dev, stream, lib().rfx_add_rms_norm,
-                 _pack_norm(xp, dp, x_stride, d_stride, wp, op, yp, qp, sp, np_, eps, q, cols, 0))
+        args = _pack_norm(xp, dp, x_stride, d_stride, wp, op, yp, qp, sp, np_, eps, q, cols, 0)
+        if dev >= 0 and stream is None and t.current_device() == dev:
+            _check(lib().rfx_add_rms_norm(args, t.raw_stream(dev)))
+        else:
+            _call_on(dev, stream, lib().rfx_add_rms_norm, args)
 
 
 class DeviceLora:
@@ -811,6 +841,7 @@ def lora_workspace_bytes(loras, n_tokens: int) -> int:
 
 # rfx_lora up to its matrices, and one of those
 _pack_lora, _pack_lora_mat = struct.Struct("6iPqP").pack, struct.Struct("5P2i").pack
+_LORA_BYTES = ctypes.sizeof(LoraC)
 
 
 def lora(x, ids, loras, ys, resids=None, ws=None, stream=None):
@@ -822,21 +853,22 @@ def lora(x, ids, loras, ys, resids=None, ws=None, stream=None):
     shapes, an entry None for 0; resids None: ys are added to in place."""
     first = loras[0]
     dev, (T, _) = first.index, x.shape
-    f32 = _torch().f32
-    if len(loras) > LORA_MAX_MATS or len(ys) != len(loras) or (resids is not None and len(resids) != len(loras)):
-        raise ValueError(f"{len(loras)} matrices (at most {LORA_MAX_MATS}), {len(ys)} results")
+    t = _torch()
+    f32, kind = t.f32, first.kind
+    n = len(loras)
+    if n > LORA_MAX_MATS or len(ys) != n or (resids is not None and len(resids) != n):
+        raise ValueError(f"{n} matrices (at most {LORA_MAX_MATS}), {len(ys)} results")
     xp, x_stride = _rows(x, "x", (T, first.cols), dev)
-    args = [_pack_lora(*first.kind, T, len(loras), xp, x_stride, _want(ids, "ids", _Torch.i32, (T,), dev))]
-    for i, (m, y) in enumerate(zip(loras, ys)):
-        if m.kind != first.kind or m.index != dev:
-            raise ValueError(f"matrix {i}: (type, adapters, rank, cols) {m.kind} on GPU {m.index}, {first.kind} on GPU {dev} wanted")
+    args = [_pack_lora(*kind, T, n, xp, x_stride, _want(ids, "ids", t.i32, (T,), dev))]
+    for m, y, r in zip(loras, ys, ys if resids is None else resids):
+        if m is not first and (m.kind != kind or m.index != dev):
+            raise ValueError(f"matrices of (type, adapters, rank, cols) {m.kind} on GPU {m.index} and {kind} on GPU {dev}")
         shape = (T, m.rows)
         yp = _want(y, "y", f32, shape, dev)
-        r = y if resids is None else resids[i]
         args.append(_pack_lora_mat(*m.pointers, 0 if r is None else yp if r is y else _want(r, "resid", f32, shape, dev), yp, m.rows, 0))
     if T: # an empty tensor has no address
         wp, wn = _workspace(ws, dev)
-        _call_on(dev, stream, lib().rfx_lora_apply, b"".join(args).ljust(ctypes.sizeof(LoraC), b"\0"), wp, wn)
+        _call_on(dev, stream, lib().rfx_lora_apply, b"".join(args).ljust(_LORA_BYTES, b"\0"), wp, wn)
 
 
 def token_logprobs_workspace_bytes(q: int, n_vocab: int, top_k: int) -> int:
