@@ -16,12 +16,10 @@
 //
 // The k best: an element is a key of 64 bits, the value's order above the
 // complement of its index, so that no two are equal and ties are decided. In
-// a set of 256 threads the ceil(k / 4)-th largest of a wave's 64 thread
-// maxima is exceeded by that many elements of the wave; the least of the four
-// waves' is a bound that at least k elements reach and, in random
-// data, few more (k = 20 of 8192: about 40). They are compacted and ranked by
-// counting. Where more than 256 reach it (equal logits, sorted
-// ones), the k are taken out one after the other.
+// a workgroup the k-th largest of the threads' maxima is a bound that at least
+// k elements reach and, in random data, few more (64 of 8192: about 75). They
+// are compacted and ranked by counting. Where more than 512 reach it (equal
+// logits, sorted ones), the k are taken out one after the other.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -42,8 +40,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMaxTop = 64;
+constexpr int kList = 512; // 63 threads' eight elements fit: fewer than 64 that have any, at a row's end
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kShort = 8;               // elements per thread of a short chunk
+constexpr int kWaveTop = 8;            // up to so many alternatives a chunk is one wave's
 constexpr int kLoads = 4;               // 16-byte loads per thread of a long one
 constexpr int kJoinKeys = 32;           // keys per thread of the join
 constexpr float kLog2e = 1.4426950408889634f;
@@ -59,6 +59,7 @@ struct LogpArgs {
     const void *z;
     int64_t stride;
     int q, V, k, S, chunk;
+    int waves;       // of a chunk
     const int32_t *tokens;
     Stat *stat;      // [q][S][wave]
     uint64_t *keys;  // [q][S][k]
@@ -133,22 +134,27 @@ __device__ __forceinline__ float wave_max(float x)
 }
 
 struct Shared {
-    uint64_t list[kThreads];
+    uint64_t list[kList];
     uint64_t wave[kWaves];
+    uint32_t top[kThreads];
     int count;
 };
 
-// The upper 16 bits of the n-th largest (n >= 1) of a wave's 64 values, the
-// lower ones zero, uniform: its bits one after the other, from the highest, by
-// counting who reaches them.
-__device__ __forceinline__ uint32_t nth_largest(uint32_t v, int n)
+// The upper 16 bits of the n-th largest (n >= 1) of 64 N values, N per lane,
+// the lower ones zero, uniform: its bits one after the other, from the highest,
+// by counting who reaches them. 0: fewer than n values are not 0.
+template <int N>
+__device__ __forceinline__ uint32_t nth_largest(const uint32_t (&v)[N], int n)
 {
     uint32_t t = 0;
 #pragma unroll
     for (int b = 31; b >= 16; b--) {
         const uint32_t u = t | 1u << b;
-        if (__popcll(__ballot(v >= u)) >= n)
-            t = u;
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            count += __popcll(__ballot(v[i] >= u));
+        t = count >= n ? u : t;
     }
     return t;
 }
@@ -156,41 +162,51 @@ __device__ __forceinline__ uint32_t nth_largest(uint32_t v, int n)
 // The k largest keys of the workgroup's to out[0..k), in descending order,
 // 0 where there are fewer. This thread's N elements are value(j), -inf for
 // none, and key(j); best: the largest value. All threads call it.
-template <int N, class Value, class Key>
+template <int N, int WAVES, class Value, class Key>
 __device__ __forceinline__ void top_keys(Shared &sh, int k, float best, Value &&value, Key &&key, uint64_t *out)
 {
-    const int tid = threadIdx.x, wave = tid >> 6;
-    // values that at least k elements reach: one for the largest, else in
-    // every wave ceil(k / 4)
-    const uint32_t bound = k == 1 ? ordered(wave_max(best)) : nth_largest(best > -INFINITY ? ordered(best) : 0u, (k + kWaves - 1) / kWaves);
-    if ((tid & 63) == 0)
-        sh.wave[wave] = bound;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    // the k-th largest of the threads' largest, which at least k elements reach
+    const float own = k == 1 ? wave_max(best) : best;
+    const uint32_t top = own > -INFINITY ? ordered(own) : 0u;
+    uint32_t tops[WAVES];
     if (tid == 0)
         sh.count = 0;
+    sh.top[tid] = top;
     __syncthreads();
-    uint64_t t = sh.wave[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; w++)
-        t = (k == 1) == (sh.wave[w] > t) ? sh.wave[w] : t;
+    for (int w = 0; w < WAVES; w++)
+        tops[w] = sh.top[64 * w + lane];
+    uint64_t t;
+    if (k == 1) {
+        t = tops[0];
+#pragma unroll
+        for (int w = 1; w < WAVES; w++)
+            t = tops[w] > t ? tops[w] : t;
+    } else {
+        t = nth_largest(tops, k);
+    }
     const float from = fmaxf(value_of(t << 32), -3.4028234663852886e38f); // not -inf, which is no element
     if (best >= from)
 #pragma unroll
         for (int j = 0; j < N; j++)
             if (value(j) >= from) {
                 const int at = atomicAdd(&sh.count, 1);
-                if (at < kThreads)
+                if (at < kList)
                     sh.list[at] = key(j);
             }
     __syncthreads();
     const int n = sh.count;
-    if (n <= kThreads) {
-        const uint64_t mine = tid < n ? sh.list[tid] : 0;
-        int rank = 0;
+    if (n <= kList) {
+        for (int at = tid; at < n; at += 64 * WAVES) {
+            const uint64_t mine = sh.list[at];
+            int rank = 0;
 #pragma unroll 4
-        for (int i = 0; i < n; i++)
-            rank += sh.list[i] > mine;
-        if (tid < n && rank < k)
-            out[rank] = mine;
+            for (int i = 0; i < n; i++)
+                rank += sh.list[i] > mine;
+            if (rank < k)
+                out[rank] = mine;
+        }
         if (tid >= n && tid < k)
             out[tid] = 0;
         return;
@@ -211,7 +227,7 @@ __device__ __forceinline__ void top_keys(Shared &sh, int k, float best, Value &&
         __syncthreads();
         m = sh.wave[0];
 #pragma unroll
-        for (int w = 1; w < kWaves; w++)
+        for (int w = 1; w < WAVES; w++)
             m = sh.wave[w] > m ? sh.wave[w] : m;
         if (tid == 0)
             out[i] = m;
@@ -232,8 +248,8 @@ __device__ __forceinline__ float logit(const void *row, int i)
 // One workgroup per (row, chunk of E elements per thread). A thread's 16-byte
 // loads are aligned, so that the row's elements start `lead` elements into the
 // first; a load that the row fills only in part goes element by element.
-template <int TYPE, int E>
-__global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(LogpArgs a)
+template <int TYPE, int E, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void logprob_chunk_kernel(LogpArgs a)
 {
     constexpr int PER = TYPE == RFX_F32 ? 4 : 8, LOADS = E / PER, SIZE = 16 / PER;
     __shared__ Shared sh;
@@ -244,14 +260,14 @@ __global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(LogpArgs a)
     const int token = a.tokens ? a.tokens[row] : -1;
     const bool known = (unsigned)token < (unsigned)a.V;
 
-    const auto index = [&](int l) { return c * a.chunk + (l * kThreads + tid) * PER - lead; }; // of a load's first element
+    const auto index = [&](int l) { return c * a.chunk + (l * 64 * WAVES + tid) * PER - lead; }; // of a load's first element
     const bool whole = c * a.chunk >= lead && (c + 1) * a.chunk - lead <= a.V;                 // uniform
     u32x4 raw[LOADS];
     if (whole) {
         const char *p = zr + ((int64_t)c * a.chunk - lead) * SIZE;
 #pragma unroll
         for (int l = 0; l < LOADS; l++)
-            raw[l] = *reinterpret_cast<const u32x4 *>(p + 16 * (unsigned)(l * kThreads + tid));
+            raw[l] = *reinterpret_cast<const u32x4 *>(p + 16 * (unsigned)(l * 64 * WAVES + tid));
     } else { // what the row does not fill reads the workspace instead
 #pragma unroll
         for (int l = 0; l < LOADS; l++) {
@@ -302,10 +318,9 @@ __global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(LogpArgs a)
     float rest = 0.f, dot = 0.f;
 #pragma unroll
     for (int j = 0; j < E; j++) {
-        const float x = fmaxf(fmaf(z[j], kLog2e, -off), -1e30f); // 0 * -inf where nothing is left
-        const float e = __builtin_amdgcn_exp2f(x);
-        rest += e;
-        dot = fmaf(e, x, dot);
+        const float x = fmaf(z[j], kLog2e, -off), e = __builtin_amdgcn_exp2f(x);
+        rest += e; // NaN where x is
+        dot = fmaf(e, fmaxf(x, -1e30f), dot); // not 0 * -inf
     }
     const float fix = __builtin_amdgcn_exp2f(-lack), s = uniform(wave_sum(rest));
     rest = s * fix;
@@ -332,9 +347,9 @@ __global__ __launch_bounds__(kThreads) void logprob_chunk_kernel(LogpArgs a)
         above = wave_sum(above);
     }
     if ((tid & 63) == 0) // from powers of two
-        a.stat[((size_t)row * a.S + c) * kWaves + wave] = Stat{m, (float)n, rest, dot * 0.69314718055994531f, (float)above};
+        a.stat[((size_t)row * a.S + c) * WAVES + wave] = Stat{m, (float)n, rest, dot * 0.69314718055994531f, (float)above};
     if (a.k)
-        top_keys<E>(sh, a.k, top, [&](int j) { return z[j]; }, [&](int j) { return make_key(z[j], index(j / PER) + j % PER); },
+        top_keys<E, WAVES>(sh, a.k, top, [&](int j) { return z[j]; }, [&](int j) { return make_key(z[j], index(j / PER) + j % PER); },
                     a.keys + ((size_t)row * a.S + c) * a.k);
 }
 
@@ -348,20 +363,32 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const size_t row = blockIdx.x;
     const rfx_logprob &o = a.out;
-    const Stat *st = a.stat + row * a.S * kWaves;
-    const int parts = a.S * kWaves;
+    const int parts = a.S * a.waves;
+    const Stat *st = a.stat + row * parts;
 
     // Everything is read before it is waited for: the first statistics, the
-    // keys (S lists of k; the threads of a wave take every fourth), the token.
+    // keys, the token. Keys are S ordered lists of k, taken across the lists, all
+    // first ones, all second ones, so that every thread has some of the best (a
+    // bound from threads of which some have none lets most keys pass).
     const Stat none = {-INFINITY, 0.f, 0.f, 0.f, 0.f}, own = tid < parts ? st[tid] : none;
     const uint64_t *keys = a.keys + row * a.S * a.k;
-    const int n = a.S * a.k, first = lane * kWaves + wave;
     uint64_t mine[kJoinKeys];
+    {
+        const int n = a.S * a.k, first = lane * kWaves + wave, step_pos = kThreads / a.S, step_list = kThreads - step_pos * a.S;
+        int pos = first / a.S, list = first - pos * a.S;
 #pragma unroll
-    for (int j = 0; j < kJoinKeys; j++) {
-        mine[j] = 0;
-        if (j * kThreads < n) // uniform
-            mine[j] = j * kThreads + first < n ? keys[j * kThreads + first] : 0;
+        for (int j = 0; j < kJoinKeys; j++) {
+            mine[j] = 0;
+            if (j * kThreads < n) { // uniform
+                mine[j] = pos < a.k ? keys[list * a.k + pos] : 0;
+                pos += step_pos;
+                list += step_list;
+                if (list >= a.S) {
+                    list -= a.S;
+                    pos++;
+                }
+            }
+        }
     }
     const int token = a.tokens ? a.tokens[row] : -1;
     const bool known = (unsigned)token < (unsigned)a.V;
@@ -433,7 +460,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     for (int j = 0; j < kJoinKeys; j++)
         best = mine[j] > best ? mine[j] : best;
     const auto value = [](uint64_t key) { return key ? value_of(key) : -INFINITY; };
-    top_keys<kJoinKeys>(sh, a.k, value(best), [&](int j) { return value(mine[j]); }, [&](int j) { return mine[j]; }, best_keys);
+    top_keys<kJoinKeys, kWaves>(sh, a.k, value(best), [&](int j) { return value(mine[j]); }, [&](int j) { return mine[j]; }, best_keys);
     __syncthreads();
     if (tid < a.k) {
         const uint64_t key = best_keys[tid];
@@ -445,27 +472,30 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
 }
 
 struct Plan {
-    int E, chunk, S;
+    int E, waves, chunk, S;
     size_t stat, keys;
 };
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Chunks of four loads per thread (4096 fp32 or 8192 16-bit logits; twice the
-// fp32 ones where the join could not hold all keys), or of 2048 logits where
-// the long ones would leave compute units idle.
+// Chunks of four loads per thread (4096 fp32 or 8192 16-bit logits, a quarter
+// of that for one wave; twice the fp32 ones where the join could not hold all
+// keys), or of eight logits per thread where the long ones would leave compute
+// units idle.
 Plan plan(int type, int q, int V, int k)
 {
     Plan p{};
     // a row may start up to seven elements into its first 16 bytes
-    const auto chunks = [&](int E) { return (int)ceil_div((int64_t)V + 7, (int64_t)E * kThreads); };
-    const auto fits = [&](int E) { return chunks(E) * k <= kJoinKeys * kThreads; };
-    p.E = kLoads * (type == RFX_F32 && fits(kLoads * 4) ? 4 : 8);
-    if ((int64_t)q * chunks(p.E) < 512 && fits(kShort))
+    const auto chunks = [&](int E, int waves) { return (int)ceil_div((int64_t)V + 7, (int64_t)E * 64 * waves); };
+    const auto fits = [&](int E, int waves) { return (int64_t)chunks(E, waves) * k <= kJoinKeys * kThreads; };
+    const int f32 = type == RFX_F32 ? 4 : 8;
+    p.waves = k <= kWaveTop && fits(kLoads * f32, 1) ? 1 : kWaves;
+    p.E = kLoads * (fits(kLoads * f32, p.waves) ? f32 : 8);
+    if ((int64_t)q * chunks(p.E, p.waves) * p.waves < 2048 && fits(kShort, p.waves))
         p.E = kShort;
-    p.chunk = p.E * kThreads;
-    p.S = chunks(p.E);
-    p.stat = align256((size_t)q * p.S * kWaves * sizeof(Stat));
+    p.chunk = p.E * 64 * p.waves;
+    p.S = chunks(p.E, p.waves);
+    p.stat = align256((size_t)q * p.S * p.waves * sizeof(Stat));
     p.keys = align256((size_t)q * p.S * k * sizeof(uint64_t));
     return p;
 }
@@ -474,16 +504,30 @@ static_assert((kMaxVocab + 7 + 8 * kLoads * kThreads - 1) / (8 * kLoads * kThrea
 
 bool shape_ok(int q, int V, int k) { return q >= 0 && q <= RFX_LOGPROB_MAX_Q && V >= 1 && V <= kMaxVocab && k >= 0 && k <= kMaxTop; }
 
-template <int E>
-void launch(const LogpArgs &a, int type, hipStream_t st)
+template <int WAVES>
+void launch(const LogpArgs &a, int type, int E, hipStream_t st)
 {
-    const dim3 grid((unsigned)a.q * a.S), block(kThreads);
-    if (type == RFX_F32)
-        hipLaunchKernelGGL((logprob_chunk_kernel<RFX_F32, E>), grid, block, 0, st, a);
-    else if (type == RFX_F16)
-        hipLaunchKernelGGL((logprob_chunk_kernel<RFX_F16, E>), grid, block, 0, st, a);
-    else
-        hipLaunchKernelGGL((logprob_chunk_kernel<RFX_BF16, E>), grid, block, 0, st, a);
+    const dim3 grid((unsigned)a.q * a.S), block(64 * WAVES);
+#define RFX_LOGP(TYPE, N) hipLaunchKernelGGL((logprob_chunk_kernel<TYPE, N, WAVES>), grid, block, 0, st, a)
+    if (type == RFX_F32) {
+        if (E == kShort)
+            RFX_LOGP(RFX_F32, kShort);
+        else if (E == kLoads * 4)
+            RFX_LOGP(RFX_F32, kLoads * 4);
+        else
+            RFX_LOGP(RFX_F32, kLoads * 8);
+    } else if (type == RFX_F16) {
+        if (E == kShort)
+            RFX_LOGP(RFX_F16, kShort);
+        else
+            RFX_LOGP(RFX_F16, kLoads * 8);
+    } else {
+        if (E == kShort)
+            RFX_LOGP(RFX_BF16, kShort);
+        else
+            RFX_LOGP(RFX_BF16, kLoads * 8);
+    }
+#undef RFX_LOGP
 }
 
 } // namespace
@@ -546,17 +590,16 @@ int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens
     a.k = O->top_index || O->top_logprob ? O->top_k : 0;
     a.S = p.S;
     a.chunk = p.chunk;
+    a.waves = p.waves;
     a.tokens = tokens;
     a.stat = static_cast<Stat *>(ws);
     a.keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + p.stat);
     a.out = *O;
     const hipStream_t hs = (hipStream_t)stream;
-    if (p.E == kShort)
-        launch<kShort>(a, O->type, hs);
-    else if (p.E == kLoads * 4) // fp32 alone
-        hipLaunchKernelGGL((logprob_chunk_kernel<RFX_F32, kLoads * 4>), dim3((unsigned)a.q * a.S), dim3(kThreads), 0, hs, a);
+    if (p.waves == 1)
+        launch<1>(a, O->type, p.E, hs);
     else
-        launch<kLoads * 8>(a, O->type, hs);
+        launch<kWaves>(a, O->type, p.E, hs);
     if ((st = hip_status("token_logprobs chunk launch")))
         return st;
     hipLaunchKernelGGL(logprob_join_kernel, dim3(a.q), dim3(kThreads), 0, hs, a);
