@@ -9,9 +9,19 @@
 // group is a sequence whose new tokens, which are neighbours, all come after
 // its keys, so with 64 sequences of four heads per kv head a key tile serves
 // 256 rows instead of four.
+//
+// Two launches, the parts and the join (rfx_kv.h: AttnArgs, SharedArgs).
+// Bound by latency where prefixes are short, by the own keys' bytes and the
+// matrix pipe where there is much: 32 heads of 128, four sequences behind 500
+// keys (8 kv heads) 10 us; two groups of twelve with four new tokens each behind
+// 3001 keys (4) 24; 64 sequences of up to 700 keys behind 16384 (8) 54
+// (45 and the join's 9; the bytes take 23 and one after the other the prefix
+// takes 33, 17 GFLOP, and the own keys 27).
+#include <algorithm>
 #include <cmath>
 
-#include "rfx_kv.h"
+#include "rfx_attn_decode.h"
+#include "rfx_attn_prefill.h"
 
 using namespace rfx;
 using namespace rfx::dev;
@@ -19,6 +29,65 @@ using namespace rfx::dev;
 namespace {
 
 constexpr int kMaxSplits = 64; // one lane of the join each
+
+// The prefix of many rows on the prefill kernel's tiles and the sequences' own
+// keys on the decode kernel's, in one launch: the one is bound by the matrix
+// pipe, the other by latency and memory, and a compute unit has both at a time
+// (64 sequences of up to 700 keys behind 16384: 54 us with the join, 72 with the
+// two one after the other).
+template <class T, int DP, int TERMS, int NR, decode::Pages PG>
+__global__ __launch_bounds__(256, prefill::waves_per_simd(DP, TERMS) > 2 ? 2 : prefill::waves_per_simd(DP, TERMS))
+void shared_both_kernel(SharedArgs args)
+{
+    constexpr int A = 2 * prefill::Tile<DP>::buf, B = decode::lds_bytes<DP>();
+    __shared__ __align__(16) char smem[A > B ? A : B];
+    // the smaller arrays of either
+    constexpr int kBad = 3 * 2 * 4, kSmall = std::max(kBad + prefill::kIds * 4, 2 * decode::kWaves * NR * 16 * 4);
+    __shared__ __align__(16) char small[kSmall];
+    const int block = blockIdx.x;
+    if (block < args.group_blocks) {
+        prefill::attention<T, DP, TERMS>(args, block, smem, reinterpret_cast<unsigned (*)[2]>(small), reinterpret_cast<int *>(small + kBad));
+    } else {
+        float(*m)[NR * 16] = reinterpret_cast<float(*)[NR * 16]>(small);
+        decode::attention<T, DP, NR, PG>(args, block, smem, m, m + decode::kWaves);
+    }
+}
+
+template <class T, int DP, int TERMS, int NR>
+void both_pages(const SharedArgs &a, hipStream_t st)
+{
+    const KvArgs &kv = a.own.kv;
+    const dim3 grid(a.group_blocks + (unsigned)kv.n_seq * kv.Hk * a.own.S), block(256);
+    if (kv.D != DP || kv.page_shift < 4)
+        hipLaunchKernelGGL((shared_both_kernel<T, DP, TERMS, NR, decode::kAny>), grid, block, 0, st, a);
+    else if (kv.page_shift == 4)
+        hipLaunchKernelGGL((shared_both_kernel<T, DP, TERMS, NR, decode::kTwo>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((shared_both_kernel<T, DP, TERMS, NR, decode::kOne>), grid, block, 0, st, a);
+}
+
+template <class T, int DP, int NR>
+void both_terms(const SharedArgs &a, hipStream_t st)
+{
+    if (a.own.out_f32)
+        both_pages<T, DP, T::TERMS, NR>(a, st);
+    else
+        both_pages<T, DP, 1, NR>(a, st);
+}
+
+template <class T>
+int both(const SharedArgs &a, hipStream_t st)
+{
+    const int D = a.own.kv.D;
+    const bool one = a.own.rows == 16;
+    if (D > 128)
+        both_terms<T, 256, 1>(a, st);
+    else if (D > 64)
+        one ? both_terms<T, 128, 1>(a, st) : both_terms<T, 128, 2>(a, st);
+    else
+        one ? both_terms<T, 64, 1>(a, st) : both_terms<T, 64, 2>(a, st);
+    return hip_status("attn shared launch");
+}
 
 // The first eight partials of a row, `stride` elements apart, past the last
 // (of most) the last again.
@@ -145,7 +214,7 @@ struct Part {
 
 struct Plan {
     bool shared;     // else rfx_attn
-    bool tall;       // the prefix on the prefill kernel
+    bool tall;       // the prefix on the prefill kernel's tiles
     Part group, own;
     size_t units, bytes;
 };
@@ -164,10 +233,12 @@ int splits(int64_t units, int64_t tiles, const Part &p, int places = 512)
 }
 
 // Sequences of more rows than the decode kernel takes are left to rfx_attn,
-// whose prefill tiles already have 128 rows of one sequence per key. A prefix
-// of few rows and keys stays on the decode kernel, in the launch of the
-// sequences' own keys; larger ones go to the prefill kernel.
-constexpr int64_t kTall = 2 << 20;
+// whose prefill tiles already have 128 rows of one sequence per key. The
+// prefix of a group of few rows is the decode kernel's, which reads it once
+// per 32 (16) rows, mostly from L2: 80 rows of 8000 keys 28 us, on the prefill
+// kernel's tiles 32; 30000 keys 52 and 53. With more rows it is the other way
+// round: 384 rows of 3001 keys 24 against 27, 256 of 500 24 against 32.
+constexpr int64_t kTallRows = 96;
 
 Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, int n_heads)
 {
@@ -178,7 +249,7 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, 
     p.shared = rows <= most;
     if (!p.shared)
         return p;
-    p.tall = all > 64 && all * P->max_len > kTall;
+    p.tall = all > kTallRows;
     p.own.rows = rows > 16 || (!p.tall && all > 16 && most > 16) ? 32 : 16;
     p.own.row_blocks = 1;
     p.own.bn = 32;
@@ -196,7 +267,11 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, 
     p.group.cap_shift = 5;
     p.group.units = (int64_t)P->n_groups * C->n_kv_heads * p.group.row_blocks;
     p.group.S = splits(p.group.units, ceil_div(P->max_len < room ? P->max_len : room, p.group.bn), p.group, p.tall ? 512 : 256);
-    const int cap = p.tall ? 16 : 32; // partials of more splits cost the join more than they save
+    // Partials of more splits cost the join more than they save, unless the
+    // chip is not full without them (16384 keys, 256 rows of 8 kv heads: 16
+    // splits 54 us, 32 72; 16000 keys, 320 rows of 2: 16 splits 88, 32 55).
+    const int64_t full = 256 / (p.group.units < 256 ? p.group.units : 256);
+    const int cap = p.tall ? (int)(full > 16 ? full : 16) : 32;
     p.group.S = p.group.S < cap ? p.group.S : cap;
     sizes(p.group, dp);
     sizes(p.own, dp);
@@ -286,12 +361,11 @@ int rfx_attn_shared(const void *q, const rfx_kv_cache *C, const rfx_kv_batch *B,
     a.units = reinterpret_cast<SharedArgs::Unit *>(w);
     a.group_blocks = (int)(p.group.units * p.group.S);
     const hipStream_t hs = (hipStream_t)stream;
-    if (p.tall) {
-        if ((st = attn_prefill_launch(a, C->type, hs)))
-            return st;
-        a.group_blocks = 0;
-    }
-    if ((st = attn_decode_launch(a, C->type, p.own.rows / 16, hs)))
+    if (p.tall)
+        st = C->type == RFX_BF16 ? both<BF16>(a, hs) : both<F16>(a, hs);
+    else
+        st = attn_decode_launch(a, C->type, p.own.rows / 16, hs);
+    if (st)
         return st;
     return C->type == RFX_BF16 ? join<BF16>(a, hs) : join<F16>(a, hs);
 }

@@ -119,7 +119,6 @@ constexpr int kPairRows = 256, kPairIds = 4096;
 
 int attn_decode_launch(const AttnArgs &a, int type, int row_tiles, hipStream_t st);
 int attn_decode_launch(const SharedArgs &a, int type, int row_tiles, hipStream_t st);
-int attn_prefill_launch(const SharedArgs &a, int type, hipStream_t st); // its `group` alone
 int attn_prefill_launch(const AttnArgs &a, int type, hipStream_t st);
 int attn_join_launch(const AttnArgs &a, int type, int64_t units, hipStream_t st);
 

@@ -560,12 +560,12 @@ typedef struct rfx_kv_prefix {
  * prefix's keys and values are read once for all new tokens of its group, what
  * a sequence has behind it once for the sequence. Arguments as rfx_attn's. For
  * a 16-bit result the softmax weights of a prefix enter the matrix core as one
- * term where max_tokens makes more than 64 rows (new tokens x query heads per
- * kv head) and rows times max_len is more than 2^21. Sequences of more than 32 rows, 16 with heads over 128, go to
+ * term where max_tokens makes more than 96 rows (new tokens x query heads per
+ * kv head). Sequences of more than 32 rows, 16 with heads over 128, go to
  * rfx_attn, which reads a key once per 128 rows of one sequence. A prefix is
  * read from the pages of its group's first sequence.
  * ws: workspace of rfx_attn_shared_workspace_bytes, as rfx_attn's. Two
- * launches, and a third for prefixes as large as that.
+ * launches.
  * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */
 size_t rfx_attn_shared_workspace_bytes(const rfx_kv_cache *cache, const rfx_kv_batch *batch, const rfx_kv_prefix *prefix,
                                        int n_heads);
