@@ -4,10 +4,17 @@
 //
 //   lse = M + log(s),  s = sum e^(z - M),  entropy = log(s) - sum e^(z - M) (z - M) / s
 //
-// Bound by memory where there are many rows: every logit is read once, by the
-// first launch, in which a workgroup takes a chunk of a row into registers
-// and leaves the chunk's maximum, sums, count and k best keys. A second
-// launch, one workgroup per row, joins the chunks in 64 bits.
+// Every logit is read once, by the first launch, in which a workgroup takes a
+// chunk of a row into registers and leaves the chunk's maximum, sums, count and
+// k best keys. A second launch, one workgroup per row, joins the chunks in 64
+// bits.
+//
+// Measured (both launches): one row of 32000 fp32 logits and five alternatives
+// 9 us, latency; 64 rows of 131072, half of them -inf, and 20 alternatives 18,
+// of which the join is 6 and reading takes 5; 1021 rows of 100003 bf16 logits
+// 55 (204 MB, 3.7 TB/s; 30 at the rate of a large read). There the vector pipe
+// is busy all the time: an element is some ten operations, an exponential
+// among them, and there is nothing that the matrix pipe could take.
 //
 // Where little is beside the maximum, the elements equal to it are counted
 // and the others' sum is kept apart from that count, so that a row with one
@@ -18,8 +25,8 @@
 // complement of its index, so that no two are equal and ties are decided. In
 // a workgroup the k-th largest of the threads' maxima is a bound that at least
 // k elements reach and, in random data, few more (64 of 8192: about 75). They
-// are compacted and ranked by counting. Where more than 512 reach it (equal
-// logits, sorted ones), the k are taken out one after the other.
+// are listed and ranked by counting. Where more than 512 of a wave reach it
+// (equal logits, sorted ones), the k are taken out one after the other.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -44,7 +51,7 @@ constexpr int kList = 512; // 63 threads' eight elements fit: fewer than 64 that
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kShort = 8;               // elements per thread of a short chunk
 constexpr int kWaveTop = 8;            // up to so many alternatives a chunk is one wave's
-constexpr int kLoads = 4;               // 16-byte loads per thread of a long one
+constexpr int kLoads = 6;               // 16-byte loads per thread of a long one
 constexpr int kJoinKeys = 32;           // keys per thread of the join
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -58,7 +65,7 @@ struct Stat {
 struct LogpArgs {
     const void *z;
     int64_t stride;
-    int q, V, k, S, chunk;
+    int q, V, k, S;
     int waves;       // of a chunk
     const int32_t *tokens;
     Stat *stat;      // [q][S][wave]
@@ -133,11 +140,25 @@ __device__ __forceinline__ float wave_max(float x)
     return wave_reduce(x, [](float p, float q) { return fmaxf(p, q); });
 }
 
+template <int WAVES>
 struct Shared {
-    uint64_t list[kList];
-    uint64_t wave[kWaves];
-    uint32_t top[kThreads];
-    int count;
+    uint64_t list[WAVES][kList];
+    uint64_t wave[WAVES];
+    uint32_t top[64 * WAVES];
+    int count[WAVES];
+    int larger[WAVES > 1 ? kList * WAVES / 2 : 1]; // two counts of 16 bits each
+    // The i-th of all lists' keys, which are `counts` long.
+    __device__ __forceinline__ uint64_t at(int i, const int (&counts)[WAVES]) const
+    {
+        int w = 0;
+#pragma unroll
+        for (int u = 0; u < WAVES - 1; u++)
+            if (w == u && i >= counts[u]) {
+                i -= counts[u];
+                w++;
+            }
+        return list[w][i];
+    }
 };
 
 // The upper 16 bits of the n-th largest (n >= 1) of 64 N values, N per lane,
@@ -160,65 +181,105 @@ __device__ __forceinline__ uint32_t nth_largest(const uint32_t (&v)[N], int n)
 }
 
 // The k largest keys of the workgroup's to out[0..k), in descending order,
-// 0 where there are fewer. This thread's N elements are value(j), -inf for
-// none, and key(j); best: the largest value. All threads call it.
-template <int N, int WAVES, class Value, class Key>
-__device__ __forceinline__ void top_keys(Shared &sh, int k, float best, Value &&value, Key &&key, uint64_t *out)
+// 0 where there are fewer. This thread's N elements are key(j), where reach(1)(j);
+// best: the largest's upper half; reach(t)(j) for t > 0: whether the upper
+// half of key(j) is t or more; anew(j) has the compiler forget what it knows
+// of them. All threads call it.
+template <int N, int WAVES, class Anew, class Reach, class Key>
+__device__ __forceinline__ void top_keys(Shared<WAVES> &sh, int k, uint32_t best, Anew &&anew, Reach &&reach, Key &&key, uint64_t *out)
 {
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     // the k-th largest of the threads' largest, which at least k elements reach
-    const float own = k == 1 ? wave_max(best) : best;
-    const uint32_t top = own > -INFINITY ? ordered(own) : 0u;
-    uint32_t tops[WAVES];
-    if (tid == 0)
-        sh.count = 0;
-    sh.top[tid] = top;
-    __syncthreads();
+    uint32_t tops[WAVES], t;
+    if constexpr (WAVES > 1) {
+        sh.top[tid] = best;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WAVES; w++)
-        tops[w] = sh.top[64 * w + lane];
-    uint64_t t;
+        for (int w = 0; w < WAVES; w++)
+            tops[w] = sh.top[64 * w + lane];
+    } else {
+        tops[0] = best;
+    }
     if (k == 1) {
         t = tops[0];
 #pragma unroll
         for (int w = 1; w < WAVES; w++)
-            t = tops[w] > t ? tops[w] : t;
+            t = max(t, tops[w]);
+        t = __builtin_amdgcn_readfirstlane(wave_reduce(t, [](uint32_t p, uint32_t q) { return max(p, q); }));
     } else {
         t = nth_largest(tops, k);
     }
-    const float from = fmaxf(value_of(t << 32), -3.4028234663852886e38f); // not -inf, which is no element
-    if (best >= from)
+    t = max(t, 1u);
+    const auto from = reach(t);
+    // each wave lists its own, four elements a thread at a time
+    uint64_t *list = sh.list[wave];
+    int n = 0;
 #pragma unroll
-        for (int j = 0; j < N; j++)
-            if (value(j) >= from) {
-                const int at = atomicAdd(&sh.count, 1);
-                if (at < kList)
-                    sh.list[at] = key(j);
-            }
+    for (int j0 = 0; j0 < N; j0 += 4) {
+        uint64_t in[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            in[j] = __ballot(from(j0 + j));
+        if (in[0] | in[1] | in[2] | in[3])
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (in[j]) {
+                    const int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[j], 0));
+                    if (from(j0 + j) && at < kList)
+                        list[at] = key(j0 + j);
+                    n += (int)__popcll(in[j]);
+                }
+    }
+    if (lane == 0)
+        sh.count[wave] = n;
+    if constexpr (WAVES > 1)
+        for (int i = tid; i < kList * WAVES / 2; i += 64 * WAVES)
+            sh.larger[i] = 0;
     __syncthreads();
-    const int n = sh.count;
-    if (n <= kList) {
-        for (int at = tid; at < n; at += 64 * WAVES) {
-            const uint64_t mine = sh.list[at];
-            int rank = 0;
+    int counts[WAVES], all = 0, most = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) {
+        counts[w] = __builtin_amdgcn_readfirstlane(sh.count[w]);
+        all += counts[w];
+        most = max(most, counts[w]);
+    }
+    if (most <= kList) {
+        // each wave counts, for all, who of its own is larger
+        for (int i = lane; i < all; i += 64) {
+            const uint64_t mine = sh.at(i, counts);
+            int larger = 0;
 #pragma unroll 4
-            for (int i = 0; i < n; i++)
-                rank += sh.list[i] > mine;
-            if (rank < k)
-                out[rank] = mine;
+            for (int v = 0; v < n; v++)
+                larger += list[v] > mine;
+            if constexpr (WAVES > 1)
+                atomicAdd(&sh.larger[i / 2], larger << (16 * (i & 1)));
+            else if (larger < k)
+                out[larger] = mine;
         }
-        if (tid >= n && tid < k)
+        if constexpr (WAVES > 1) {
+            __syncthreads();
+            for (int i = tid; i < all; i += 64 * WAVES) {
+                const int rank = sh.larger[i / 2] >> (16 * (i & 1)) & 0xffff;
+                if (rank < k)
+                    out[rank] = sh.at(i, counts);
+            }
+        }
+        if (tid >= all && tid < k)
             out[tid] = 0;
         return;
     }
     // one after the other: the largest key below the last
+    const auto any = reach(1u);
     uint64_t last = ~0ull;
     for (int i = 0; i < k; i++) {
         uint64_t m = 0;
 #pragma unroll
         for (int j = 0; j < N; j++) {
-            const uint64_t v = value(j) > -INFINITY ? key(j) : 0;
+            anew(j);
+            const uint64_t v = any(j) ? key(j) : 0;
             m = v < last && v > m ? v : m;
+            if (j % 4 == 3)
+                asm volatile("" : "+v"(m));  // no more of them side by side
         }
         m = wave_reduce(m, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
         __syncthreads();
@@ -236,6 +297,11 @@ __device__ __forceinline__ void top_keys(Shared &sh, int k, float best, Value &&
 }
 
 template <int TYPE>
+__device__ __forceinline__ uint32_t bits(const void *row, int i)
+{
+    return TYPE == RFX_F32 ? static_cast<const uint32_t *>(row)[i] : static_cast<const uint16_t *>(row)[i];
+}
+template <int TYPE>
 __device__ __forceinline__ float logit(const void *row, int i)
 {
     if (TYPE == RFX_F32)
@@ -245,6 +311,17 @@ __device__ __forceinline__ float logit(const void *row, int i)
     return __uint_as_float((uint32_t)static_cast<const uint16_t *>(row)[i] << 16);
 }
 
+// The logit of a 32-bit word, of two the lower or the upper one.
+template <int TYPE>
+__device__ __forceinline__ float widen(uint32_t u, int upper)
+{
+    if (TYPE == RFX_F32)
+        return __uint_as_float(u);
+    if (TYPE == RFX_F16)
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)(upper ? u >> 16 : u));
+    return __uint_as_float(upper ? u & 0xffff0000u : u << 16);
+}
+
 // One workgroup per (row, chunk of E elements per thread). A thread's 16-byte
 // loads are aligned, so that the row's elements start `lead` elements into the
 // first; a load that the row fills only in part goes element by element.
@@ -252,19 +329,21 @@ template <int TYPE, int E, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void logprob_chunk_kernel(LogpArgs a)
 {
     constexpr int PER = TYPE == RFX_F32 ? 4 : 8, LOADS = E / PER, SIZE = 16 / PER;
-    __shared__ Shared sh;
-    const int tid = threadIdx.x, wave = tid >> 6;
+    constexpr int CHUNK = E * 64 * WAVES;
+    __shared__ Shared<WAVES> sh;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int row = blockIdx.x / a.S, c = blockIdx.x - row * a.S;
     const char *zr = static_cast<const char *>(a.z) + (int64_t)row * a.stride * SIZE;
     const int lead = (int)((reinterpret_cast<uintptr_t>(zr) & 15) / SIZE);
     const int token = a.tokens ? a.tokens[row] : -1;
     const bool known = (unsigned)token < (unsigned)a.V;
 
-    const auto index = [&](int l) { return c * a.chunk + (l * 64 * WAVES + tid) * PER - lead; }; // of a load's first element
-    const bool whole = c * a.chunk >= lead && (c + 1) * a.chunk - lead <= a.V;                 // uniform
+    int first = c * CHUNK + tid * PER - lead;
+    const auto index = [&](int l) { return first + l * 64 * WAVES * PER; }; // of a load's first element
+    const bool whole = c * CHUNK >= lead && (c + 1) * CHUNK - lead <= a.V; // uniform
     u32x4 raw[LOADS];
     if (whole) {
-        const char *p = zr + ((int64_t)c * a.chunk - lead) * SIZE;
+        const char *p = zr + ((int64_t)c * CHUNK - lead) * SIZE;
 #pragma unroll
         for (int l = 0; l < LOADS; l++)
             raw[l] = *reinterpret_cast<const u32x4 *>(p + 16 * (unsigned)(l * 64 * WAVES + tid));
@@ -278,85 +357,101 @@ __global__ __launch_bounds__(64 * WAVES) void logprob_chunk_kernel(LogpArgs a)
     }
     const float zt = uniform(known ? logit<TYPE>(zr, token) : INFINITY);
 
-    float z[E];
-#pragma unroll
-    for (int l = 0; l < LOADS; l++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const uint32_t w = raw[l][e]; // a bit cast of the vector's element itself reads another one
-            if (TYPE == RFX_F32) {
-                z[l * PER + e] = __uint_as_float(w);
-            } else if (TYPE == RFX_BF16) {
-                z[l * PER + 2 * e] = __uint_as_float(w << 16);
-                z[l * PER + 2 * e + 1] = __uint_as_float(w & 0xffff0000u);
-            } else {
-                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-                const h2 h = __builtin_bit_cast(h2, w);
-                z[l * PER + 2 * e] = (float)h[0];
-                z[l * PER + 2 * e + 1] = (float)h[1];
-            }
-        }
     if (!whole)
 #pragma unroll
         for (int l = 0; l < LOADS; l++) {
             const int i = index(l);
             if (i < 0 || i + PER > a.V) {
+                constexpr uint32_t none = TYPE == RFX_F32 ? 0xff800000u : TYPE == RFX_F16 ? 0xfc00u : 0xff80u; // -inf
 #pragma unroll
-                for (int e = 0; e < PER; e++)
-                    z[l * PER + e] = i + e >= 0 && i + e < a.V ? logit<TYPE>(zr, i + e) : -INFINITY;
+                for (int e = 0; e < 4; e++) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int h = 0; h < PER / 4; h++) {
+                        const int at = i + e * (PER / 4) + h;
+                        w |= (at >= 0 && at < a.V ? bits<TYPE>(zr, at) : none) << (16 * h);
+                    }
+                    raw[l][e] = w;
+                }
             }
         }
+    // 16-bit logits stay packed and are widened anew by each pass, and keys are
+    // made anew: in half the registers or less a SIMD holds up to eight waves
+    // instead of four (78 -> 70 us for 1021 rows of 100003 and eight
+    // alternatives)
+    uint32_t w[4 * LOADS];
+#pragma unroll
+    for (int i = 0; i < 4 * LOADS; i++)
+        w[i] = raw[i / 4][i % 4]; // a bit cast of the vector's element itself reads another one
+    const auto anew = [&](int j) { asm volatile("" : "+v"(w[j / (PER / 4)]), "+v"(first)); };
+    const auto pass = [&]() {
+        if constexpr (PER == 8)
+#pragma unroll
+            for (int i = 0; i < 4 * LOADS; i++)
+                anew(2 * i);
+    };
+    const auto z = [&](int j) { return widen<TYPE>(w[j / (PER / 4)], j & 1); };
 
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < E; j++)
-        top = fmaxf(top, z[j]);
+        top = fmaxf(top, z(j));
     // e^(z - m) = 2^(c z - c m), one fused operation: c m is rounded, by
     // the same for all, and what it lacks is made up for below
     const float m = uniform(wave_max(top)), base = m == -INFINITY ? 0.f : m;
     const float off = base * kLog2e, lack = fmaf(base, kLog2e, -off);
-    float rest = 0.f, dot = 0.f;
+    // two sums each: half the roundings on either
+    float rests[2] = {0.f, 0.f}, dots[2] = {0.f, 0.f};
+    pass();
 #pragma unroll
     for (int j = 0; j < E; j++) {
-        const float x = fmaf(z[j], kLog2e, -off), e = __builtin_amdgcn_exp2f(x);
-        rest += e; // NaN where x is
-        dot = fmaf(e, fmaxf(x, -1e30f), dot); // not 0 * -inf
+        const float x = fmaf(z(j), kLog2e, -off), e = __builtin_amdgcn_exp2f(x);
+        rests[j & 1] += e; // NaN where x is
+        dots[j & 1] = fmaf(e, fmaxf(x, -1e30f), dots[j & 1]); // not 0 * -inf
     }
-    const float fix = __builtin_amdgcn_exp2f(-lack), s = uniform(wave_sum(rest));
-    rest = s * fix;
-    dot = (wave_sum(dot) - lack * s) * fix;
+    const float fix = __builtin_amdgcn_exp2f(-lack), s = uniform(wave_sum(rests[0] + rests[1]));
+    float rest = s * fix, dot = (wave_sum(dots[0] + dots[1]) - lack * s) * fix;
     int n = 0, above = 0;
     // little beside the largest, or c m past fp32's range: the others alone
     if (rest < 1.25f || fabsf(base) > 2e38f) {
-        rest = dot = 0.f;
+        rests[0] = rests[1] = dots[0] = dots[1] = 0.f;
+        pass();
 #pragma unroll
         for (int j = 0; j < E; j++) {
-            const float x = fmaxf((z[j] - m) * kLog2e, -1e30f), e = z[j] == m ? 0.f : __builtin_amdgcn_exp2f((z[j] - m) * kLog2e);
-            rest += e;
-            dot = fmaf(e, x, dot);
-            n += z[j] == m;
+            const float x = fmaxf((z(j) - m) * kLog2e, -1e30f), e = z(j) == m ? 0.f : __builtin_amdgcn_exp2f((z(j) - m) * kLog2e);
+            rests[j & 1] += e;
+            dots[j & 1] = fmaf(e, x, dots[j & 1]);
+            n += z(j) == m;
+            if (j % 4 == 3) // no more of them side by side: registers that the other passes would have to leave free
+                asm volatile("" : "+v"(rests[0]), "+v"(rests[1]), "+v"(dots[0]), "+v"(dots[1]), "+v"(n));
         }
-        rest = m == INFINITY ? NAN : wave_sum(rest);
-        dot = wave_sum(dot);
+        rest = m == INFINITY ? NAN : wave_sum(rests[0] + rests[1]);
+        dot = wave_sum(dots[0] + dots[1]);
         n = m == -INFINITY ? 0 : wave_sum(n);
     }
     if (m > zt) {
+        pass();
 #pragma unroll
         for (int j = 0; j < E; j++)
-            above += z[j] > zt;
-        above = wave_sum(above);
+            above += __popcll(__ballot(z(j) > zt));
     }
-    if ((tid & 63) == 0) // from powers of two
+    if (lane == 0) // from powers of two
         a.stat[((size_t)row * a.S + c) * WAVES + wave] = Stat{m, (float)n, rest, dot * 0.69314718055994531f, (float)above};
-    if (a.k)
-        top_keys<E, WAVES>(sh, a.k, top, [&](int j) { return z[j]; }, [&](int j) { return make_key(z[j], index(j / PER) + j % PER); },
-                    a.keys + ((size_t)row * a.S + c) * a.k);
+    if (!a.k)
+        return;
+    pass();
+    const auto key = [&](int j) { return make_key(z(j), index(j / PER) + j % PER); };
+    const auto reach = [&](uint32_t t) {
+        const float from = fmaxf(value_of((uint64_t)t << 32), -3.4028234663852886e38f); // not -inf, which is no element
+        return [&z, from](int j) { return z(j) >= from; };
+    };
+    top_keys<E, WAVES>(sh, a.k, top > -INFINITY ? ordered(top) : 0u, anew, reach, key, a.keys + ((size_t)row * a.S + c) * a.k);
 }
 
 // One workgroup per row.
 __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
 {
-    __shared__ Shared sh;
+    __shared__ Shared<kWaves> sh;
     __shared__ uint64_t best_keys[kMaxTop];
     __shared__ double part[kWaves][4];
     __shared__ float tops[kWaves];
@@ -459,8 +554,8 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
 #pragma unroll
     for (int j = 0; j < kJoinKeys; j++)
         best = mine[j] > best ? mine[j] : best;
-    const auto value = [](uint64_t key) { return key ? value_of(key) : -INFINITY; };
-    top_keys<kJoinKeys, kWaves>(sh, a.k, value(best), [&](int j) { return value(mine[j]); }, [&](int j) { return mine[j]; }, best_keys);
+    const auto reach = [&](uint32_t t) { return [&mine, t](int j) { return (uint32_t)(mine[j] >> 32) >= t; }; };
+    top_keys<kJoinKeys, kWaves>(sh, a.k, (uint32_t)(best >> 32), [](int) {}, reach, [&](int j) { return mine[j]; }, best_keys);
     __syncthreads();
     if (tid < a.k) {
         const uint64_t key = best_keys[tid];
@@ -472,35 +567,34 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
 }
 
 struct Plan {
-    int E, waves, chunk, S;
+    int E, waves, S;
     size_t stat, keys;
 };
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Chunks of four loads per thread (4096 fp32 or 8192 16-bit logits, a quarter
-// of that for one wave; twice the fp32 ones where the join could not hold all
-// keys), or of eight logits per thread where the long ones would leave compute
-// units idle.
+// Chunks of six loads per thread (6144 fp32 or 12288 16-bit logits, a quarter
+// of that for one wave), or of eight logits per thread where the long ones
+// would leave compute units idle. 1021 rows of 100003 bf16 logits, with four,
+// six, eight loads: 60, 58, 61 us; 300 of 131072 fp32 ones: 43 with four, 39
+// with six.
 Plan plan(int type, int q, int V, int k)
 {
     Plan p{};
     // a row may start up to seven elements into its first 16 bytes
     const auto chunks = [&](int E, int waves) { return (int)ceil_div((int64_t)V + 7, (int64_t)E * 64 * waves); };
     const auto fits = [&](int E, int waves) { return (int64_t)chunks(E, waves) * k <= kJoinKeys * kThreads; };
-    const int f32 = type == RFX_F32 ? 4 : 8;
-    p.waves = k <= kWaveTop && fits(kLoads * f32, 1) ? 1 : kWaves;
-    p.E = kLoads * (fits(kLoads * f32, p.waves) ? f32 : 8);
+    p.E = kLoads * (type == RFX_F32 ? 4 : 8);
+    p.waves = k <= kWaveTop && fits(p.E, 1) ? 1 : kWaves;
     if ((int64_t)q * chunks(p.E, p.waves) * p.waves < 2048 && fits(kShort, p.waves))
         p.E = kShort;
-    p.chunk = p.E * 64 * p.waves;
     p.S = chunks(p.E, p.waves);
     p.stat = align256((size_t)q * p.S * p.waves * sizeof(Stat));
     p.keys = align256((size_t)q * p.S * k * sizeof(uint64_t));
     return p;
 }
 
-static_assert((kMaxVocab + 7 + 8 * kLoads * kThreads - 1) / (8 * kLoads * kThreads) * kMaxTop <= kJoinKeys * kThreads, "the join holds all keys");
+static_assert((kMaxVocab + 7 + 4 * kLoads * kThreads - 1) / (4 * kLoads * kThreads) * kMaxTop <= kJoinKeys * kThreads, "the join holds all keys");
 
 bool shape_ok(int q, int V, int k) { return q >= 0 && q <= RFX_LOGPROB_MAX_Q && V >= 1 && V <= kMaxVocab && k >= 0 && k <= kMaxTop; }
 
@@ -512,20 +606,18 @@ void launch(const LogpArgs &a, int type, int E, hipStream_t st)
     if (type == RFX_F32) {
         if (E == kShort)
             RFX_LOGP(RFX_F32, kShort);
-        else if (E == kLoads * 4)
-            RFX_LOGP(RFX_F32, kLoads * 4);
         else
-            RFX_LOGP(RFX_F32, kLoads * 8);
+            RFX_LOGP(RFX_F32, 4 * kLoads);
     } else if (type == RFX_F16) {
         if (E == kShort)
             RFX_LOGP(RFX_F16, kShort);
         else
-            RFX_LOGP(RFX_F16, kLoads * 8);
+            RFX_LOGP(RFX_F16, 8 * kLoads);
     } else {
         if (E == kShort)
             RFX_LOGP(RFX_BF16, kShort);
         else
-            RFX_LOGP(RFX_BF16, kLoads * 8);
+            RFX_LOGP(RFX_BF16, 8 * kLoads);
     }
 #undef RFX_LOGP
 }
@@ -589,7 +681,6 @@ int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens
     a.V = O->n_vocab;
     a.k = O->top_index || O->top_logprob ? O->top_k : 0;
     a.S = p.S;
-    a.chunk = p.chunk;
     a.waves = p.waves;
     a.tokens = tokens;
     a.stat = static_cast<Stat *>(ws);
