@@ -42,6 +42,7 @@ struct LoraArgs {
     int T16;          // tokens in whole tiles
     float *v;         // [splits][T16][n_mats * R16]
     int row_blocks[kMats]; // of the second launch
+    int turns;             // of its workgroups over the rows, with the same v
     int vec;          // bit m: rows of matrix m are 16-byte aligned
 };
 
@@ -339,16 +340,19 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
     while (m + 1 < l.n_mats && rb >= a.row_blocks[m])
         rb -= a.row_blocks[m++];
     const rfx_lora_mat &M = l.mats[m];
-    const int n0 = (rb * kWaves + wave) * 16 * RT;
+    constexpr int STRIDE = kWaves * 16 * RT; // rows of the workgroup's waves
+    int n0 = (rb * a.turns * kWaves + wave) * 16 * RT;
+    const int n_end = min(M.rows, n0 + a.turns * STRIDE);
     const int id = adapter_of(l, t);
-    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;
-    const bool any = todo != 0; // the same in every wave
+    const uint32_t all = (uint32_t)__ballot(id >= 0) & 0xffffu;
+    const bool any = all != 0; // the same in every wave
     if (!any && M.resid == M.y)
         return;
 
-    // ADS adapters of those left: their rows of B, and who has them
+    // The next ADS adapters: their rows of B from next_n on, and who has them.
     bool live[ADS];
-    uint32_t keep[ADS];
+    uint32_t keep[ADS], todo = all;
+    int next_n = n0;
     u4 w[ADS][RT][KS];
     const auto fetch = [&] {
 #pragma unroll
@@ -365,19 +369,14 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
             for (int i = 0; i < RT; i++)
 #pragma unroll
                 for (int k = 0; k < KS; k++) {
-                    const int n = min(n0 + 16 * i + r16, M.rows - 1), r = 32 * k + 8 * g4;
+                    const int n = min(next_n + 16 * i + r16, M.rows - 1), r = 32 * k + 8 * g4;
                     const u4 x = *reinterpret_cast<const u4 *>(p + (size_t)n * l.rank + (r < l.rank ? r : 0));
                     w[j][i][k] = r < l.rank ? x : (u4){0, 0, 0, 0};
                 }
         }
     };
-    f32x4 acc[RT][X::SUMS];
-#pragma unroll
-    for (int i = 0; i < RT; i++)
-#pragma unroll
-        for (int s = 0; s < X::SUMS; s++)
-            acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
     float out = 1.0f;
+    u4 vt[KS][X::N];
     if (any) {
         fetch();
         const float c = id >= 0 && M.scale ? M.scale[id] : 1.0f;
@@ -433,52 +432,83 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
                 for (int e = 0; e < 8; e++)
                     v[k][e] *= in;
         }
-        u4 vt[KS][X::N];
 #pragma unroll
         for (int k = 0; k < KS; k++)
             X::split(v[k], vt[k]);
-        for (;;) {
+    }
+    const bool vec = a.vec >> m & 1;
+    const float *resid = M.resid + (size_t)t * M.rows;
+    for (; n0 < n_end; n0 += STRIDE) {
+        // lane: token r16, rows 4 g4 .. + 3 of tile i
+        f32x4 acc[RT][X::SUMS], y[RT];
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
+#pragma unroll
+            for (int s = 0; s < X::SUMS; s++)
+                acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            const int n = n0 + 16 * i + 4 * g4;
+            y[i] = acc[i][0];
+            if (vec && M.resid && t < l.n_tokens && n < M.rows)
+                y[i] = *reinterpret_cast<const f32x4 *>(resid + n);
+        }
+        for (bool more = any; more;) {
+            u4 now[ADS][RT][KS];
+            bool on[ADS];
+            uint32_t who[ADS];
 #pragma unroll
             for (int j = 0; j < ADS; j++) {
-                if (!live[j])
+                on[j] = live[j];
+                who[j] = keep[j];
+#pragma unroll
+                for (int i = 0; i < RT; i++)
+#pragma unroll
+                    for (int k = 0; k < KS; k++)
+                        now[j][i][k] = w[j][i][k];
+            }
+            more = todo != 0;
+            if (!more) {
+                todo = all;
+                next_n += STRIDE;
+            }
+            if (ADS == 1 && next_n < n_end) // the next ones' loads before these's products
+                fetch();
+#pragma unroll
+            for (int j = 0; j < ADS; j++) {
+                if (!on[j])
                     continue;
 #pragma unroll
                 for (int k = 0; k < KS; k++) {
                     u4 tm[X::N];
 #pragma unroll
                     for (int s = 0; s < X::N; s++)
-                        tm[s] = vt[k][s] & keep[j];
+                        tm[s] = vt[k][s] & who[j];
 #pragma unroll
                     for (int s = 0; s < X::N; s++)
 #pragma unroll
                         for (int i = 0; i < RT; i++)
-                            X::mma(s, w[j][i][k], tm, acc[i]);
+                            X::mma(s, now[j][i][k], tm, acc[i]);
                 }
             }
-            if (!todo)
-                break;
-            fetch();
+            if (ADS > 1 && next_n < n_end)
+                fetch();
         }
-    }
-    // lane: token r16, rows 4 g4 .. + 3 of tile i
-    if (t >= l.n_tokens)
-        return;
-#pragma unroll
-    for (int i = 0; i < RT; i++) {
-        const int n = n0 + 16 * i + 4 * g4, left = M.rows - n;
-        if (left <= 0)
+        if (t >= l.n_tokens)
             continue;
-        const size_t at = (size_t)t * M.rows + n;
-        f32x4 y = X::total(acc[i]) * out;
-        if (a.vec >> m & 1) {
-            if (M.resid)
-                y += *reinterpret_cast<const f32x4 *>(M.resid + at);
-            *reinterpret_cast<f32x4 *>(M.y + at) = y;
-        } else {
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (e < left)
-                    M.y[at + e] = M.resid ? y[e] + M.resid[at + e] : y[e];
+        for (int i = 0; i < RT; i++) {
+            const int n = n0 + 16 * i + 4 * g4, left = M.rows - n;
+            if (left <= 0)
+                continue;
+            const size_t at = (size_t)t * M.rows + n;
+            y[i] += X::total(acc[i]) * out;
+            if (vec) {
+                *reinterpret_cast<f32x4 *>(M.y + at) = y[i];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (e < left)
+                        M.y[at + e] = M.resid ? y[i][e] + resid[n + e] : y[i][e];
+            }
         }
     }
 }
@@ -558,8 +588,16 @@ template <class T, int KS>
 void launch_up_rank(LoraArgs &a, bool many, hipStream_t st)
 {
     int blocks = 0;
-    for (int m = 0; m < a.l.n_mats; m++)
-        blocks += a.row_blocks[m] = (int)ceil_div(a.l.mats[m].rows, (many ? 32 : 16) * kWaves);
+    a.turns = 1;
+    for (;; a.turns = 2) {
+        blocks = 0;
+        for (int m = 0; m < a.l.n_mats; m++)
+            blocks += a.row_blocks[m] = (int)ceil_div(a.l.mats[m].rows, (many ? 32 : 16) * kWaves * a.turns);
+        // Two turns where the chip is full without (4001 tokens 81 us, with one
+        // 82, four 85; 300 tokens 18 and 17).
+        if (!many || a.turns == 2 || (int64_t)blocks * (a.T16 / 16) < 2048)
+            break;
+    }
     const dim3 grid(blocks, a.T16 / 16), block(kThreads);
     if (many)
         hipLaunchKernelGGL((lora_up_kernel<T, KS, 2, 1>), grid, block, 0, st, a);
