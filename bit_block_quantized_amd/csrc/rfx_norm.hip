@@ -4,9 +4,12 @@
 //   h = x + delta,   y = h w / sqrt(mean(h^2) + eps),
 //   per 32 elements: s = max |y| (1 / 127), code = round(y / s), sum of codes.
 //
-// Bound by memory: each row is read once and held in the registers of one
-// workgroup, four elements of every THREADS * 4 per thread, until its sum of
-// squares is known. The sum, the root and the products are fp64 (the vector
+// Bound by memory where there are many rows: 4099 rows of 7168 with delta, weight
+// and all outputs take 104 us, 507 MB at 4.9 TB/s (a large copy has 4.8, a read
+// of 235 MB and a write of 272 one after the other would take 108). One row of
+// 4096, and four of 7168, take 3.7, mostly the launch. Each row is read once and
+// held in the registers of one workgroup, four elements of every THREADS * 4
+// per thread, until its sum of squares is known. The sum, the root and the products are fp64 (the vector
 // pipe's fp64 rate is its fp32 rate, and there are some 60 operations to
 // spare per element): y is then the fp32 number next to the exact value but
 // for one in 2^28, the codes do not depend on the order of the sum, and

@@ -624,7 +624,7 @@ typedef struct rfx_lora_mat {
     const void *a, *b;  /* 16-B aligned */
     const float *scale; /* fp32 [n_adapters] (alpha / rank), or NULL: 1 */
     const float *resid; /* fp32 [n_tokens][rows], or NULL: 0 */
-    float *y;           /* fp32 [n_tokens][rows]; overlaps nothing but resid */
+    float *y;           /* fp32 [n_tokens][rows]; overlaps nothing but its resid */
     int32_t rows;       /* 1..2^24 */
     int32_t reserved;
 } rfx_lora_mat;

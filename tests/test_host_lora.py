@@ -38,6 +38,16 @@ def test_takes():
     assert R.lib().rfx_lora_apply(None, P, 1 << 30, None) == INVAL
 
 
+def test_refuses_results_that_overlap():
+    """Whole, in part, and the last row of one with the first of the next."""
+    m = lambda y, rows: R.LoraMatC(P, P, None, None, y, rows, 0)  # noqa: E731
+    for a, b in ((m(P, 8), m(P, 8)), (m(P, 8), m(P + 16, 4)), (m(P + 80, 64), m(P, 8)), (m(P, 1 << 24), m(P + (1 << 27), 4))):
+        c = R.LoraC(R.BF16, 4, 16, 64, 3, 2, P, 64, P, (R.LoraMatC * R.LORA_MAX_MATS)(a, b))
+        assert R.lib().rfx_lora_apply(ctypes.byref(c), None, 0, None) == INVAL
+    c = R.LoraC(R.BF16, 4, 16, 64, 3, 2, P, 64, P, (R.LoraMatC * R.LORA_MAX_MATS)(m(P, 8), m(P + 96, 8)))  # neighbours
+    assert R.lib().rfx_lora_apply(ctypes.byref(c), None, 0, None) == WORKSPACE
+
+
 def test_packed_arguments_are_the_structure():
     m = R.LoraMatC(P, 2 * P, 3 * P, 4 * P, 5 * P, 77, 0)
     c = R.LoraC(R.F16, 3, 24, 96, 5, 2, 6 * P, 128, 7 * P, (R.LoraMatC * 4)(m, m))
