@@ -21,9 +21,9 @@
 // Measured: one token, rank 16, query, key and value (4096 x 4096 + 2 x 1024)
 // 8.6 us, the time of two launches that wait for memory twice (one launch in
 // which every workgroup makes v itself took 10.0); 64 tokens of 48 adapters of
-// rank 64, 4096 x 4096, 17.2 (the 37 MB of those that occur take 6); 4001 tokens of seven prompts,
-// rank 32, 81: 32 for the first launch (66 MB of x, ten at its start and end)
-// and 50 for the second (197 MB, 3.9 TB/s; a large copy has 4.8).
+// rank 64, 4096 x 4096, 17.2 (the 37 MB of those that occur take 6); 4001 tokens
+// of seven prompts, rank 32, 81: 32 for the first launch (66 MB of x, ten at its
+// start and end) and 50 for the second (197 MB, 3.9 TB/s; a large copy has 4.8).
 #include <algorithm>
 
 #include "rfx_kv.h"

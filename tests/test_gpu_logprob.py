@@ -212,3 +212,15 @@ def test_captured_and_deterministic():
         again = R.LogprobBuffers(5, 30000, 7).run(zd, td)
         for name in ("logprob", "lse", "entropy", "rank", "top_index", "top_logprob"):
             assert torch.equal(getattr(again, name), getattr(b, name)), name
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_borders_of_long_chunks(kind):
+    """Rows that end beside the end of a chunk, so many that chunks are long
+    ones, with few alternatives and with more."""
+    n = 1536 if kind == "f32" else 3072 # of one wave, of four: four times that
+    for q, V, k in ((1100, n - 3, 5), (1100, n + 1, 1), (300, 4 * n - 3, 20), (300, 4 * n + 1, 64)):
+        check(*logits(q, V, V + k, kind), k)
+    for q, V, k in ((1100, n + 1, 8), (300, 4 * n + 1, 20)):
+        z = torch.stack(list(_orders(V).values())).repeat(q // 9 + 1, 1)[:q].to(TYPES[kind])
+        check(z, torch.arange(q) % V, k)

@@ -180,3 +180,12 @@ def test_captured_with_other_ids(T):
         again = [torch.empty_like(y) for y in c.ys]
         R.lora(x, ids, c.loras, again, resid, c.ws)
         assert all(torch.equal(p, q) for p, q in zip(again, c.ys))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows", [[7001], [4096, 4100], [64, 7168]])
+def test_many_tokens_and_rows(rows, kind):
+    """So many that a workgroup takes rows twice, ends inside its second turn
+    or has none."""
+    Case(700, 64, 24, rows, 5, kind).check()
+    Case(700, 64, 24, rows, 5, kind, ids=[0] * 40 + [-1] * 100 + [4] * 300 + [7] * 60 + [2] * 200, resid=False).check()

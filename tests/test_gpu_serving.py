@@ -9,7 +9,7 @@ import torch
 
 import bit_block_quantized_amd as R
 import inputgen
-from gpu_common import need_gpu
+from gpu_common import need_gpu, say
 from moe_common import LayerSpec
 from test_gpu_attention_layer import D, H, HK, HQ, batch_of, new_cache
 
@@ -180,3 +180,54 @@ def test_serving_steps(new):
         assert ((want.logprob.cpu().double() - lp.gather(1, tokens[:, None])[:, 0]).abs() <= 1e-5).all()
         assert torch.equal(want.top_index.cpu().long(), z.sort(dim=-1, descending=True, stable=True).indices[:, :4])
         assert ((want.entropy.cpu().double() + (lp.exp() * lp).sum(-1)).abs() <= 1e-5).all()
+
+
+def test_two_calls_at_once():
+    """On two streams, with a workspace each, the results are those of one
+    after the other."""
+    need_gpu()
+    say("two streams")
+    g = torch.Generator().manual_seed(5)
+    T, rows, K, V = 96, 1024, 2048, 20000
+    sides = []
+    for side in range(2):
+        b = R.DeviceKVCache(*(torch.randn((80, 2, 64, 128), generator=g).bfloat16().cuda() for _ in range(2)))
+        table = torch.full((T, 2), -1, dtype=torch.int32)
+        table[:, 0], table[:, 1] = side, torch.arange(T) % 70 + 5
+        batch = R.KVBatch(i32(list(range(T + 1))), i32([64 + s % 64 + 1 for s in range(T)]), table.cuda(), T, 1)
+        pre = R.KVPrefix(i32([0, T]), i32([64]), T, 64)
+        lo = R.DeviceLora((torch.randn(9, 16, K, generator=g) * K ** -0.5).half().cuda(),
+                          torch.randn(9, rows, 16, generator=g).half().cuda())
+        x, z = torch.randn(T, K, generator=g).cuda(), torch.randn(T, V, generator=g).cuda()
+        q = torch.randn((T, 8, 128), generator=g).bfloat16().cuda()
+        d = dict(cache=b, batch=batch, pre=pre, lo=lo, x=x, z=z, q=q, ids=i32([(s * 5 + side) % 11 - 1 for s in range(T)]),
+                 o=torch.empty(T, 8, 128, device="cuda"), y=torch.empty(T, rows, device="cuda"), h=torch.empty(T, K, device="cuda"),
+                 p=R.LogprobBuffers(T, V, 20), tokens=i32([s * 77 for s in range(T)]))
+        d["wa"] = torch.empty(R.attn_shared_workspace_bytes(b, batch, pre, 8), dtype=torch.uint8, device="cuda")
+        d["wl"] = torch.empty(R.lora_workspace_bytes([lo], T), dtype=torch.uint8, device="cuda")
+        sides.append(d)
+
+    def run(d):
+        R.add_rms_norm(d["x"], None, 1e-6, y=d["h"])
+        R.lora(d["h"], d["ids"], [d["lo"]], [d["y"]], [None], d["wl"])
+        R.attn_shared(d["q"], d["cache"], d["batch"], d["pre"], d["o"], 0.09, d["wa"])
+        d["p"].run(d["z"], d["tokens"])
+
+    def results(d):
+        return [t.clone() for t in (d["h"], d["y"], d["o"], d["p"].logprob, d["p"].entropy, d["p"].top_index, d["p"].rank)]
+
+    want = []
+    for d in sides:
+        run(d)
+        torch.cuda.synchronize()
+        want.append(results(d))
+    streams = [torch.cuda.Stream() for _ in sides]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for d, s in zip(sides, streams):
+            with torch.cuda.stream(s):
+                run(d)
+    torch.cuda.synchronize()
+    for d, w in zip(sides, want):
+        assert all(torch.equal(a, b) for a, b in zip(results(d), w))
