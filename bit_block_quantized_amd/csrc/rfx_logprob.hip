@@ -10,9 +10,9 @@
 // bits.
 //
 // Measured (both launches): one row of 32000 fp32 logits and five alternatives
-// 9 us, latency; 64 rows of 131072, half of them -inf, and 20 alternatives 18,
-// of which the join is 6 and reading takes 5; 1021 rows of 100003 bf16 logits
-// 55 (204 MB, 3.7 TB/s; 30 at the rate of a large read). There the vector pipe
+// 7 us, latency; 64 rows of 131072, half of them -inf, and 20 alternatives 17,
+// of which the join is 5 and reading takes 5; 1021 rows of 100003 bf16 logits
+// 51 (204 MB, 4.0 TB/s; 30 at the rate of a large read). There the vector pipe
 // is busy all the time: an element is some ten operations, an exponential
 // among them, and there is nothing that the matrix pipe could take.
 //
@@ -53,6 +53,7 @@ constexpr int kShort = 8;               // elements per thread of a short chunk
 constexpr int kWaveTop = 8;            // up to so many alternatives a chunk is one wave's
 constexpr int kLoads = 6;               // 16-byte loads per thread of a long one
 constexpr int kJoinKeys = 32;           // keys per thread of the join
+constexpr int kFewKeys = 8;             // of a join by one wave
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What a wave's part of a chunk leaves: its maximum m; sum e^(z - m), as the number of elements
@@ -448,13 +449,15 @@ __global__ __launch_bounds__(64 * WAVES) void logprob_chunk_kernel(LogpArgs a)
     top_keys<E, WAVES>(sh, a.k, top > -INFINITY ? ordered(top) : 0u, anew, reach, key, a.keys + ((size_t)row * a.S + c) * a.k);
 }
 
-// One workgroup per row.
-__global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
+// One workgroup per row, KEYS keys a thread.
+template <int WAVES, int KEYS>
+__global__ __launch_bounds__(64 * WAVES) void logprob_join_kernel(LogpArgs a)
 {
-    __shared__ Shared<kWaves> sh;
+    constexpr int THREADS = 64 * WAVES;
+    __shared__ Shared<WAVES> sh;
     __shared__ uint64_t best_keys[kMaxTop];
-    __shared__ double part[kWaves][4];
-    __shared__ float tops[kWaves];
+    __shared__ double part[WAVES][4];
+    __shared__ float tops[WAVES];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const size_t row = blockIdx.x;
     const rfx_logprob &o = a.out;
@@ -467,14 +470,14 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     // bound from threads of which some have none lets most keys pass).
     const Stat none = {-INFINITY, 0.f, 0.f, 0.f, 0.f}, own = tid < parts ? st[tid] : none;
     const uint64_t *keys = a.keys + row * a.S * a.k;
-    uint64_t mine[kJoinKeys];
+    uint64_t mine[KEYS];
     {
-        const int n = a.S * a.k, first = lane * kWaves + wave, step_pos = kThreads / a.S, step_list = kThreads - step_pos * a.S;
+        const int n = a.S * a.k, first = lane * WAVES + wave, step_pos = THREADS / a.S, step_list = THREADS - step_pos * a.S;
         int pos = first / a.S, list = first - pos * a.S;
 #pragma unroll
-        for (int j = 0; j < kJoinKeys; j++) {
+        for (int j = 0; j < KEYS; j++) {
             mine[j] = 0;
-            if (j * kThreads < n) { // uniform
+            if (j * THREADS < n) { // uniform
                 mine[j] = pos < a.k ? keys[list * a.k + pos] : 0;
                 pos += step_pos;
                 list += step_list;
@@ -494,13 +497,17 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     }
 
     float m = own.m;
-    for (int i = tid + kThreads; i < parts; i += kThreads)
+    for (int i = tid + THREADS; i < parts; i += THREADS)
         m = fmaxf(m, st[i].m);
     m = wave_max(m);
     if (lane == 0)
         tops[wave] = m;
     __syncthreads();
-    m = uniform(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+    m = tops[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; w++)
+        m = fmaxf(m, tops[w]);
+    m = uniform(m);
     double ones = 0.0, rest = 0.0, dot = 0.0, above = 0.0;
     const auto add = [&](const Stat &p) {
         above += p.above;
@@ -513,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
         dot += f * ((double)p.dot + (p.m == m ? 0.0 : (double)d * mass));
     };
     add(own);
-    for (int i = tid + kThreads; i < parts; i += kThreads)
+    for (int i = tid + THREADS; i < parts; i += THREADS)
         add(st[i]);
     ones = wave_sum(ones);
     rest = wave_sum(rest);
@@ -528,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
     __syncthreads();
     ones = rest = dot = above = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) {
+    for (int w = 0; w < WAVES; w++) {
         ones += part[w][0];
         rest += part[w][1];
         dot += part[w][2];
@@ -552,10 +559,10 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogpArgs a)
         return;
     uint64_t best = 0;
 #pragma unroll
-    for (int j = 0; j < kJoinKeys; j++)
+    for (int j = 0; j < KEYS; j++)
         best = mine[j] > best ? mine[j] : best;
     const auto reach = [&](uint32_t t) { return [&mine, t](int j) { return (uint32_t)(mine[j] >> 32) >= t; }; };
-    top_keys<kJoinKeys, kWaves>(sh, a.k, (uint32_t)(best >> 32), [](int) {}, reach, [&](int j) { return mine[j]; }, best_keys);
+    top_keys<KEYS, WAVES>(sh, a.k, (uint32_t)(best >> 32), [](int) {}, reach, [&](int j) { return mine[j]; }, best_keys);
     __syncthreads();
     if (tid < a.k) {
         const uint64_t key = best_keys[tid];
@@ -621,6 +628,11 @@ void launch(const LogpArgs &a, int type, int E, hipStream_t st)
     }
 #undef RFX_LOGP
 }
+
+// Whether one wave joins a row: no barriers, and more rows on a compute unit
+// (one row of 32000 and five alternatives 7.0 us, with four waves 8.8; one of
+// 128000 in 250 chunks 6.4 and 5.3).
+bool few_keys(const LogpArgs &a) { return a.k <= 32 && a.S * a.k <= 64 * kFewKeys && a.S * a.waves <= 128; }
 
 } // namespace
 
@@ -693,7 +705,10 @@ int rfx_token_logprobs(const void *logits, int64_t stride, const int32_t *tokens
         launch<kWaves>(a, O->type, p.E, hs);
     if ((st = hip_status("token_logprobs chunk launch")))
         return st;
-    hipLaunchKernelGGL(logprob_join_kernel, dim3(a.q), dim3(kThreads), 0, hs, a);
+    if (few_keys(a))
+        hipLaunchKernelGGL((logprob_join_kernel<1, kFewKeys>), dim3(a.q), dim3(64), 0, hs, a);
+    else
+        hipLaunchKernelGGL((logprob_join_kernel<kWaves, kJoinKeys>), dim3(a.q), dim3(kThreads), 0, hs, a);
     return hip_status("token_logprobs join launch");
 }
 
