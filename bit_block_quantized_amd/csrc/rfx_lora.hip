@@ -21,9 +21,9 @@
 // Measured: one token, rank 16, query, key and value (4096 x 4096 + 2 x 1024)
 // 8.6 us, the time of two launches that wait for memory twice (one launch in
 // which every workgroup makes v itself took 10.0); 64 tokens of 48 adapters of
-// rank 64, 4096 x 4096, 17.2 (the 37 MB of those that occur take 6); 4001 tokens
-// of seven prompts, rank 32, 81: 32 for the first launch (66 MB of x, ten at its
-// start and end) and 50 for the second (197 MB, 3.9 TB/s; a large copy has 4.8).
+// rank 64, 4096 x 4096, 16.8 (the 37 MB of those that occur take 6); 4001 tokens
+// of seven prompts, rank 32, 79: 32 for the first launch (66 MB of x, ten at its
+// start and end) and 48 for the second (197 MB, 4.1 TB/s; a large copy has 4.8).
 #include <algorithm>
 
 #include "rfx_kv.h"
@@ -382,6 +382,20 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
                 }
         }
     };
+    // The residual's rows, ahead of everything that they are added to.
+    const bool vec = a.vec >> m & 1;
+    const float *resid = M.resid + (size_t)t * M.rows;
+    f32x4 next_y[RT];
+    const auto load_resid = [&](int from) {
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
+            const int n = from + 16 * i + 4 * g4;
+            next_y[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+            if (vec && M.resid && t < l.n_tokens && n < M.rows)
+                next_y[i] = *reinterpret_cast<const f32x4 *>(resid + n);
+        }
+    };
+    load_resid(n0);
     float out = 1.0f;
     u4 vt[KS][X::N];
     if (any) {
@@ -443,8 +457,6 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
         for (int k = 0; k < KS; k++)
             X::split(v[k], vt[k]);
     }
-    const bool vec = a.vec >> m & 1;
-    const float *resid = M.resid + (size_t)t * M.rows;
     for (; n0 < n_end; n0 += STRIDE) {
         // lane: token r16, rows 4 g4 .. + 3 of tile i
         f32x4 acc[RT][X::SUMS], y[RT];
@@ -453,11 +465,10 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
 #pragma unroll
             for (int s = 0; s < X::SUMS; s++)
                 acc[i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
-            const int n = n0 + 16 * i + 4 * g4;
-            y[i] = acc[i][0];
-            if (vec && M.resid && t < l.n_tokens && n < M.rows)
-                y[i] = *reinterpret_cast<const f32x4 *>(resid + n);
+            y[i] = next_y[i];
         }
+        if (n0 + STRIDE < n_end)
+            load_resid(n0 + STRIDE);
         for (bool more = any; more;) {
             u4 now[ADS][RT][KS];
             bool on[ADS];
@@ -600,8 +611,8 @@ void launch_up_rank(LoraArgs &a, bool many, hipStream_t st)
         blocks = 0;
         for (int m = 0; m < a.l.n_mats; m++)
             blocks += a.row_blocks[m] = (int)ceil_div(a.l.mats[m].rows, (many ? 32 : 16) * kWaves * a.turns);
-        // Two turns where the chip is full without (4001 tokens 81 us, with one
-        // 82, four 85; 300 tokens 18 and 17).
+        // Two turns where the chip is full without (4001 tokens 80.9 us, with
+        // one 82.4, four 85.3; 300 tokens 18.4 and 17.1).
         if (!many || a.turns == 2 || (int64_t)blocks * (a.T16 / 16) < 2048)
             break;
     }
