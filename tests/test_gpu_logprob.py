@@ -218,7 +218,7 @@ def test_captured_and_deterministic():
 def test_borders_of_long_chunks(kind):
     """Rows that end beside the end of a chunk, so many that chunks are long
     ones, with few alternatives and with more."""
-    n = 1536 if kind == "f32" else 3072 # of one wave, of four: four times that
+    n = 1536 * (1 if kind == "f32" else 2) # of one wave, of four: four times that
     for q, V, k in ((1100, n - 3, 5), (1100, n + 1, 1), (300, 4 * n - 3, 20), (300, 4 * n + 1, 64)):
         check(*logits(q, V, V + k, kind), k)
     for q, V, k in ((1100, n + 1, 8), (300, 4 * n + 1, 20)):
