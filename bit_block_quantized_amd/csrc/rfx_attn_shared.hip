@@ -14,7 +14,7 @@
 // Bound by latency where prefixes are short, by the own keys' bytes and the
 // matrix pipe where there is much: 32 heads of 128, four sequences behind 500
 // keys (8 kv heads) 10 us; two groups of twelve with four new tokens each behind
-// 3001 keys (4) 24; 64 sequences of up to 700 keys behind 16384 (8) 54
+// 3001 keys (4) 23; 64 sequences of up to 700 keys behind 16384 (8) 54
 // (45 and the join's 9; the bytes take 23 and one after the other the prefix
 // takes 33, 17 GFLOP, and the own keys 27).
 #include <algorithm>
@@ -266,13 +266,17 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, 
     p.group.one_tiles = p.tall ? 4 : 8;
     p.group.cap_shift = 5;
     p.group.units = (int64_t)P->n_groups * C->n_kv_heads * p.group.row_blocks;
-    p.group.S = splits(p.group.units, ceil_div(P->max_len < room ? P->max_len : room, p.group.bn), p.group, p.tall ? 512 : 256);
+    const int64_t tiles = ceil_div(P->max_len < room ? P->max_len : room, p.group.bn);
+    p.group.S = splits(p.group.units, tiles, p.group, p.tall ? 384 : 256);
     // Partials of more splits cost the join more than they save, unless the
     // chip is not full without them (16384 keys, 256 rows of 8 kv heads: 16
-    // splits 54 us, 32 72; 16000 keys, 320 rows of 2: 16 splits 88, 32 55).
+    // splits 54 us, 32 72; 16000 keys, 320 rows of 2: 16 splits 88, 32 55), and
+    // past eight a split wants four tiles (256 rows, 2000 keys: 8 splits 29 us,
+    // 16 35). Beside the own keys' workgroups 384 are enough (48 sequences of
+    // up to four tokens behind 16000: 59, with 512 62, with 256 66).
     const int64_t full = 256 / (p.group.units < 256 ? p.group.units : 256);
-    const int cap = p.tall ? (int)(full > 16 ? full : 16) : 32;
-    p.group.S = p.group.S < cap ? p.group.S : cap;
+    const int64_t cap = p.tall ? std::min(std::max<int64_t>(full, 16), std::max<int64_t>(8, ceil_div(tiles, 4))) : 32;
+    p.group.S = (int)std::min<int64_t>(p.group.S, cap);
     sizes(p.group, dp);
     sizes(p.own, dp);
     p.units = align256((size_t)p.own.units * sizeof(SharedArgs::Unit));
