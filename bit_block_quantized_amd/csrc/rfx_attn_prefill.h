@@ -22,8 +22,8 @@
 //
 // Rounding: weights are rounded once to the cache's type for a result of
 // that type (its own rounding is as large), and the row sums are of the
-// rounded ones; for an fp32 result they are carried as the sum of TERMS
-// values, and the sums are of the fp32 weights.
+// rounded ones; for an fp32 result, and for a shared prefix, they are carried as
+// the sum of TERMS values, and the sums are of the fp32 weights.
 #pragma once
 
 #include <type_traits>

@@ -35,8 +35,11 @@ constexpr int kMaxSplits = 64; // one lane of the join each
 // pipe, the other by latency and memory, and a compute unit has both at a time
 // (64 sequences of up to 700 keys behind 16384: 54 us with the join, 72 with the
 // two one after the other).
-template <class T, int DP, int TERMS, int NR, decode::Pages PG>
-__global__ __launch_bounds__(256, prefill::waves_per_simd(DP, TERMS) > 2 ? 2 : prefill::waves_per_simd(DP, TERMS))
+// Weights of the prefix are carried as all of their terms, whatever the result's
+// type, as those of a sequence's own keys and of small groups are: what a
+// request gets does not depend on how many are in its group.
+template <class T, int DP, int NR, decode::Pages PG>
+__global__ __launch_bounds__(256, prefill::waves_per_simd(DP, T::TERMS) > 2 ? 2 : prefill::waves_per_simd(DP, T::TERMS))
 void shared_both_kernel(SharedArgs args)
 {
     constexpr int A = 2 * prefill::Tile<DP>::buf, B = decode::lds_bytes<DP>();
@@ -46,33 +49,24 @@ void shared_both_kernel(SharedArgs args)
     __shared__ __align__(16) char small[kSmall];
     const int block = blockIdx.x;
     if (block < args.group_blocks) {
-        prefill::attention<T, DP, TERMS>(args, block, smem, reinterpret_cast<unsigned (*)[2]>(small), reinterpret_cast<int *>(small + kBad));
+        prefill::attention<T, DP, T::TERMS>(args, block, smem, reinterpret_cast<unsigned (*)[2]>(small), reinterpret_cast<int *>(small + kBad));
     } else {
         float(*m)[NR * 16] = reinterpret_cast<float(*)[NR * 16]>(small);
         decode::attention<T, DP, NR, PG>(args, block, smem, m, m + decode::kWaves);
     }
 }
 
-template <class T, int DP, int TERMS, int NR>
+template <class T, int DP, int NR>
 void both_pages(const SharedArgs &a, hipStream_t st)
 {
     const KvArgs &kv = a.own.kv;
     const dim3 grid(a.group_blocks + (unsigned)kv.n_seq * kv.Hk * a.own.S), block(256);
     if (kv.D != DP || kv.page_shift < 4)
-        hipLaunchKernelGGL((shared_both_kernel<T, DP, TERMS, NR, decode::kAny>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((shared_both_kernel<T, DP, NR, decode::kAny>), grid, block, 0, st, a);
     else if (kv.page_shift == 4)
-        hipLaunchKernelGGL((shared_both_kernel<T, DP, TERMS, NR, decode::kTwo>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((shared_both_kernel<T, DP, NR, decode::kTwo>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((shared_both_kernel<T, DP, TERMS, NR, decode::kOne>), grid, block, 0, st, a);
-}
-
-template <class T, int DP, int NR>
-void both_terms(const SharedArgs &a, hipStream_t st)
-{
-    if (a.own.out_f32)
-        both_pages<T, DP, T::TERMS, NR>(a, st);
-    else
-        both_pages<T, DP, 1, NR>(a, st);
+        hipLaunchKernelGGL((shared_both_kernel<T, DP, NR, decode::kOne>), grid, block, 0, st, a);
 }
 
 template <class T>
@@ -81,11 +75,11 @@ int both(const SharedArgs &a, hipStream_t st)
     const int D = a.own.kv.D;
     const bool one = a.own.rows == 16;
     if (D > 128)
-        both_terms<T, 256, 1>(a, st);
+        both_pages<T, 256, 1>(a, st);
     else if (D > 64)
-        one ? both_terms<T, 128, 1>(a, st) : both_terms<T, 128, 2>(a, st);
+        one ? both_pages<T, 128, 1>(a, st) : both_pages<T, 128, 2>(a, st);
     else
-        one ? both_terms<T, 64, 1>(a, st) : both_terms<T, 64, 2>(a, st);
+        one ? both_pages<T, 64, 1>(a, st) : both_pages<T, 64, 2>(a, st);
     return hip_status("attn shared launch");
 }
 

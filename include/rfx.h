@@ -558,12 +558,12 @@ typedef struct rfx_kv_prefix {
 
 /* rfx_attn (without a window) for a batch in which sequences share prefixes: a
  * prefix's keys and values are read once for all new tokens of its group, what
- * a sequence has behind it once for the sequence. Arguments as rfx_attn's. For
- * a 16-bit result the softmax weights of a prefix enter the matrix core as one
- * term where max_tokens makes more than 96 rows (new tokens x query heads per
- * kv head). Sequences of more than 32 rows, 16 with heads over 128, go to
- * rfx_attn, which reads a key once per 128 rows of one sequence. A prefix is
- * read from the pages of its group's first sequence.
+ * a sequence has behind it once for the sequence. Arguments as rfx_attn's. The
+ * softmax weights enter the matrix core as two (fp16) or three (bf16) terms for
+ * a result of either type. Sequences of more than 32 rows (new tokens x query
+ * heads per kv head), 16 with heads over 128, go to rfx_attn, which reads a key
+ * once per 128 rows of one sequence, with its weights. A prefix is read from the
+ * pages of its group's first sequence.
  * ws: workspace of rfx_attn_shared_workspace_bytes, as rfx_attn's. Two
  * launches.
  * Errors: RFX_E_INVAL, RFX_E_ALIGN, RFX_E_WORKSPACE, RFX_E_HIP. */

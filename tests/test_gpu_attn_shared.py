@@ -4,6 +4,8 @@ groups that the arrays do not let share. To see that a prefix is read from the
 first sequence's pages, the others' hold NaN in its places and their tables ids
 out of range (which a caller's do not)."""
 
+import math
+
 import pytest
 import torch
 
@@ -238,3 +240,30 @@ def test_captured_with_growing_sequences(n):
         again = torch.empty_like(o)
         R.attn_shared(qd, cache, batch, pre, again, 0.09, ws)
         assert torch.equal(again, o)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n", [4, 40])
+def test_weights_of_a_16_bit_result_are_whole(n, dim, kind):
+    """Half of a prefix's keys have the weight 1 and the value 1, half have
+    0.501953125 (or 0.500244140625), between two 16-bit values, and the value
+    -2: nothing averages out what a weight is off by. Rounded to one value each
+    the weights are off by 2^-8 (2^-11) of that, 2.6e-3 (3.3e-4) of a result
+    whose bound here is below 1e-4. Four sequences' rows and forty's, which
+    take another kernel, are held to the same bound."""
+    need_gpu()
+    say(f"whole weights {n} sequences, heads of {dim}, {kind}")
+    b = SharedBatch([(200, [(1, 203)] * n)], 16, 2, dim, kind, seed=n)
+    w = 0.5 * (1 + (2.0 ** -8 if kind == "bf16" else 2.0 ** -11))
+    for t in (b.k, b.v):
+        t.copy_(torch.where(torch.isnan(t), t, torch.zeros_like(t)))
+    b.k[..., 0] = torch.where(torch.isnan(b.k[..., 0]), b.k[..., 0], torch.full_like(b.k[..., 0], -1.0))
+    for j in range(200):
+        page, slot = int(b.table[0, j // 16]), j % 16
+        b.k[page, :, slot, 0] = 0.0 if j % 2 else -1.0
+        b.v[page, :, slot] = 1.0 if j % 2 else -2.0
+    q = torch.zeros((n, 8, dim), dtype=TYPES[kind])
+    q[..., 0] = 1
+    scale = -math.log(w)
+    compare(b, q, run(b, q, scale, "same"), scale, "same", False)
