@@ -13,10 +13,10 @@
 // Two launches, the parts and the join (rfx_kv.h: AttnArgs, SharedArgs).
 // Bound by latency where prefixes are short, by the own keys' bytes and the
 // matrix pipe where there is much: 32 heads of 128, four sequences behind 500
-// keys (8 kv heads) 10 us; two groups of twelve with four new tokens each behind
-// 3001 keys (4) 23; 64 sequences of up to 700 keys behind 16384 (8) 54
-// (45 and the join's 9; the bytes take 23 and one after the other the prefix
-// takes 33, 17 GFLOP, and the own keys 27).
+// keys (8 kv heads) 10 us; two groups of twelve with up to four new tokens each
+// behind 3001 and 1606 keys (4) 23; 64 sequences of up to 700 keys behind 16384
+// (8) 69 (60 and the join's 9; the bytes take 23, the prefix with hardly an own
+// key 58 with its join, the own keys with hardly a prefix 27).
 #include <algorithm>
 #include <cmath>
 
@@ -33,8 +33,8 @@ constexpr int kMaxSplits = 64; // one lane of the join each
 // The prefix of many rows on the prefill kernel's tiles and the sequences' own
 // keys on the decode kernel's, in one launch: the one is bound by the matrix
 // pipe, the other by latency and memory, and a compute unit has both at a time
-// (64 sequences of up to 700 keys behind 16384: 54 us with the join, 72 with the
-// two one after the other).
+// (64 sequences of up to 700 keys behind 16384, weights of one term: 54 us with
+// the join, 72 with the two one after the other).
 // Weights of the prefix are carried as all of their terms, whatever the result's
 // type, as those of a sequence's own keys and of small groups are: what a
 // request gets does not depend on how many are in its group.
@@ -229,10 +229,11 @@ int splits(int64_t units, int64_t tiles, const Part &p, int places = 512)
 // Sequences of more rows than the decode kernel takes are left to rfx_attn,
 // whose prefill tiles already have 128 rows of one sequence per key. The
 // prefix of a group of few rows is the decode kernel's, which reads it once
-// per 32 (16) rows, mostly from L2: 80 rows of 8000 keys 28 us, on the prefill
-// kernel's tiles 32; 30000 keys 52 and 53. With more rows it is the other way
-// round: 384 rows of 3001 keys 24 against 27, 256 of 500 24 against 32.
-constexpr int64_t kTallRows = 96;
+// per 32 (16) rows, mostly from L2: 128 rows of 3001 keys of 8 kv heads 22.3 us,
+// on the prefill kernel's tiles 24.6, of 8000 27.6 and 30.2. With more rows it is
+// the other way round: 256 rows of 500 keys 27.3 and 21.8, of 8000 41.5 and 40.0,
+// 384 of 8000 65 and 51.
+constexpr int64_t kTallRows = 128;
 
 Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, int n_heads)
 {
@@ -263,11 +264,11 @@ Plan plan(const rfx_kv_cache *C, const rfx_kv_batch *B, const rfx_kv_prefix *P, 
     const int64_t tiles = ceil_div(P->max_len < room ? P->max_len : room, p.group.bn);
     p.group.S = splits(p.group.units, tiles, p.group, p.tall ? 384 : 256);
     // Partials of more splits cost the join more than they save, unless the
-    // chip is not full without them (16384 keys, 256 rows of 8 kv heads: 16
-    // splits 54 us, 32 72; 16000 keys, 320 rows of 2: 16 splits 88, 32 55), and
-    // past eight a split wants four tiles (256 rows, 2000 keys: 8 splits 29 us,
-    // 16 35). Beside the own keys' workgroups 384 are enough (48 sequences of
-    // up to four tokens behind 16000: 59, with 512 62, with 256 66).
+    // chip is not full without them (64 sequences behind 16384 keys, 256 rows of
+    // 8 kv heads: 16 splits 69 us, 32 76; 80 behind 16000, 320 rows of 2: 37, with
+    // 16 splits 52), and past eight a split wants four tiles (256 rows, 2000 keys:
+    // 39.6 us, else 44.4). Beside the own keys' workgroups 384 are enough (48
+    // sequences of up to four tokens behind 16000: 85, with 512 90, with 256 96).
     const int64_t full = 256 / (p.group.units < 256 ? p.group.units : 256);
     const int64_t cap = p.tall ? std::min(std::max<int64_t>(full, 16), std::max<int64_t>(8, ceil_div(tiles, 4))) : 32;
     p.group.S = (int)std::min<int64_t>(p.group.S, cap);
