@@ -413,8 +413,10 @@ __global__ __launch_bounds__(64 * WAVES) void logprob_chunk_kernel(LogpArgs a)
     const float fix = __builtin_amdgcn_exp2f(-lack), s = uniform(wave_sum(rests[0] + rests[1]));
     float rest = s * fix, dot = (wave_sum(dots[0] + dots[1]) - lack * s) * fix;
     int n = 0, above = 0;
-    // little beside the largest, or c m past fp32's range: the others alone
-    if (rest < 1.25f || fabsf(base) > 2e38f) {
+    // Little beside the largest: the others alone. So too where c m lacks more
+    // than 1 (from |m| of about 1e7 on, and where c m is past fp32's range): 2^lack
+    // and 2^-lack would leave that range, and their product what it stands for.
+    if (rest < 1.25f || !(fabsf(lack) <= 1.f)) {
         rests[0] = rests[1] = dots[0] = dots[1] = 0.f;
         pass();
 #pragma unroll

@@ -224,3 +224,29 @@ def test_borders_of_long_chunks(kind):
     for q, V, k in ((1100, n + 1, 8), (300, 4 * n + 1, 20)):
         z = torch.stack(list(_orders(V).values())).repeat(q // 9 + 1, 1)[:q].to(TYPES[kind])
         check(z, torch.arange(q) % V, k)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [0, 5, 20])
+@pytest.mark.parametrize("q", [9, 600])
+def test_finite_values_of_any_size(q, k, kind):
+    """Tokens excluded by a large finite number, or rows that are nothing
+    else: whole waves and chunks of them beside ordinary logits, in short
+    chunks and long ones."""
+    V = 5000
+    g = torch.Generator().manual_seed(q + k)
+    i = torch.arange(V)
+    per = 256 if kind == "f32" else 512 # what a wave takes at a time
+    masks = [i < 2048 if kind == "f32" else i < 4096, i >= 3000, i % (4 * per) < per, i % (4 * per) >= per, i >= 0, i != 77]
+    rows = []
+    for value in (1e4, 1e7, 1e9, 3e9, 1e10, 3e10, 1e13, 1e20, 1e30, 1e38, 2e38, 3.3e38):
+        for sign in (-1.0, 1.0):
+            for j, m in enumerate(masks):
+                z = torch.randn(V, generator=g) * 3
+                # the same number everywhere, or near it (some steps of fp32 below)
+                rows.append(torch.where(m, sign * value * (1 if j % 2 else 1 - (i % 5) * 2.0 ** -22), z))
+    z = torch.stack(rows).to(TYPES[kind])
+    t = torch.randint(0, V, (len(z),), generator=g)
+    for at in range(0, len(z), q):
+        part = torch.arange(at, at + q) % len(z)
+        check(z[part], t[part], k)
