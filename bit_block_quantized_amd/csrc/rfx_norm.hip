@@ -12,8 +12,7 @@
 // per thread, until its sum of squares is known. The sum, the root and the products are fp64 (the vector
 // pipe's fp64 rate is its fp32 rate, and there are some 60 operations to
 // spare per element): y is then the fp32 number next to the exact value but
-// for one in 2^28, the codes do not depend on the order of the sum, and
-// the result is that of a norm followed by rfx_quantize_act.
+// for one in 2^28, and the codes do not depend on the order of the sum.
 // Eight neighbouring lanes hold a block of 32, so its maximum and its sum of
 // codes are lane exchanges of the vector pipe.
 #include <hip/hip_runtime.h>
@@ -51,17 +50,20 @@ struct RowOut {
 };
 
 // Four elements of one block in each of its eight lanes to codes, scale and
-// sum. The scale is a product (one division less per block; it is within a
-// step of rfx_quantize_act's quotient), the codes' division is IEEE's. i4: the
+// sum. The scale is by definition a product, within a step of the quotient that
+// rfx_quantize_act takes (about one scale in twenty is that step off); the codes'
+// division is IEEE's. Magnitudes are compared as whole numbers, which order as
+// they do and have NaN above all, so that a NaN is its block's scale. i4: the
 // four's index in its row.
 __device__ __forceinline__ void quantize4(const f32x4 y, int i4, const RowOut &o)
 {
 #pragma clang fp contract(off)
-    float a = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
-    a = __int_as_float(block8(__float_as_int(a), [](int p, int q) {
-        return __float_as_int(fmaxf(__int_as_float(p), __int_as_float(q)));
-    }));
-    const float s = a * (1.0f / 127.0f);
+    int a = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        a = max(a, __float_as_int(fabsf(y[k])));
+    a = block8(a, [](int p, int q) { return max(p, q); });
+    const float s = __int_as_float(a) * (1.0f / 127.0f);
     uint32_t packed = 0u;
     int sum = 0;
 #pragma unroll
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(rfx_norm a)
     for (int i = 0; i < WAVES; i++)
         ss += part[i];
     const double ms = ss / a.cols + (double)a.eps;
-    const double r = ms > 0.0 ? 1.0 / sqrt(ms) : 0.0; // a row of zeros stays one
+    const double r = ms == 0.0 ? 0.0 : 1.0 / sqrt(ms); // a row of zeros stays one, a NaN spreads
 
     const size_t at = row * (size_t)a.cols;
     const RowOut o = {a.sum ? a.sum + at : nullptr, a.y ? a.y + at : nullptr, reinterpret_cast<uint32_t *>(a.xq ? a.xq + at : nullptr),

@@ -584,6 +584,8 @@ int rfx_attn_shared(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch
  * 127), s = 0 -> codes 0, and the codes' sum. The mean, the root and the
  * products are fp64 and y is rounded to fp32 once, so results do not depend
  * on the order of a sum. A row whose mean square and eps are zero gives y = 0.
+ * A NaN in a row makes its y and s NaN, an infinity the y there NaN and the
+ * others 0; a block with a NaN or an infinity in y has that as s, and any codes.
  * Any output may be NULL, but not all; xs and xsum are wanted with xq. sum
  * [q][cols] takes h; it may be x or delta where their rows are contiguous,
  * and so may y if it is not sum too. q may be 0; cols a multiple of 32, at

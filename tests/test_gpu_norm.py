@@ -149,3 +149,65 @@ def test_captured_and_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         check(o, *exact(x.cpu(), d.cpu(), None, EPS))
+
+
+# both workgroup sizes, and rows that are read twice
+@pytest.mark.parametrize("q,cols", [(7, 96), (7, 4128), (7, 32800), (520, 96), (520, 4128), (513, 8224)])
+def test_what_is_not_finite(q, cols):
+    """A row with a NaN is NaN in y and in every scale; one with an infinity
+    is NaN there, in its block's scale, and zero elsewhere; an infinite or NaN
+    weight stays in its column and block. Other rows are as they were."""
+    need_gpu()
+    say(f"norm {q} x {cols}, not finite")
+    x, d = rows(q, cols, 1), rows(q, cols, 2)
+    plain = outputs(q, cols)
+    R.add_rms_norm(x.cuda(), None, EPS, d.cuda(), **plain)
+    inf, nan = float("inf"), float("nan")
+    places = {0: (cols - 1, nan, 1.0), 1: (5, 1.0, nan), 2: (40, inf, 1.0), 3: (cols - 20, -inf, 2.0), 4: (33, inf, -inf)}
+    for r, (c, a, b) in places.items():
+        x[r, c], d[r, c] = a, b
+    o = outputs(q, cols)
+    R.add_rms_norm(x.cuda(), None, EPS, d.cuda(), **o)
+    h = (x + d).cuda()
+    assert torch.equal(torch.isnan(o["out"]), torch.isnan(h)) and torch.equal(o["out"].nan_to_num(), h.nan_to_num())
+    for r in (0, 1, 4): # inf - inf is NaN
+        assert torch.isnan(o["y"][r]).all() and torch.isnan(o["xs"][r]).all()
+    for r in (2, 3):
+        c = places[r][0]
+        there = torch.arange(cols, device="cuda") == c
+        assert torch.equal(torch.isnan(o["y"][r]), there) and not o["y"][r][~there].any()
+        block = torch.arange(cols // 32, device="cuda") == c // 32
+        assert torch.equal(torch.isnan(o["xs"][r]), block) and not o["xs"][r][~block].any()
+        assert not o["xq"][r].view(-1, 32)[~block].any() and not o["xsum"][r][~block].any()
+    for k in o:
+        assert torch.equal(o[k][5:], plain[k][5:]), k
+    # codes alone say the same
+    only = {k: v for k, v in outputs(q, cols).items() if k in ("xq", "xs", "xsum")}
+    R.add_rms_norm(x.cuda(), None, EPS, d.cuda(), **only)
+    for k in only:
+        assert torch.equal(only[k].nan_to_num(), o[k].nan_to_num()) and torch.equal(torch.isnan(only[k]), torch.isnan(o[k])), k
+    w = torch.ones(cols)
+    w[7], w[70] = inf, nan
+    o = outputs(q, cols)
+    R.add_rms_norm(plain["out"], w.cuda(), EPS, **o)
+    assert torch.isinf(o["y"][:, 7]).all() and torch.isnan(o["y"][:, 70]).all()
+    assert torch.isinf(o["xs"][:, 0]).all() and torch.isnan(o["xs"][:, 2]).all()
+    rest = [i for i in range(cols // 32) if i not in (0, 2)]
+    assert torch.equal(o["xs"][:, rest], plain["xs"][:, rest]) and torch.equal(o["xsum"][:, rest], plain["xsum"][:, rest])
+
+
+@pytest.mark.parametrize("fmt", ["FP2", "FP3", "FP4"])
+@pytest.mark.parametrize("q", [1, 3, 7, 40])
+def test_a_broken_row_shows_in_the_logits(q, fmt):
+    need_gpu()
+    g = torch.Generator().manual_seed(q)
+    V, H = 320, 256
+    head = R.DeviceHead.build(V, H, torch.randn(V, H, generator=g).numpy(), getattr(R, fmt), torch.ones(H).numpy())
+    buf = R.HeadBuffers(head, q, 3)
+    x = torch.randn(q, H, generator=g)
+    want = buf.run(head, x.cuda()).lse.clone()
+    assert torch.isfinite(want).all()
+    for bad in (float("nan"), float("inf")):
+        x[q - 1, 200] = bad
+        p = buf.run(head, x.cuda())
+        assert torch.equal(p.lse[:-1], want[:-1]) and torch.isnan(p.lse[-1]) and torch.isnan(p.entropy[-1])
