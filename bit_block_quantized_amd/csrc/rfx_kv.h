@@ -278,7 +278,8 @@ __device__ __forceinline__ int find_run(const int32_t *off, int n, int t)
 // What a group of sequences has in common, as the batch's kernels see it: its
 // new tokens are rows t0 .. t0 + nt - 1, its prefix the first len tokens of
 // sequence s0's pages. len = 0: no prefix (more new tokens than max_tokens,
-// rows or sequences that leave the arrays, a prefix that leaves the table).
+// rows or sequences that leave the arrays, a prefix that leaves the table or
+// that s0 does not have).
 struct Group {
     int s0, t0, nt, len;
 };
@@ -289,7 +290,8 @@ __device__ __forceinline__ Group make_group(const KvArgs &a, const PrefixArgs &p
     if (s0 < 0 || s1 <= s0 || s1 > a.n_seq || len <= 0 || len > a.stride << a.page_shift)
         return {0, 0, 0, 0};
     const int t0 = __builtin_amdgcn_readfirstlane(a.q_off[s0]), t1 = __builtin_amdgcn_readfirstlane(a.q_off[s1]);
-    if (t0 < 0 || t1 <= t0 || t1 > a.n_tokens || t1 - t0 > pre.max_tokens)
+    const int held = __builtin_amdgcn_readfirstlane(a.kv_len[s0]);
+    if (t0 < 0 || t1 <= t0 || t1 > a.n_tokens || t1 - t0 > pre.max_tokens || held < len || held > a.stride << a.page_shift)
         return {0, 0, 0, 0};
     return {s0, t0, t1 - t0, len};
 }

@@ -543,10 +543,12 @@ int rfx_attn(const void *q, const rfx_kv_cache *cache, const rfx_kv_batch *batch
  * prefix in the same pages or in copies of them; a group says that one's may be
  * read for all. A group may have no sequence, and a sequence no group. Where
  * len is not positive, the prefix leaves the table, a group's sequences or rows
- * leave the batch's or it has more than max_tokens new tokens, its sequences
- * are attended one by one, and so is a sequence whose new tokens begin inside
- * the prefix. max_len sets how a prefix is split and no more. The arrays are on
- * the device and may change between replays. */
+ * leave the batch's, its first sequence (which needs no new token) has fewer
+ * than len cached tokens or more than the table holds, or it has more than
+ * max_tokens new tokens, its sequences are attended one by one, and so is a
+ * sequence whose new tokens begin inside the prefix. max_len sets how a prefix
+ * is split and no more. The arrays are on the device and may change between
+ * replays. */
 typedef struct rfx_kv_prefix {
     int32_t n_groups;         /* 1..2^23 */
     int32_t max_tokens;       /* most new tokens of a group's sequences in all, 1..2^23 */

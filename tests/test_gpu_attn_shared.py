@@ -267,3 +267,28 @@ def test_weights_of_a_16_bit_result_are_whole(n, dim, kind):
     q[..., 0] = 1
     scale = -math.log(w)
     compare(b, q, run(b, q, scale, "same"), scale, "same", False)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("first", [(1, 40), (0, 40), (0, 0), (1, 99), (4, 99), (0, 5000)])
+def test_a_first_sequence_without_the_prefix(first, n):
+    """Its pages cannot be read for the group: whoever is in it is attended
+    alone. The table behind its tokens names pages that others hold."""
+    need_gpu()
+    say(f"first sequence {first} of {n}")
+    b = Batch([(first[0], min(first[1], 40 if first[1] > 100 else first[1]))] + [(1, 130 + i) for i in range(n)], 16, 2, 64, "bf16",
+              seed=n)
+    held = -(-int(b.kv_len[0]) // 16)
+    b.table[0, held:] = b.table[1, :b.table.shape[1] - held].clamp(0, b.n_pages - 1)
+    cache, batch = b.device(R)
+    batch.kv_len[0] = first[1] # 5000 tokens leave the table
+    q = torch.randn((b.n_tokens, 8, 64), generator=torch.Generator().manual_seed(n)).bfloat16()
+    i = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    pre = R.KVPrefix(i([0, n + 1]), i([100]), b.n_tokens, 100)
+    o = torch.full(q.shape, 7.0, device="cuda")
+    ws = torch.full((R.attn_shared_workspace_bytes(cache, batch, pre, 8),), 255, dtype=torch.uint8, device="cuda")
+    R.attn_shared(q.cuda(), cache, batch, pre, o, 0.125, ws)
+    compare(b, q, o.cpu(), 0.125, "f32", False)
+    # a prefix that it has, to the last token or without a new one, is read from it
+    for seqs in ([(1, 100)] + [(1, 101 + i) for i in range(n)], [(0, 99)] + [(1, 100 + i) for i in range(n)]):
+        check([(99, seqs)], 8, 2, 64, 16, "bf16", copies=True)
