@@ -292,3 +292,13 @@ def test_a_first_sequence_without_the_prefix(first, n):
     # a prefix that it has, to the last token or without a new one, is read from it
     for seqs in ([(1, 100)] + [(1, 101 + i) for i in range(n)], [(0, 99)] + [(1, 100 + i) for i in range(n)]):
         check([(99, seqs)], 8, 2, 64, 16, "bf16", copies=True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("groups", [64, 65, 90, 300])
+def test_many_groups(groups, kind):
+    """More than a wave has lanes; some have no sequence, some no prefix."""
+    seqs = lambda g: [(1 + (g + i) % 2, 60 + (7 * g + i) % 30) for i in range(g % 4)]  # noqa: E731
+    many = [(-1 if g % 11 == 5 else 16 + g % 40, seqs(g)) for g in range(groups)]
+    check([(None, [(1, 30)])] + many + [(None, [(2, 45), (1, 7)])], 8, 2, 64, 16, kind, seed=groups)
+    check(many, 4, 1, 128, 32, kind, out="same", seed=groups + 1, share=dict(max_tokens=100))
