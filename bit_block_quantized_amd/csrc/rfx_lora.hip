@@ -11,7 +11,11 @@
 // v_mfma_16x16x32 products whose rows are one adapter's, for each adapter
 // among the 16 tokens in turn; the columns of other adapters' tokens are zero,
 // so one accumulator collects all. Tokens may have any order of adapters;
-// runs of one adapter (a prompt) cost one pass.
+// runs of one adapter (a prompt) cost one pass. An adapter that is not finite
+// makes the others' columns NaN (zero times infinity): where sums of several
+// adapters hold a NaN, they are made again one adapter at a time, of which only
+// its tokens take the result. Sums apart from the start cost 300 tokens of as
+// many requests 66 us instead of 49.
 //
 // Adapters are 16-bit, x and v fp32: these enter as 16-bit terms, bf16 as
 // three that sum to the fp32 value, fp16 as two (the second 2^11 larger, with
@@ -110,6 +114,7 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
     constexpr int XP = 128 + 16, WP = 64 + 16;            // pitches of 32 columns of x and of A
     constexpr int PIECE = NB > 1 ? 16 * NB * XP + 16 * TILES * WP : 0, LDS = PIECE > SUMS * 1024 ? PIECE : SUMS * 1024;
     __shared__ __align__(16) char smem[kWaves * LDS];
+    __shared__ int bad[kWaves];
     auto &sums = *reinterpret_cast<f32x4 (*)[kWaves][SUMS][64]>(smem);
     const rfx_lora &l = a.l;
     const int lane = threadIdx.x & 63, r16 = lane & 15, g4 = lane >> 4;
@@ -131,200 +136,232 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
     f32x4 acc[NB][TILES][X::SUMS];
     int id[NB];
     bool mine[NB]; // this workgroup has the lane's token
-    uint32_t todo = 0;
+    uint32_t all = 0;
 #pragma unroll
     for (int n = 0; n < NB; n++) {
         id[n] = adapter_of(l, t0 + 16 * n + r16);
-        mine[n] = false;
-        todo |= ((uint32_t)__ballot(id[n] >= 0) & 0xffffu) << 16 * n;
-#pragma unroll
-        for (int i = 0; i < TILES; i++)
-#pragma unroll
-            for (int s = 0; s < X::SUMS; s++)
-                acc[n][i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        all |= ((uint32_t)__ballot(id[n] >= 0) & 0xffffu) << 16 * n;
     }
 
-    bool any = false;
-    for (int turn = 0; todo; turn++) {
-        const int first = __builtin_ctz(todo);
-        int ad = __builtin_amdgcn_readlane(id[0], first & 15);
-        if (NB > 1 && first >= 16)
-            ad = __builtin_amdgcn_readlane(id[NB - 1], first & 15);
-        const bool own = turn % a.slots == slot;
-        any |= own;
-        uint32_t keep[NB];
-        const float *x[NB];
+    // All of this workgroup's adapters at once (only = 0), or, where that holds a
+    // NaN, one after the other. The same in every wave.
+    for (int only = 0;;) {
+        int from_tile = tile0; // addresses are made anew: kept, they take the sums' registers
+        asm volatile("" : "+s"(from_tile));
 #pragma unroll
         for (int n = 0; n < NB; n++) {
-            const bool match = id[n] == ad;
-            todo &= ~(((uint32_t)__ballot(match) & 0xffffu) << 16 * n);
-            mine[n] |= match & own;
-            keep[n] = match ? ~0u : 0u;
-            // (few tokens) lanes of other adapters' tokens read along with the first one's
-            x[n] = l.x + (int64_t)(t0 + (match ? 16 * n + r16 : first)) * l.x_stride + 8 * g4;
+            mine[n] = false;
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+#pragma unroll
+                for (int s = 0; s < X::SUMS; s++)
+                    acc[n][i][s] = (f32x4){0.f, 0.f, 0.f, 0.f};
         }
-        if (!own || k0 >= k1)
-            continue;
-        if constexpr (NB == 1) {
-            const uint16_t *w[TILES];
+        int taken = 0;
+        uint32_t todo = all;
+        for (int turn = 0; todo; turn++) {
+            const int first = __builtin_ctz(todo);
+            int ad = __builtin_amdgcn_readlane(id[0], first & 15);
+            if (NB > 1 && first >= 16)
+                ad = __builtin_amdgcn_readlane(id[NB - 1], first & 15);
+            bool own = turn % a.slots == slot;
+            taken += own;
+            own &= !only || taken == only;
+            uint32_t keep[NB];
+            const float *x[NB];
 #pragma unroll
-            for (int i = 0; i < TILES; i++) {
-                const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + r16, l.rank - 1);
-                w[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * g4;
+            for (int n = 0; n < NB; n++) {
+                const bool match = id[n] == ad;
+                todo &= ~(((uint32_t)__ballot(match) & 0xffffu) << 16 * n);
+                mine[n] |= match & own;
+                keep[n] = match ? ~0u : 0u;
+                // (few tokens) lanes of other adapters' tokens read along with the first one's
+                x[n] = l.x + (int64_t)(t0 + (match ? 16 * n + r16 : first)) * l.x_stride + 8 * g4;
             }
-            struct Step {
-                f32x4 x[2][NB][2];
-                u4 w[TILES][2];
-            } s0, s1;
-            const auto load = [&](Step &s, int k) { // columns past the last: the step's first half again
-                const size_t at = 64 * (size_t)min(k, k1 - 1), up = at + 32 < (size_t)l.cols ? 32 : 0;
+            if (!own || k0 >= k1)
+                continue;
+            if constexpr (NB == 1) {
+                const uint16_t *w[TILES];
 #pragma unroll
-                for (int h = 0; h < 2; h++)
-#pragma unroll
-                    for (int n = 0; n < NB; n++)
-#pragma unroll
-                        for (int q = 0; q < 2; q++)
-                            s.x[h][n][q] = *reinterpret_cast<const f32x4 *>(x[n] + at + h * up + 4 * q);
-#pragma unroll
-                for (int i = 0; i < TILES; i++)
+                for (int i = 0; i < TILES; i++) {
+                    const int row = 16 * min(from_tile + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + r16, l.rank - 1);
+                    w[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * g4;
+                }
+                struct Step {
+                    f32x4 x[2][NB][2];
+                    u4 w[TILES][2];
+                } s0, s1;
+                const auto load = [&](Step &s, int k) { // columns past the last: the step's first half again
+                    const size_t at = 64 * (size_t)min(k, k1 - 1), up = at + 32 < (size_t)l.cols ? 32 : 0;
 #pragma unroll
                     for (int h = 0; h < 2; h++)
-                        s.w[i][h] = *reinterpret_cast<const u4 *>(w[i] + at + h * up);
-                __builtin_amdgcn_sched_barrier(0);
-            };
-            const auto compute = [&](const Step &s, int k) {
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const uint32_t in = 64 * k + 32 * h < l.cols ? ~0u : 0u;
+                        for (int n = 0; n < NB; n++)
+#pragma unroll
+                            for (int q = 0; q < 2; q++)
+                                s.x[h][n][q] = *reinterpret_cast<const f32x4 *>(x[n] + at + h * up + 4 * q);
+#pragma unroll
+                    for (int i = 0; i < TILES; i++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++)
+                            s.w[i][h] = *reinterpret_cast<const u4 *>(w[i] + at + h * up);
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                const auto compute = [&](const Step &s, int k) {
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t in = 64 * k + 32 * h < l.cols ? ~0u : 0u;
+#pragma unroll
+                        for (int n = 0; n < NB; n++) {
+                            float xc[8];
+                            u4 t[X::N];
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                xc[e] = s.x[h][n][e >> 2][e & 3] * X::IN;
+                            X::split(xc, t);
+#pragma unroll
+                            for (int q = 0; q < X::N; q++)
+                                t[q] &= keep[n] & in;
+#pragma unroll
+                            for (int q = 0; q < X::N; q++) // neighbours do not depend on one another
+#pragma unroll
+                                for (int j = 0; j < TILES; j++)
+                                    X::mma(q, s.w[j][h], t, acc[n][j]);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                load(s0, k0);
+                for (int k = k0; k < k1; k += 2) {
+                    load(s1, k + 1);
+                    compute(s0, k);
+                    if (k + 1 == k1)
+                        break;
+                    load(s0, k + 2);
+                    compute(s1, k + 1);
+                }
+            } else {
+                // 32 columns at a time through the wave's own piece of LDS: a load
+                // whose 16 lanes of a quarter read 16 rows takes the cycles of
+                // sixteen, one that reads whole lines of two (x) or four (A) rows
+                // those of as many.
+                const int first_k = 2 * k0, last_k = min(2 * k1, l.cols / 32);
+                const float *px[2 * NB];
+#pragma unroll
+                for (int j = 0; j < 2 * NB; j++)
+                    px[j] = l.x + (int64_t)min(t0 + 8 * j + (lane >> 3), l.n_tokens - 1) * l.x_stride + 4 * (lane & 7);
+                const uint16_t *pw[TILES];
+#pragma unroll
+                for (int i = 0; i < TILES; i++) {
+                    const int row = 16 * min(from_tile + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + (lane >> 2), l.rank - 1);
+                    pw[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * (lane & 3);
+                }
+                constexpr int AHEAD = 2; // steps in flight
+                f32x4 xn[AHEAD][2 * NB];
+                u4 wn[AHEAD][TILES];
+                const auto load = [&](int u, int k) {
+                    const int at = 32 * min(k, last_k - 1);
+#pragma unroll
+                    for (int j = 0; j < 2 * NB; j++)
+                        xn[u][j] = *reinterpret_cast<const f32x4 *>(px[j] + at);
+#pragma unroll
+                    for (int i = 0; i < TILES; i++)
+                        wn[u][i] = *reinterpret_cast<const u4 *>(pw[i] + at);
+                };
+                const auto step = [&](int u, int k) {
+#pragma unroll
+                    for (int j = 0; j < 2 * NB; j++)
+                        *reinterpret_cast<f32x4 *>(piece + (8 * j + (lane >> 3)) * XP + 16 * (lane & 7)) = xn[u][j];
+#pragma unroll
+                    for (int i = 0; i < TILES; i++)
+                        *reinterpret_cast<u4 *>(piece + 16 * NB * XP + (16 * i + (lane >> 2)) * WP + 16 * (lane & 3)) = wn[u][i];
+                    load(u, k + AHEAD);
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                    u4 w[TILES];
+#pragma unroll
+                    for (int i = 0; i < TILES; i++)
+                        w[i] = *reinterpret_cast<const u4 *>(piece + 16 * NB * XP + (16 * i + r16) * WP + 16 * g4);
 #pragma unroll
                     for (int n = 0; n < NB; n++) {
+                        const char *p = piece + (16 * n + r16) * XP + 32 * g4;
+                        const f32x4 x0 = *reinterpret_cast<const f32x4 *>(p), x1 = *reinterpret_cast<const f32x4 *>(p + 16);
                         float xc[8];
                         u4 t[X::N];
 #pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            xc[e] = s.x[h][n][e >> 2][e & 3] * X::IN;
+                        for (int e = 0; e < 4; e++) {
+                            xc[e] = x0[e] * X::IN;
+                            xc[e + 4] = x1[e] * X::IN;
+                        }
                         X::split(xc, t);
 #pragma unroll
                         for (int q = 0; q < X::N; q++)
-                            t[q] &= keep[n] & in;
+                            t[q] &= keep[n];
 #pragma unroll
-                        for (int q = 0; q < X::N; q++) // neighbours do not depend on one another
+                        for (int q = 0; q < X::N; q++)
 #pragma unroll
-                            for (int j = 0; j < TILES; j++)
-                                X::mma(q, s.w[j][h], t, acc[n][j]);
+                            for (int i = 0; i < TILES; i++)
+                                X::mma(q, w[i], t, acc[n][i]);
                     }
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            };
-            load(s0, k0);
-            for (int k = k0; k < k1; k += 2) {
-                load(s1, k + 1);
-                compute(s0, k);
-                if (k + 1 == k1)
-                    break;
-                load(s0, k + 2);
-                compute(s1, k + 1);
-            }
-        } else {
-            // 32 columns at a time through the wave's own piece of LDS: a load
-            // whose 16 lanes of a quarter read 16 rows takes the cycles of
-            // sixteen, one that reads whole lines of two (x) or four (A) rows
-            // those of as many.
-            const int first_k = 2 * k0, last_k = min(2 * k1, l.cols / 32);
-            const float *px[2 * NB];
-#pragma unroll
-            for (int j = 0; j < 2 * NB; j++)
-                px[j] = l.x + (int64_t)min(t0 + 8 * j + (lane >> 3), l.n_tokens - 1) * l.x_stride + 4 * (lane & 7);
-            const uint16_t *pw[TILES];
-#pragma unroll
-            for (int i = 0; i < TILES; i++) {
-                const int row = 16 * min(tile0 + i, a.tiles - 1), m = row / a.R16, r = min(row - m * a.R16 + (lane >> 2), l.rank - 1);
-                pw[i] = static_cast<const uint16_t *>(l.mats[m].a) + ((size_t)ad * l.rank + r) * l.cols + 8 * (lane & 3);
-            }
-            constexpr int AHEAD = 2; // steps in flight
-            f32x4 xn[AHEAD][2 * NB];
-            u4 wn[AHEAD][TILES];
-            const auto load = [&](int u, int k) {
-                const int at = 32 * min(k, last_k - 1);
-#pragma unroll
-                for (int j = 0; j < 2 * NB; j++)
-                    xn[u][j] = *reinterpret_cast<const f32x4 *>(px[j] + at);
-#pragma unroll
-                for (int i = 0; i < TILES; i++)
-                    wn[u][i] = *reinterpret_cast<const u4 *>(pw[i] + at);
-            };
-            const auto step = [&](int u, int k) {
-#pragma unroll
-                for (int j = 0; j < 2 * NB; j++)
-                    *reinterpret_cast<f32x4 *>(piece + (8 * j + (lane >> 3)) * XP + 16 * (lane & 7)) = xn[u][j];
-#pragma unroll
-                for (int i = 0; i < TILES; i++)
-                    *reinterpret_cast<u4 *>(piece + 16 * NB * XP + (16 * i + (lane >> 2)) * WP + 16 * (lane & 3)) = wn[u][i];
-                load(u, k + AHEAD);
-                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                u4 w[TILES];
-#pragma unroll
-                for (int i = 0; i < TILES; i++)
-                    w[i] = *reinterpret_cast<const u4 *>(piece + 16 * NB * XP + (16 * i + r16) * WP + 16 * g4);
-#pragma unroll
-                for (int n = 0; n < NB; n++) {
-                    const char *p = piece + (16 * n + r16) * XP + 32 * g4;
-                    const f32x4 x0 = *reinterpret_cast<const f32x4 *>(p), x1 = *reinterpret_cast<const f32x4 *>(p + 16);
-                    float xc[8];
-                    u4 t[X::N];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        xc[e] = x0[e] * X::IN;
-                        xc[e + 4] = x1[e] * X::IN;
-                    }
-                    X::split(xc, t);
-#pragma unroll
-                    for (int q = 0; q < X::N; q++)
-                        t[q] &= keep[n];
-#pragma unroll
-                    for (int q = 0; q < X::N; q++)
-#pragma unroll
-                        for (int i = 0; i < TILES; i++)
-                            X::mma(q, w[i], t, acc[n][i]);
-                }
-                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-            };
-#pragma unroll
-            for (int u = 0; u < AHEAD; u++)
-                load(u, first_k + u);
-            for (int k = first_k; k < last_k; k += AHEAD)
+                    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                };
 #pragma unroll
                 for (int u = 0; u < AHEAD; u++)
-                    if (k + u < last_k)
-                        step(u, k + u);
-        }
-    }
-    if (NB > 1 && any)
-        __syncthreads(); // the pieces become the sums
-    if (!any) // the same in every wave
-        return;
-    // lane: token r16 of its sixteen, rows 4 g4 .. + 3 of tile i
-    const int RS = l.n_mats * a.R16;
+                    load(u, first_k + u);
+                for (int k = first_k; k < last_k; k += AHEAD)
 #pragma unroll
-    for (int j = 0; j < TILES * NB; j += SUMS) {
-        if (j)
+                    for (int u = 0; u < AHEAD; u++)
+                        if (k + u < last_k)
+                            step(u, k + u);
+            }
+        }
+        if (!taken)
+            return;
+        if (NB > 1 || only)
+            __syncthreads(); // the pieces, or the last ones, become the sums
+        if (!only && taken > 1) {
+            float any = 0.f;
+#pragma unroll
+            for (int n = 0; n < NB; n++)
+#pragma unroll
+                for (int i = 0; i < TILES; i++)
+#pragma unroll
+                    for (int s = 0; s < X::SUMS; s++)
+                        any += (acc[n][i][s][0] + acc[n][i][s][1]) + (acc[n][i][s][2] + acc[n][i][s][3]);
+            const bool nan = __ballot(any != any) != 0;
+            if (lane == 0)
+                bad[wave] = nan;
             __syncthreads();
-#pragma unroll
-        for (int i = j; i < j + SUMS; i++)
-            if (i < TILES * NB)
-                sums[wave][i - j][lane] = X::total(acc[i / TILES][i % TILES]) * (1.0f / X::IN);
-        __syncthreads();
-        const int i = j + wave, n = i / TILES, tile = tile0 + i % TILES; // SUMS is at most the waves' number
-        if (wave < SUMS && i < TILES * NB && tile < a.tiles) {
-            f32x4 s = sums[0][wave][lane];
-#pragma unroll
-            for (int w = 1; w < kWaves; w++)
-                s += sums[w][wave][lane];
-            if (NB > 1 && n ? mine[NB - 1] : mine[0])
-                *reinterpret_cast<f32x4 *>(a.v + ((size_t)split * a.T16 + t0 + 16 * n + r16) * RS + 16 * tile + 4 * g4) = s;
+            if (bad[0] | bad[1] | bad[2] | bad[3]) {
+                only = 1;
+                continue;
+            }
         }
+        // lane: token r16 of its sixteen, rows 4 g4 .. + 3 of tile i
+        const int RS = l.n_mats * a.R16;
+#pragma unroll
+        for (int j = 0; j < TILES * NB; j += SUMS) {
+            if (j)
+                __syncthreads();
+#pragma unroll
+            for (int i = j; i < j + SUMS; i++)
+                if (i < TILES * NB)
+                    sums[wave][i - j][lane] = X::total(acc[i / TILES][i % TILES]) * (1.0f / X::IN);
+            __syncthreads();
+            const int i = j + wave, n = i / TILES, tile = from_tile + i % TILES; // SUMS is at most the waves' number
+            if (wave < SUMS && i < TILES * NB && tile < a.tiles) {
+                f32x4 s = sums[0][wave][lane];
+#pragma unroll
+                for (int w = 1; w < kWaves; w++)
+                    s += sums[w][wave][lane];
+                if (NB > 1 && n ? mine[NB - 1] : mine[0])
+                    *reinterpret_cast<f32x4 *>(a.v + ((size_t)split * a.T16 + t0 + 16 * n + r16) * RS + 16 * tile + 4 * g4) = s;
+            }
+        }
+        if (!only || ++only > taken)
+            return;
+        __syncthreads(); // the sums are read
     }
 }
 
@@ -353,9 +390,17 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
     const int id = adapter_of(l, t);
     const uint32_t all = (uint32_t)__ballot(id >= 0) & 0xffffu;
     const bool any = all != 0; // the same in every wave
+    // more than one adapter
+    const bool several = any && (all & ~(uint32_t)__ballot(id == __builtin_amdgcn_readlane(id, any ? __builtin_ctz(all) : 0)));
     if (!any && M.resid == M.y)
         return;
 
+    // Step k's part of a row of an adapter's B; past the last, the last again.
+    const auto load_b = [&](const uint16_t *p, int n, int k) {
+        const int r = 32 * k + 8 * g4;
+        const u4 x = *reinterpret_cast<const u4 *>(p + (size_t)min(n, M.rows - 1) * l.rank + (r < l.rank ? r : 0));
+        return r < l.rank ? x : (u4){0, 0, 0, 0};
+    };
     // The next ADS adapters: their rows of B from next_n on, and who has them.
     bool live[ADS];
     uint32_t keep[ADS], todo = all;
@@ -375,11 +420,8 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
 #pragma unroll
             for (int i = 0; i < RT; i++)
 #pragma unroll
-                for (int k = 0; k < KS; k++) {
-                    const int n = min(next_n + 16 * i + r16, M.rows - 1), r = 32 * k + 8 * g4;
-                    const u4 x = *reinterpret_cast<const u4 *>(p + (size_t)n * l.rank + (r < l.rank ? r : 0));
-                    w[j][i][k] = r < l.rank ? x : (u4){0, 0, 0, 0};
-                }
+                for (int k = 0; k < KS; k++)
+                    w[j][i][k] = load_b(p, next_n + 16 * i + r16, k);
         }
     };
     // The residual's rows, ahead of everything that they are added to.
@@ -510,6 +552,44 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
             if (ADS > 1 && next_n < n_end)
                 fetch();
         }
+        f32x4 sum[RT];
+        float nan = 0.f;
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
+            const f32x4 total = X::total(acc[i]);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                sum[i][e] = id >= 0 ? total[e] : 0.f;
+                nan += sum[i][e];
+            }
+        }
+        if (several && __ballot(nan != nan)) { // apart
+#pragma unroll 1
+            for (uint32_t left = all; left;) {
+                const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+                const bool match = id == ad;
+                left &= ~(uint32_t)__ballot(match);
+                const uint16_t *p = static_cast<const uint16_t *>(M.b) + (size_t)ad * M.rows * l.rank;
+#pragma unroll
+                for (int i = 0; i < RT; i++) {
+                    f32x4 one[X::SUMS];
+#pragma unroll
+                    for (int s = 0; s < X::SUMS; s++)
+                        one[s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < KS; k++) {
+                        const u4 b = load_b(p, n0 + 16 * i + r16, k);
+#pragma unroll
+                        for (int s = 0; s < X::N; s++)
+                            X::mma(s, b, vt[k], one);
+                    }
+                    const f32x4 total = X::total(one);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        sum[i][e] = match ? total[e] : sum[i][e];
+                }
+            }
+        }
         if (t >= l.n_tokens)
             continue;
 #pragma unroll
@@ -518,7 +598,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
             if (left <= 0)
                 continue;
             const size_t at = (size_t)t * M.rows + n;
-            y[i] += X::total(acc[i]) * out;
+            y[i] += sum[i] * out;
             if (vec) {
                 *reinterpret_cast<f32x4 *>(M.y + at) = y[i];
             } else {

@@ -189,3 +189,33 @@ def test_many_tokens_and_rows(rows, kind):
     or has none."""
     Case(700, 64, 24, rows, 5, kind).check()
     Case(700, 64, 24, rows, 5, kind, ids=[0] * 40 + [-1] * 100 + [4] * 300 + [7] * 60 + [2] * 200, resid=False).check()
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("T,K,rank,rows", [(4, 96, 16, [50]), (20, 512, 8, [70, 33]), (64, 4096, 64, [512]), (130, 256, 40, [64, 64, 64]),
+                                           (200, 1024, 128, [100, 40]), (300, 2048, 32, [96, 50]), (700, 64, 24, [4100])])
+def test_an_adapter_keeps_its_infinities(T, K, rank, rows, kind):
+    """Infinities and NaN in one adapter's first factor, or in a row of
+    another's second, reach its own tokens alone; without an adapter y is the
+    residual."""
+    n = 7
+    g = torch.Generator().manual_seed(T)
+    for ids in (torch.arange(T) % (n + 1) - 1, torch.randint(-1, n, (T,), generator=g), torch.arange(T) * n // T):
+        c = Case(T, K, rank, rows, n, kind, ids=ids.tolist())
+        want = c.run()
+        for y, r in zip(want, c.resid):
+            assert torch.equal(y[ids < 0], r[ids < 0])
+        for bad in (float("inf"), float("-inf"), float("nan")):
+            a, b = [t.clone() for t in c.a], [t.clone() for t in c.b]
+            for m in range(len(rows)):
+                c.a[m][2, rank - 1, K - 5] = bad
+                c.b[m][4, rows[m] // 2, 3] = bad
+                c.b[m][5, :, 0] = bad
+            got = c.run()
+            c.a, c.b = a, b
+            for y, w, N in zip(got, want, rows):
+                own, one = (ids == 2) | (ids == 5), ids == 4
+                assert not torch.isfinite(y[own]).any()
+                assert not torch.isfinite(y[one][:, N // 2]).any()
+                y[one, N // 2] = w[one, N // 2]
+                assert torch.equal(y[~own], w[~own]), bad
