@@ -20,7 +20,9 @@
 // Adapters are 16-bit, x and v fp32: these enter as 16-bit terms, bf16 as
 // three that sum to the fp32 value, fp16 as two (the second 2^11 larger, with
 // sums of its own, so that it stays clear of fp16's subnormals), 2^-22 of the
-// value. Sums are fp32.
+// value. fp16 has few exponents: a token's x and v are brought into them by a
+// power of two of its own, so that elements down to 2^-21 of the largest have
+// that precision and smaller ones 2^-43 of the largest. Sums are fp32.
 //
 // Measured: one token, rank 16, query, key and value (4096 x 4096 + 2 x 1024)
 // 8.6 us, the time of two launches that wait for memory twice (one launch in
@@ -64,7 +66,6 @@ struct Terms;
 template <>
 struct Terms<BF16> {
     static constexpr int N = 3, SUMS = 1;
-    static constexpr float IN = 1.0f;
     static __device__ __forceinline__ void split(const float (&x)[8], u4 (&t)[3]) { split_terms<BF16, 3>(x, t); }
     // One term's product, the smallest first (s = 0).
     static __device__ __forceinline__ void mma(int s, u4 a, const u4 (&t)[3], f32x4 (&c)[1]) { c[0] = BF16::mma16(a, t[2 - s], c[0]); }
@@ -74,7 +75,6 @@ struct Terms<BF16> {
 template <>
 struct Terms<F16> {
     static constexpr int N = 2, SUMS = 2;
-    static constexpr float IN = 0x1p-4f; // x below 2^20 stays finite
     static __device__ __forceinline__ void split(const float (&x)[8], u4 (&t)[2])
     {
 #pragma unroll
@@ -88,6 +88,35 @@ struct Terms<F16> {
     static __device__ __forceinline__ void mma(int s, u4 a, const u4 (&t)[2], f32x4 (&c)[2]) { c[s] = F16::mma16(a, t[s], c[s]); }
     static __device__ __forceinline__ f32x4 total(const f32x4 (&c)[2]) { return c[0] + c[1] * 0x1p-11f; }
 };
+
+// The power of two that brings `top` into 128 .. 256 (tiny and huge ones as near
+// as a normal power does, infinity anywhere), and what undoes it.
+__device__ __forceinline__ float fitting(float top)
+{
+    const int ex = (int)(__float_as_uint(top) >> 23);
+    return __uint_as_float((uint32_t)max(1, min(253, 254 + 7 - ex)) << 23);
+}
+__device__ __forceinline__ float inverse(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
+
+// A token's factor of x, that of what its columns had so far, made smaller where
+// the next ones (at most `top` in this lane) would leave fp16, its sums with it.
+// That takes elements 2^7 times as large: rescaling is rare. The four lanes of a
+// token have the same factor.
+template <int TILES, int SUMS>
+__device__ __forceinline__ void refit(float top, float &factor, f32x4 (&acc)[TILES][SUMS])
+{
+    if (__any(top * factor > 0x1p15f)) {
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float next = top * factor > 0x1p15f ? fitting(top) : factor, f = next * inverse(factor);
+#pragma unroll
+        for (int i = 0; i < TILES; i++)
+#pragma unroll
+            for (int s = 0; s < SUMS; s++)
+                acc[i][s] *= f;
+        factor = next;
+    }
+}
 
 // The adapter of token t, -1 for none.
 __device__ __forceinline__ int adapter_of(const rfx_lora &l, int t)
@@ -134,6 +163,7 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
     const int k0 = (int)((int64_t)steps * p / part), k1 = (int)((int64_t)steps * (p + 1) / part);
 
     f32x4 acc[NB][TILES][X::SUMS];
+    [[maybe_unused]] float factor[NB]; // of the lane's tokens
     int id[NB];
     bool mine[NB]; // this workgroup has the lane's token
     uint32_t all = 0;
@@ -151,6 +181,7 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
 #pragma unroll
         for (int n = 0; n < NB; n++) {
             mine[n] = false;
+            factor[n] = 0x1p126f;
 #pragma unroll
             for (int i = 0; i < TILES; i++)
 #pragma unroll
@@ -208,6 +239,15 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
                     __builtin_amdgcn_sched_barrier(0);
                 };
                 const auto compute = [&](const Step &s, int k) {
+                    if constexpr (X::SUMS > 1)
+#pragma unroll
+                        for (int n = 0; n < NB; n++) {
+                            float top = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; e++)
+                                top = fmaxf(top, fabsf(s.x[e >> 3][n][(e >> 2) & 1][e & 3]));
+                            refit(keep[n] ? top : 0.f, factor[n], acc[n]);
+                        }
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         const uint32_t in = 64 * k + 32 * h < l.cols ? ~0u : 0u;
@@ -217,7 +257,7 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
                             u4 t[X::N];
 #pragma unroll
                             for (int e = 0; e < 8; e++)
-                                xc[e] = s.x[h][n][e >> 2][e & 3] * X::IN;
+                                xc[e] = X::SUMS > 1 ? s.x[h][n][e >> 2][e & 3] * factor[n] : s.x[h][n][e >> 2][e & 3];
                             X::split(xc, t);
 #pragma unroll
                             for (int q = 0; q < X::N; q++)
@@ -290,8 +330,18 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
                         u4 t[X::N];
 #pragma unroll
                         for (int e = 0; e < 4; e++) {
-                            xc[e] = x0[e] * X::IN;
-                            xc[e + 4] = x1[e] * X::IN;
+                            xc[e] = x0[e];
+                            xc[e + 4] = x1[e];
+                        }
+                        if constexpr (X::SUMS > 1) {
+                            float top = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                top = fmaxf(top, fabsf(xc[e]));
+                            refit(keep[n] ? top : 0.f, factor[n], acc[n]);
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                xc[e] *= factor[n];
                         }
                         X::split(xc, t);
 #pragma unroll
@@ -347,7 +397,8 @@ __global__ __launch_bounds__(kThreads, down_waves(TILES, NB, Terms<T>::SUMS)) vo
 #pragma unroll
             for (int i = j; i < j + SUMS; i++)
                 if (i < TILES * NB)
-                    sums[wave][i - j][lane] = X::total(acc[i / TILES][i % TILES]) * (1.0f / X::IN);
+                    sums[wave][i - j][lane] = X::SUMS > 1 ? X::total(acc[i / TILES][i % TILES]) * inverse(factor[i / TILES])
+                                                          : X::total(acc[i / TILES][i % TILES]);
             __syncthreads();
             const int i = j + wave, n = i / TILES, tile = from_tile + i % TILES; // SUMS is at most the waves' number
             if (wave < SUMS && i < TILES * NB && tile < a.tiles) {
@@ -477,7 +528,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
                 v[k][e + 4] = on ? s1[e] * c : 0.f;
             }
         }
-        if (X::SUMS > 1) { // a token's v below 2 in magnitude: a power of two off, and on again below
+        if (X::SUMS > 1) { // a power of two off, and on again below
             float top = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; k++)
@@ -486,9 +537,8 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraArgs a)
                     top = fmaxf(top, fabsf(v[k][e]));
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const int ex = top > 0.f && top < INFINITY ? max(-100, min(100, (int)(__float_as_uint(top) >> 23) - 127)) : 0;
-            const float in = __uint_as_float((uint32_t)(127 - ex) << 23);
-            out = __uint_as_float((uint32_t)(127 + ex) << 23);
+            const float in = fitting(top);
+            out = inverse(in);
 #pragma unroll
             for (int k = 0; k < KS; k++)
 #pragma unroll

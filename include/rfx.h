@@ -616,10 +616,10 @@ int rfx_add_rms_norm(const rfx_norm *args, void *stream);
  * to RFX_LORA_MAX_MATS matrices over the same x (query, key, value) share the
  * launches. Adapters of smaller rank are padded with zeros. Sums are fp32; x
  * and A x enter the matrix core as three bf16 terms (together the fp32 value)
- * or two fp16 terms (2^-22 of it; with fp16 adapters |x| < 2^19.9). One token's
- * infinities and NaN stay its own, and an adapter's reach its own tokens alone.
- * Results are deterministic, and a token's do not depend on the other tokens'
- * values.
+ * or two fp16 terms (2^-22 of it, or of the token's largest element 2^-43 where
+ * that is more). One token's infinities and NaN stay its own, and an adapter's
+ * reach its own tokens alone. Results are deterministic, and a token's do not
+ * depend on the other tokens' values.
  * ws: workspace of rfx_lora_workspace_bytes, 256-B aligned; it needs no
  * initialisation and holds anything afterwards. Calls that can run
  * concurrently must not share it. Two launches.

@@ -219,3 +219,77 @@ def test_an_adapter_keeps_its_infinities(T, K, rank, rows, kind):
                 assert not torch.isfinite(y[one][:, N // 2]).any()
                 y[one, N // 2] = w[one, N // 2]
                 assert torch.equal(y[~own], w[~own]), bad
+
+
+def _loose(c):
+    """exact() with what is documented of small elements beside fp16 adapters,
+    2^-43 of the token's largest, instead of an absolute bound."""
+    step, extra = 2.0 ** -24, 8 if c.kind == "f16" else 0
+    for a, b in zip(c.a, c.b):
+        T, N = len(c.x), b.shape[1]
+        y, tol = torch.zeros(T, N, dtype=torch.float64), torch.zeros(T, N, dtype=torch.float64)
+        for ad in range(len(a)):
+            on = (c.ids == ad).nonzero()[:, 0]
+            if not len(on):
+                continue
+            x, A, B = c.x[on].double(), a[ad].double(), b[ad].double()
+            s = 1.0 if c.scale is None else float(c.scale[ad])
+            v, mag = x @ A.t(), x.abs() @ A.abs().t()
+            dv = (3 * c.K + 24 + extra) * step * mag
+            if extra:
+                dv += 2.0 ** -43 * x.abs().amax(1, keepdim=True) * A.abs().sum(1)
+            d, dm = s * (v @ B.t()), abs(s) * (v.abs() @ B.abs().t())
+            y[on] = d
+            if extra: # the second factor's operand has the same two terms
+                tol[on] = 2.0 ** -43 * abs(s) * v.abs().amax(1, keepdim=True) * B.abs().sum(1)
+            tol[on] += abs(s) * (dv @ B.abs().t()) + (3 * c.rank + 8 + extra) * step * dm + 2 * step * d.abs()
+        yield y, tol
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("T,K", [(1, 4096), (18, 256), (150, 1056), (300, 640)])
+def test_inputs_of_any_size(T, K, kind):
+    """From 1e-30 to 1e30, whole tokens of a size or sizes that rise and fall
+    along a token; an adapter's result is as good relative to its input."""
+    for factor in (1e-30, 1e-20, 1e-12, 1e-7, 1e-5, 1.0, 1e8, 1e20, 1e30):
+        c = Case(T, K, 16, [64], 3, kind, ids=[i % 3 for i in range(T)], resid=False)
+        c.x = c.x / c.x.abs().amax(1, keepdim=True) * factor
+        for got, (y, tol) in zip(c.run(), _loose(c)):
+            assert ((got.double() - y).abs() <= tol).all(), (kind, factor)
+            # additions' errors have no common sign, and two fp16 terms are off by 2^-22
+            assert float((got.double() - y).norm() / y.norm()) <= 2.0 ** -22 * (3 * K + 64) ** 0.5, (kind, factor)
+    up = 10.0 ** torch.linspace(-30, 10, K)
+    for shape in (up, up.flip(0), torch.where(torch.arange(K) % 7 == 3, 1e6, 1e-6), torch.where(torch.arange(K) >= K - 3, 1e9, 0.0)):
+        c = Case(T, K, 16, [64], 3, kind, ids=[i % 3 for i in range(T)], resid=False)
+        c.x = c.x / c.x.abs().amax(1, keepdim=True) * shape
+        for got, (y, tol) in zip(c.run(), _loose(c)):
+            assert ((got.double() - y).abs() <= tol).all(), kind
+
+
+def test_a_token_does_not_see_its_neighbours_sizes():
+    """fp16 operands are scaled by a power of two of the token's own."""
+    for T in (20, 150, 300):
+        c = Case(T, 512, 16, [64], 4, "f16", ids=[i % 4 for i in range(T)])
+        want = c.run()[0]
+        for t in range(0, T, 3):
+            c.x[t] *= 1e12 if t % 2 else 1e-12
+        got = c.run()[0]
+        rest = [t for t in range(T) if t % 3]
+        assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("T", [1, 18, 300])
+def test_small_elements_beside_a_large_one(T, kind):
+    """The adapter does not look at the large one, and its result is the small
+    ones' down to 2^-43 of the large one."""
+    for large in (1.0, 1e15):
+        for small in (2.0 ** -10, 2.0 ** -20, 2.0 ** -26, 2.0 ** -32, 2.0 ** -38):
+            c = Case(T, 512, 16, [64], 3, kind, ids=[i % 3 for i in range(T)], resid=False)
+            c.x = c.x / c.x.abs().amax(1, keepdim=True) * small * large
+            for at in (0, 300, 511):
+                c.x[:, at] = large
+                for a in c.a:
+                    a[:, :, at] = 0
+            for got, (y, tol) in zip(c.run(), _loose(c)):
+                assert ((got.double() - y).abs() <= tol).all(), (kind, large, small)
