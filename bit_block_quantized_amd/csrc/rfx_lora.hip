@@ -25,10 +25,10 @@
 // that precision and smaller ones 2^-43 of the largest. Sums are fp32.
 //
 // Measured: one token, rank 16, query, key and value (4096 x 4096 + 2 x 1024)
-// 8.6 us, the time of two launches that wait for memory twice (one launch in
+// 8.5 us, the time of two launches that wait for memory twice (one launch in
 // which every workgroup makes v itself took 10.0); 64 tokens of 48 adapters of
-// rank 64, 4096 x 4096, 16.8 (the 37 MB of those that occur take 6); 4001 tokens
-// of seven prompts, rank 32, 79: 32 for the first launch (66 MB of x, ten at its
+// rank 64, 4096 x 4096, 17.3 (the 37 MB of those that occur take 6); 4001 tokens
+// of seven prompts, rank 32, 79.5: 32 for the first launch (66 MB of x, ten at its
 // start and end) and 48 for the second (197 MB, 4.1 TB/s; a large copy has 4.8).
 #include <algorithm>
 
